@@ -1,0 +1,588 @@
+"""The operators around the routed experts, as measured cases: the norms on
+either side of a block, tokens sorted by expert and back, MXFP4 quantisation
+of activation rows and the experts' MXFP4 products.
+
+Every case has a plain form in elementary torch operations (``own`` False),
+the calls into the library (``own`` True) and an exact form in 64 bits.
+
+Operators and their formulas (rows t of T tokens, slots s = t*k + j):
+
+norm     r = 1 / sqrt(mean_c h^2 + eps)          x    = h r w_pre
+         q = 1 / sqrt(mean_c y^2 + eps)          h'   = rho h + g (y q w_post)
+         r' of h' (before its rounding)          x'   = h' r' w_next
+         train: from dx and dh'  dy, dw_post, dg  and
+         dh = rho dh' + r (w dx - h r^2 mean_c(h w dx)),  dw_pre = sum_t dx h r
+moe      counts, offsets, perm, inv of the slots in order of (expert, slot),
+         xs[inv[s]] = x[t],  y[t] = base[t] + sum_j w[t, j] ys[inv[s]]
+         train: dys = w dy, dw = <dy, ys>, dl = w (dw - sum_j w dw) and
+         dx[t] = sum_j dxs[inv[s]]; an expert outside [0, E) takes no part
+quant    32 values share a scale 2^(floor(log2 max|x|) - 2); elements go to the
+         nearest E2M1 value, ties to the even code, beyond 6 to 6
+product  y[p] = A[p] W_e^T for the rows p of expert e, and silu(g) u of two
+         such products; back: dA[p] = dY[p] W_e
+"""
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-6
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+SIZE = {"f32": 4, "bf16": 2}
+MAGNITUDES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def listed():
+    moe = dict(op="moe", E=256, k=6, d=4096, x="bf16", ys="bf16", y="f32", dead=0.0, train=False)
+    norm = dict(op="norm", d=4096, rho=1.0, train=False)
+    return [
+        # one decoded token: the layer's fp32 output joins the fp32 stream, the next block's bf16 input leaves
+        dict(norm, name="norm_decode", T=1, h="f32", y="f32", x="bf16", gate="none"),
+        # a prefill chunk with a bf16 stream and one gate value a token
+        dict(norm, name="norm_prefill", T=2048, h="bf16", y="f32", x="bf16", gate="token"),
+        # training with a ragged batch, an odd number of 256s, a learned gate a channel and a scaled residual
+        dict(norm, name="norm_train", T=2047, d=1792, h="bf16", y="bf16", x="bf16", gate="channel", rho=0.5,
+             train=True),
+        # 16 batched sessions, one token each
+        dict(moe, name="moe_decode", T=16),
+        # a prefill chunk with Zipf-like expert loads
+        dict(moe, name="moe_prefill", T=2048),
+        # training in fp32 with padded tokens and slots dropped by a capacity
+        dict(moe, name="moe_train", T=1021, E=64, k=4, d=2048, x="f32", ys="f32", dead=0.1, train=True),
+        # the six rows of one decoded token
+        dict(name="quant_decode", op="quant", T=1, k=6, cols=4096, x="bf16"),
+        # a prefill chunk's rows, gathered in the experts' order
+        dict(name="quant_prefill", op="quant", T=2048, k=6, cols=4096, x="bf16"),
+        # gate and up of one decoded token's six experts
+        dict(name="product_decode", op="product", T=1, k=6, E=256, rows=2048, cols=4096, y="bf16", swiglu=True,
+             back=False),
+        # the down products of a prefill chunk with Zipf-like loads
+        dict(name="product_prefill", op="product", T=2048, k=6, E=256, rows=4096, cols=2048, y="f32", swiglu=False,
+             back=False),
+        # gate and up of an expert that every token takes, a ragged batch
+        dict(name="product_dense", op="product", T=4001, k=1, E=1, rows=4096, cols=4096, y="bf16", swiglu=True,
+             back=False),
+        # adapters trained through frozen experts: the gradient of a few experts' inputs
+        dict(name="product_grad", op="product", T=667, k=3, E=32, rows=2048, cols=4096, y="bf16", swiglu=False,
+             back=True),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "moe", "quant", "product"])
+    types = ["f32", "bf16"]
+    if op == "norm":
+        return dict(op=op, T=_log_int(rng, 1, 2048), d=256 * rng.randint(1, 16), h=rng.choice(types),
+                    y=rng.choice(types), x=rng.choice(types), gate=rng.choice(["none", "token", "channel", "full"]),
+                    rho=rng.choice([1.0, 0.5]), train=rng.random() < 0.5)
+    if op == "moe":
+        E = _log_int(rng, 2, 256)
+        return dict(op=op, T=_log_int(rng, 1, 2048), E=E, k=rng.randint(1, min(6, E)), d=256 * rng.randint(1, 16),
+                    x=rng.choice(types), ys=rng.choice(types), y=rng.choice(types), dead=rng.choice([0.0, 0.1, 0.5]),
+                    train=rng.random() < 0.5)
+    if op == "quant":
+        return dict(op=op, T=_log_int(rng, 1, 2048), k=rng.randint(1, 6), cols=256 * rng.randint(1, 16),
+                    x=rng.choice(types))
+    E = rng.choice([1, 1, 8, 32, 64, 200])
+    rows, cols = 16 * _log_int(rng, 4, 256), 256 * rng.randint(1, 16)
+    while E * rows * cols > 2 ** 30:
+        rows = max(16, rows // 32 * 16)
+    k = rng.randint(1, min(6, E))
+    back = rng.random() < 0.33
+    return dict(op=op, T=_log_int(rng, 1, 2048), k=k, E=E, rows=rows, cols=cols, y=rng.choice(types),
+                swiglu=not back and rng.random() < 0.5, back=back)
+
+
+# ------------------------------------------------------------------ inputs
+
+class _Rand:
+    """Seeded draws on the GPU."""
+
+    def __init__(self, seed):
+        self.g = torch.Generator(device="cuda")
+        self.g.manual_seed(seed)
+
+    def normal(self, *shape, scale=1.0, dtype="f32"):
+        return (torch.randn(*shape, generator=self.g, device="cuda") * scale).to(TYPES[dtype])
+
+    def uniform(self, *shape):
+        return torch.rand(*shape, generator=self.g, device="cuda")
+
+
+def _experts(r, T, k, E, dead=0.0):
+    """Distinct experts of every token, ascending, with Zipf-like loads; `dead`
+    of the slots and of the tokens have none (-1)."""
+    rank = torch.arange(1, E + 1, device="cuda", dtype=torch.float32)
+    order = torch.argsort(r.uniform(E))
+    score = -1.1 * torch.log(rank)[order] - torch.log(-torch.log(r.uniform(T, E).clamp(1e-9, 1 - 1e-7)))
+    idx = torch.topk(score, k, dim=1).indices.sort(dim=1).values.to(torch.int32)
+    if dead:
+        idx = torch.where((r.uniform(T, k) < dead) | (r.uniform(T, 1) < dead), torch.full_like(idx, -1), idx)
+    return idx.contiguous()
+
+
+def _sorted_slots(idx, E):
+    """counts, offsets, perm, inv of the slots sorted by (expert, slot)."""
+    flat = idx.reshape(-1).long()
+    S = flat.numel()
+    live = (flat >= 0) & (flat < E)
+    key = torch.where(live, flat, torch.full_like(flat, E))
+    order = torch.sort(key, stable=True).indices
+    counts = torch.bincount(key, minlength=E + 1)[:E]
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
+    place = torch.empty_like(order)
+    place[order] = torch.arange(S, device=order.device)
+    inv = torch.where(live, place, torch.full_like(place, -1))
+    perm = torch.where(torch.arange(S, device=order.device) < offsets[E], order, torch.full_like(order, -1))
+    return counts.int(), offsets.int(), perm.int(), inv.int()
+
+
+def _codes(x):
+    """E2M1 codes and E8M0 scale codes of fp32 blocks [..., 32]."""
+    amax = x.abs().amax(-1, keepdim=True)
+    exponent = torch.frexp(amax).exponent.int() - 1  # floor(log2 amax)
+    scale = torch.where(amax > 0, (exponent + 125).clamp(0, 254), torch.zeros_like(exponent))
+    # two exact steps, so that the factor itself stays a normal number
+    m = torch.ldexp(torch.ldexp(x.abs(), (127 - scale) // 2), (127 - scale) - (127 - scale) // 2)
+    code = ((m > 0.25).int() + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0)).int()
+    code = torch.where((x < 0) & (code > 0), code + 8, code)
+    return code, scale.squeeze(-1)
+
+
+def _pack(x):
+    """The library's MXFP4 bytes of one fp32 matrix [rows, cols]: the codes, two a byte, then the scales."""
+    rows, cols = x.shape
+    code, scale = _codes(x.reshape(rows, cols // 32, 32))
+    code = code.reshape(-1, 2)
+    return torch.cat([(code[:, 0] | (code[:, 1] << 4)).to(torch.uint8), scale.reshape(-1).to(torch.uint8)])
+
+
+def _packed_bytes(rows, cols):
+    return rows * cols * 17 // 32
+
+
+def _unpack(packed, rows, cols, dtype):
+    """The values [rows, cols] of one packed matrix."""
+    n = rows * cols // 2
+    b = packed[:n].long()
+    values = torch.tensor(MAGNITUDES + tuple(-v for v in MAGNITUDES), device=packed.device, dtype=dtype)
+    v = values[torch.stack([b & 15, b >> 4], dim=1)].reshape(rows, cols // 32, 32)
+    scale = torch.pow(torch.tensor(2.0, device=packed.device, dtype=torch.float64),
+                      packed[n:].double() - 127).to(dtype)
+    return (v * scale.reshape(rows, cols // 32, 1)).reshape(rows, cols)
+
+
+def prepare(case, seed):
+    r = _Rand(seed)
+    s = dict(case)
+    op = case["op"]
+    if op == "norm":
+        T, d = case["T"], case["d"]
+        s["w"] = {n: 1.0 + r.normal(d, scale=0.1) for n in ("pre", "post", "next")}
+        s["in_h"] = r.normal(T, d, scale=2.0, dtype=case["h"])
+        s["in_y"] = r.normal(T, d, scale=0.3, dtype=case["y"])
+        shape = {"none": None, "token": (T,), "channel": (d,), "full": (T, d)}[case["gate"]]
+        s["in_g"] = None if shape is None else r.normal(*shape, scale=0.3) + 0.5
+        if case["train"]:
+            s["in_dh"] = r.normal(T, d, dtype=case["h"])
+            s["in_dx"] = r.normal(T, d, dtype=case["x"])
+    elif op == "moe":
+        T, k, E, d = (case[n] for n in ("T", "k", "E", "d"))
+        s["idx"] = _experts(r, T, k, E, case["dead"])
+        s["in_x"] = r.normal(T, d, dtype=case["x"])
+        s["in_ys"] = r.normal(T * k, d, dtype=case["ys"])
+        s["base"] = r.normal(T, d, dtype=case["y"])
+        live = s["idx"] >= 0
+        logit = torch.where(live, r.normal(T, k), torch.full((T, k), -1e30, device="cuda"))
+        s["tw"] = torch.where(live, torch.softmax(logit, 1), torch.zeros_like(logit)).contiguous()
+        if case["train"]:
+            s["in_dy"] = r.normal(T, d, dtype=case["y"])
+            s["in_dxs"] = r.normal(T * k, d, dtype=case["x"])
+    elif op == "quant":
+        T, k = case["T"], case["k"]
+        # channels of unequal size, as activations have them
+        channel = torch.exp(r.normal(case["cols"]))
+        s["in_x"] = (r.normal(T, case["cols"]) * channel).to(TYPES[case["x"]])
+        s["perm"] = _sorted_slots(_experts(r, T, k, max(16, k)), max(16, k))[2]
+    else:
+        T, k, E, rows, cols = (case[n] for n in ("T", "k", "E", "rows", "cols"))
+        n = T * k
+        nb = _packed_bytes(rows, cols)
+        s["offsets"] = _sorted_slots(_experts(r, T, k, E), E)[1]
+        s["weights"] = []
+        for _ in range(2 if case["swiglu"] else 1):
+            w = torch.empty(E * nb, dtype=torch.uint8, device="cuda")
+            for e in range(E):
+                w[e * nb:(e + 1) * nb] = _pack(r.normal(rows, cols, scale=0.02))
+            s["weights"].append(w)
+        if case["back"]:
+            s["in_dy"] = r.normal(n, rows, dtype=case["y"])
+        else:
+            s["in_a"] = _pack(r.normal(n, cols))
+    if own:
+        _prepare_own(s)
+    return s
+
+
+# ------------------------------------------------------------------ plain
+
+def _norm(s, f, rounded):
+    """The norm operators in type f; rounded(v, kind) gives an output its type."""
+    h, y = s["in_h"].to(f), s["in_y"].to(f)
+    w = {n: v.to(f) for n, v in s["w"].items()}
+    g = s["in_g"]
+    g = torch.ones((), device=h.device, dtype=f) if g is None else g.to(f)
+    if s["gate"] == "token":
+        g = g[:, None]
+    rho = s["rho"]
+    q = 1 / torch.sqrt((y * y).mean(1, keepdim=True) + EPS)
+    out_h = rho * h + g * (y * q * w["post"])
+    if not s["train"]:
+        r = 1 / torch.sqrt((out_h * out_h).mean(1, keepdim=True) + EPS)
+        return dict(h=rounded(out_h, s["h"]), x=rounded(out_h * r * w["next"], s["x"]))
+    r = 1 / torch.sqrt((h * h).mean(1, keepdim=True) + EPS)
+    dh, dx = s["in_dh"].to(f), s["in_dx"].to(f)
+    u = dh * g * w["post"]
+    dy = q * (u - y * q * q * (y * u).mean(1, keepdim=True))
+    dw_post = (dh * g * (y * q)).sum(0)
+    dg = dh * (y * q * w["post"])
+    dg = {"none": None, "token": dg.sum(1), "channel": dg.sum(0), "full": dg}[s["gate"]]
+    v = dx * w["pre"]
+    dh_in = rho * dh + r * (v - h * r * r * (h * v).mean(1, keepdim=True))
+    out = dict(x=rounded(h * r * w["pre"], s["x"]), h=rounded(out_h, s["h"]), dy=rounded(dy, s["y"]),
+               dh=rounded(dh_in, s["h"]), dw_post=rounded(dw_post, "f32"),
+               dw_pre=rounded((dx * (h * r)).sum(0), "f32"))
+    if dg is not None:
+        out["dg"] = rounded(dg, "f32")
+    return out
+
+
+def _moe(s, f, rounded):
+    T, k, E, d = (s[n] for n in ("T", "k", "E", "d"))
+    counts, offsets, perm, inv = _sorted_slots(s["idx"], E)
+    live = inv >= 0
+    to = inv[live].long()
+    token = torch.arange(T * k, device=inv.device)[live] // k
+    xs = torch.zeros(T * k, d, device=inv.device, dtype=TYPES[s["x"]])
+    xs[to] = s["in_x"][token]
+    tw = torch.where(live.reshape(T, k), s["tw"], torch.zeros_like(s["tw"])).to(f)
+
+    def rows(a):  # each slot's row, zero for a slot without an expert
+        out = torch.zeros(T * k, d, device=a.device, dtype=f)
+        out[live] = a[to].to(f)
+        return out.reshape(T, k, d)
+
+    ys = rows(s["in_ys"])
+    y = s["base"].to(f) + (tw[:, :, None] * ys).sum(1)
+    out = dict(counts=counts, offsets=offsets, perm=perm, inv=inv.reshape(T, k), xs=xs, y=rounded(y, s["y"]))
+    if s["train"]:
+        dy = s["in_dy"].to(f)
+        dys = torch.zeros(T * k, d, device=inv.device, dtype=f)
+        dys[to] = (tw[:, :, None] * dy[:, None, :]).reshape(T * k, d)[live]
+        dw = (ys * dy[:, None, :]).sum(2)
+        dl = tw * (dw - (tw * dw).sum(1, keepdim=True))
+        out.update(dys=rounded(dys, s["ys"]), dw=rounded(dw, "f32"), dl=rounded(dl, "f32"),
+                   dx=rounded(rows(s["in_dxs"]).sum(1), s["x"]))
+    return out
+
+
+def _round(v, kind):
+    return v.to(TYPES[kind])
+
+
+def _quant_plain(s):
+    x = s["in_x"].float()[s["perm"].long() // s["k"]]
+    n, cols = x.shape
+    code, scale = _codes(x.reshape(n, cols // 32, 32))
+    values = torch.tensor(MAGNITUDES + tuple(-v for v in MAGNITUDES), device=x.device)
+    return (torch.ldexp(values[code.long()], (scale - 127)[..., None])).reshape(n, cols).to(torch.bfloat16)
+
+
+def _product(s, f, rounded):
+    rows, cols, n = s["rows"], s["cols"], s["T"] * s["k"]
+    nb = _packed_bytes(rows, cols)
+    off = s["offsets"].tolist()
+    a = s["in_dy"].to(f) if s["back"] else _unpack(s["in_a"], n, cols, f)
+    out = torch.zeros(n, cols if s["back"] else rows, device="cuda", dtype=f)
+    for e in range(s["E"]):
+        lo, hi = off[e], off[e + 1]
+        if lo == hi:
+            continue
+        w = [_unpack(m[e * nb:(e + 1) * nb], rows, cols, f) for m in s["weights"]]
+        if s["back"]:
+            out[lo:hi] = a[lo:hi] @ w[0]
+        elif s["swiglu"]:
+            g = a[lo:hi] @ w[0].t()
+            out[lo:hi] = g / (1 + torch.exp(-g)) * (a[lo:hi] @ w[1].t())
+        else:
+            out[lo:hi] = a[lo:hi] @ w[0].t()
+    return dict(y=rounded(out, s["y"]))
+
+
+def run(state):
+    if own:
+        return {"norm": _norm_own, "moe": _moe_own, "quant": _quant_own, "product": _product_own}[state["op"]](state)
+    if state["op"] == "quant":
+        return dict(values=_quant_plain(state))
+    return {"norm": _norm, "moe": _moe, "product": _product}[state["op"]](state, torch.float32, _round)
+
+
+# ------------------------------------------------------------------ library
+
+def _prepare_own(s):
+    """Descriptors, outputs and workspaces, as a program holds them between calls."""
+    from bit_quantized_routed_router_amd import ds4moe as D
+    dt = {"f32": D.DT_F32, "bf16": D.DT_BF16}
+    s["D"] = D
+    s["dt"] = {n: dt[s[n]] for n in ("h", "y", "x", "ys") if n in s}
+
+    def new(*shape, kind="f32"):
+        return torch.zeros(*shape, dtype=TYPES[kind], device="cuda")
+
+    if s["op"] == "norm":
+        T, d = s["T"], s["d"]
+        gate = {"none": D.GATE_NONE, "token": D.GATE_TOKEN, "channel": D.GATE_CHANNEL, "full": D.GATE_FULL}[s["gate"]]
+        s["norm"] = D.Norm(d, eps=EPS, res_scale=s["rho"], gate=gate, w_pre=s["w"]["pre"], w_post=s["w"]["post"],
+                           w_next=s["w"]["next"])
+        s["out"] = dict(h=new(T, d, kind=s["h"]), x=new(T, d, kind=s["x"]))
+        if s["train"]:
+            s["out"].update(dy=new(T, d, kind=s["y"]), dh=new(T, d, kind=s["h"]), dw_post=new(d), dw_pre=new(d))
+            if s["in_g"] is not None:
+                s["out"]["dg"] = new(*s["in_g"].shape)
+            s["ws"] = s["norm"].workspace(T)
+    elif s["op"] == "moe":
+        T, k, E, d = (s[n] for n in ("T", "k", "E", "d"))
+        ints = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731
+        s["out"] = dict(counts=ints(E), offsets=ints(E + 1), perm=ints(T * k), inv=ints(T, k),
+                        xs=new(T * k, d, kind=s["x"]), y=new(T, d, kind=s["y"]))
+        if s["train"]:
+            s["out"].update(dys=new(T * k, d, kind=s["ys"]), dw=new(T, k), dl=new(T, k), dx=new(T, d, kind=s["x"]))
+        n = D.group_workspace_bytes(T, k, E)
+        s["ws"] = (torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    elif s["op"] == "quant":
+        n = s["T"] * s["k"]
+        s["packed"] = torch.zeros(_packed_bytes(n, s["cols"]), dtype=torch.uint8, device="cuda")
+        s["out"] = dict(values=new(n, s["cols"], kind="bf16"))
+    else:
+        n = s["T"] * s["k"]
+        s["out"] = dict(y=new(n, s["cols"] if s["back"] else s["rows"], kind=s["y"]))
+
+
+def _norm_own(s):
+    D, N, T, dt, o = s["D"], s["norm"].desc, s["T"], s["dt"], s["out"]
+    if not s["train"]:
+        D.norm_post(N, s["in_h"], dt["h"], s["in_y"], dt["y"], s["in_g"], T, o["h"], o["x"], dt["x"])
+        return o
+    D.norm_pre(N, s["in_h"], dt["h"], T, o["x"], dt["x"])
+    D.norm_post(N, s["in_h"], dt["h"], s["in_y"], dt["y"], s["in_g"], T, o["h"], None, dt["x"])
+    ws, nb = s["ws"]
+    D.norm_post_grad(N, s["in_dh"], dt["h"], s["in_y"], dt["y"], s["in_g"], T, o["dy"], o["dw_post"], o.get("dg"), ws,
+                     nb)
+    D.norm_pre_grad(N, s["in_h"], dt["h"], s["in_dx"], dt["x"], s["in_dh"], T, o["dh"], o["dw_pre"], ws, nb)
+    return o
+
+
+def _moe_own(s):
+    D, dt, o = s["D"], s["dt"], s["out"]
+    T, k, E, d = s["T"], s["k"], s["E"], s["d"]
+    n = T * k
+    ws, nb = s["ws"]
+    D.group(s["idx"], T, k, E, o["counts"], o["offsets"], o["perm"], o["inv"], ws, nb)
+    D.dispatch(s["in_x"], dt["x"], T, k, d, o["inv"], o["xs"], n)
+    D.combine(s["in_ys"], dt["ys"], n, o["inv"], s["tw"], s["base"], T, k, d, o["y"], dt["y"])
+    if s["train"]:
+        D.combine_grad(s["in_dy"], dt["y"], s["in_ys"], dt["ys"], n, o["inv"], s["tw"], T, k, d, o["dys"], o["dw"],
+                       o["dl"])
+        D.combine(s["in_dxs"], dt["x"], n, o["inv"], None, None, T, k, d, o["dx"], dt["x"])
+    return o
+
+
+def _quant_own(s):
+    D, n = s["D"], s["T"] * s["k"]
+    D.mx_quantize(s["in_x"], s["dt"]["x"], s["T"], s["perm"], s["k"], n, s["cols"], s["packed"])
+    D.mx_dequantize(s["packed"], n, s["cols"], s["out"]["values"], D.DT_BF16)
+    return s["out"]
+
+
+def _product_own(s):
+    D, n, y = s["D"], s["T"] * s["k"], s["out"]["y"]
+    if s["back"]:
+        D.mx_product_grad(s["in_dy"], s["dt"]["y"], n, s["rows"], s["weights"][0], s["cols"], s["E"], s["offsets"], y,
+                          s["dt"]["y"])
+    else:
+        up = s["weights"][1] if s["swiglu"] else None
+        D.mx_product(s["in_a"], n, s["cols"], s["weights"][0], up, s["rows"], s["E"], s["offsets"], y, s["dt"]["y"])
+    return s["out"]
+
+
+# ------------------------------------------------------------------ work
+
+def work(case):
+    op = case["op"]
+    if op == "norm":
+        T, d = case["T"], case["d"]
+        row = SIZE[case["h"]] + SIZE[case["y"]]
+        gate = {"none": 0, "token": T, "channel": d, "full": T * d}[case["gate"]] * 4
+        if not case["train"]:
+            return {"bytes": T * d * (row + SIZE[case["h"]] + SIZE[case["x"]]) + 2 * d * 4 + gate,
+                    "flops": 11 * T * d}
+        # h, y, dh', dx in; x, h', dy, dh out; three weights, the gate and their gradients
+        return {"bytes": T * d * (2 * row + 2 * SIZE[case["h"]] + 2 * SIZE[case["x"]]) + 4 * d * 4 + 2 * gate,
+                "flops": 38 * T * d}
+    if op == "moe":
+        T, k, E, d = (case[n] for n in ("T", "k", "E", "d"))
+        S = T * k
+        b = S * 4 * 4 + 2 * E * 4 + T * d * (SIZE[case["x"]] + 2 * SIZE[case["y"]]) + \
+            S * d * (SIZE[case["x"]] + SIZE[case["ys"]])
+        f = 2 * S * d
+        if case["train"]:
+            b += S * 8 + T * d * (SIZE[case["y"]] + SIZE[case["x"]]) + S * d * (SIZE[case["ys"]] + SIZE[case["x"]])
+            f += 4 * S * d
+        return {"bytes": b, "flops": f}
+    if op == "quant":
+        n, cols = case["T"] * case["k"], case["cols"]
+        return {"bytes": case["T"] * cols * SIZE[case["x"]] + n * 4 + _packed_bytes(n, cols) + n * cols * 2,
+                "flops": 4 * n * cols}
+    n, rows, cols, E = case["T"] * case["k"], case["rows"], case["cols"], case["E"]
+    mats = 2 if case["swiglu"] else 1
+    used = _used_experts(case)
+    acts = n * rows * SIZE[case["y"]]
+    acts += n * cols * SIZE[case["y"]] if case["back"] else _packed_bytes(n, cols)
+    return {"bytes": mats * used * _packed_bytes(rows, cols) + acts + (E + 1) * 4, "flops": 2 * mats * n * rows * cols}
+
+
+def _used_experts(case):
+    """Experts that a call's Zipf-like loads are expected to reach."""
+    E, T, k = case["E"], case["T"], case["k"]
+    p = [(i + 1) ** -1.1 for i in range(E)]
+    total = sum(p)
+    return max(k, round(sum(1 - (1 - v / total) ** (T * k) for v in p)))
+
+
+# ------------------------------------------------------------------ exact
+
+def _exact_norm(s):
+    f64 = torch.float64
+    T, d = s["T"], s["d"]
+    h, y = s["in_h"].to(f64), s["in_y"].to(f64)
+    gate = torch.ones(T, d, dtype=f64, device="cuda")
+    if s["gate"] == "token":
+        gate = s["in_g"].to(f64).reshape(T, 1).expand(T, d)
+    elif s["gate"] == "channel":
+        gate = s["in_g"].to(f64).reshape(1, d).expand(T, d)
+    elif s["gate"] == "full":
+        gate = s["in_g"].to(f64)
+
+    def unit(v):  # v over its root mean square, and that root
+        root = torch.sqrt(v.pow(2).sum(1) / d + EPS).reshape(T, 1)
+        return v / root, root
+
+    yn, yroot = unit(y)
+    hp = s["rho"] * h + gate * s["w"]["post"].to(f64) * yn
+    if not s["train"]:
+        return dict(h=hp, x=unit(hp)[0] * s["w"]["next"].to(f64))
+    hn, hroot = unit(h)
+    dh, dx = s["in_dh"].to(f64), s["in_dx"].to(f64)
+
+    def unit_back(n, root, dn):  # gradient of v / root through its value n
+        return (dn - n * (n * dn).sum(1).reshape(T, 1) / d) / root
+
+    out = dict(x=hn * s["w"]["pre"].to(f64), h=hp,
+               dy=unit_back(yn, yroot, dh * gate * s["w"]["post"].to(f64)),
+               dh=s["rho"] * dh + unit_back(hn, hroot, dx * s["w"]["pre"].to(f64)),
+               dw_post=(dh * gate * yn).sum(0), dw_pre=(dx * hn).sum(0))
+    dgate = dh * yn * s["w"]["post"].to(f64)
+    if s["gate"] != "none":
+        out["dg"] = {"token": dgate.sum(1), "channel": dgate.sum(0), "full": dgate}[s["gate"]]
+    return out
+
+
+def _exact_moe(s):
+    T, k, E, d = (s[n] for n in ("T", "k", "E", "d"))
+    idx = s["idx"].cpu().reshape(-1).tolist()
+    slots = sorted((e, i) for i, e in enumerate(idx) if 0 <= e < E)
+    counts = [0] * E
+    inv = [-1] * (T * k)
+    perm = [-1] * (T * k)
+    for p, (e, i) in enumerate(slots):
+        counts[e] += 1
+        inv[i] = p
+        perm[p] = i
+    offsets = [0]
+    for c in counts:
+        offsets.append(offsets[-1] + c)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    n = len(slots)
+    src = ints([i for _, i in slots]).long()
+    f64 = torch.float64
+    weight = s["tw"].to(f64).reshape(-1)[src]
+    ys = s["in_ys"][:n].to(f64)
+    xs = torch.zeros(T * k, d, dtype=f64, device="cuda")
+    xs[:n] = s["in_x"].to(f64)[src // k]
+    y = s["base"].to(f64).index_add(0, src // k, weight[:, None] * ys)
+    out = dict(counts=ints(counts), offsets=ints(offsets), perm=ints(perm), inv=ints(inv).reshape(T, k), xs=xs, y=y)
+    if s["train"]:
+        dy = s["in_dy"].to(f64)[src // k]
+        dys = torch.zeros(T * k, d, dtype=f64, device="cuda")
+        dys[:n] = weight[:, None] * dy
+        dot = (dy * ys).sum(1)
+        dw = torch.zeros(T * k, dtype=f64, device="cuda")
+        dw[src] = dot
+        mean = torch.zeros(T, dtype=f64, device="cuda").index_add(0, src // k, weight * dot)
+        dl = torch.zeros(T * k, dtype=f64, device="cuda")
+        dl[src] = weight * (dot - mean[src // k])
+        dx = torch.zeros(T, d, dtype=f64, device="cuda").index_add(0, src // k, s["in_dxs"][:n].to(f64))
+        out.update(dys=dys, dw=dw.reshape(T, k), dl=dl.reshape(T, k), dx=dx)
+    return out
+
+
+def _exact_quant(s):
+    x = s["in_x"].double()[torch.div(s["perm"].long(), s["k"], rounding_mode="floor")]
+    blocks = x.reshape(x.shape[0], -1, 32)
+    top = blocks.abs().amax(2, keepdim=True)
+    scale = torch.where(top > 0, torch.exp2((torch.frexp(top).exponent - 3).clamp(-127, 127).double()),
+                        torch.ones_like(top))
+    v = blocks / scale
+    # the spacing of E2M1 values: 0.5 below 2, 1 below 4, 2 above; round-half-even on it takes ties to the even code
+    a = v.abs()
+    step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0)).double()
+    q = (torch.round(a / step) * step).clamp(max=6.0)
+    return dict(values=(torch.sign(v) * q * scale).reshape(x.shape))
+
+
+def _exact_product(s):
+    rows, cols, n = s["rows"], s["cols"], s["T"] * s["k"]
+    grid = torch.tensor([m * sign for sign in (1, -1) for m in MAGNITUDES], dtype=torch.float64, device="cuda")
+
+    def decode(packed, count):  # `count` rows
+        half = count * cols // 2
+        b = packed[:half].int().reshape(count, cols // 2, 1)
+        code = torch.cat([b % 16, torch.div(b, 16, rounding_mode="floor")], dim=2).reshape(count, cols)
+        power = torch.exp2(packed[half:].double() - 127.0).reshape(count, cols // 32)
+        return grid[code.long()] * power.repeat_interleave(32, dim=1)
+
+    left = s["in_dy"].double() if s["back"] else decode(s["in_a"], n)
+    out = torch.zeros(n, cols if s["back"] else rows, dtype=torch.float64, device="cuda")
+    nb = _packed_bytes(rows, cols)
+    edge = s["offsets"].cpu().tolist()
+    for e, (lo, hi) in enumerate(zip(edge, edge[1:])):
+        if hi > lo:
+            part = [decode(w[e * nb:(e + 1) * nb], rows) for w in s["weights"]]
+            if s["back"]:
+                out[lo:hi] = torch.mm(left[lo:hi], part[0])
+            else:
+                first = torch.mm(left[lo:hi], part[0].t().contiguous())
+                if s["swiglu"]:
+                    first = first * torch.sigmoid(first) * torch.mm(left[lo:hi], part[1].t().contiguous())
+                out[lo:hi] = first
+    return dict(y=out)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"norm": _exact_norm, "moe": _exact_moe, "quant": _exact_quant, "product": _exact_product}[case["op"]](s)
