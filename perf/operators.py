@@ -208,7 +208,7 @@ def prepare(case, seed):
         # channels of unequal size, as activations have them
         channel = torch.exp(r.normal(case["cols"]))
         s["in_x"] = (r.normal(T, case["cols"]) * channel).to(TYPES[case["x"]])
-        s["perm"] = _sorted_slots(_experts(r, T, k, max(16, k)), max(16, k))[2]
+        s["inv"] = _sorted_slots(_experts(r, T, k, max(16, k)), max(16, k))[3].reshape(T, k)
     else:
         T, k, E, rows, cols = (case[n] for n in ("T", "k", "E", "rows", "cols"))
         n = T * k
@@ -296,11 +296,14 @@ def _round(v, kind):
 
 
 def _quant_plain(s):
-    x = s["in_x"].float()[s["perm"].long() // s["k"]]
-    n, cols = x.shape
-    code, scale = _codes(x.reshape(n, cols // 32, 32))
+    x = s["in_x"].float()
+    T, cols = x.shape
+    code, scale = _codes(x.reshape(T, cols // 32, 32))
     values = torch.tensor(MAGNITUDES + tuple(-v for v in MAGNITUDES), device=x.device)
-    return (torch.ldexp(values[code.long()], (scale - 127)[..., None])).reshape(n, cols).to(torch.bfloat16)
+    rows = torch.ldexp(values[code.long()], (scale - 127)[..., None]).reshape(T, 1, cols).to(torch.bfloat16)
+    out = torch.zeros(T * s["k"], cols, device=x.device, dtype=torch.bfloat16)
+    out[s["inv"].reshape(-1).long()] = rows.expand(T, s["k"], cols).reshape(-1, cols)
+    return out
 
 
 def _product(s, f, rounded):
@@ -404,7 +407,7 @@ def _moe_own(s):
 
 def _quant_own(s):
     D, n = s["D"], s["T"] * s["k"]
-    D.mx_quantize(s["in_x"], s["dt"]["x"], s["T"], s["perm"], s["k"], n, s["cols"], s["packed"])
+    D.mx_quantize(s["in_x"], s["dt"]["x"], s["T"], s["inv"], s["k"], n, s["cols"], s["packed"])
     D.mx_dequantize(s["packed"], n, s["cols"], s["out"]["values"], D.DT_BF16)
     return s["out"]
 
@@ -542,7 +545,8 @@ def _exact_moe(s):
 
 
 def _exact_quant(s):
-    x = s["in_x"].double()[torch.div(s["perm"].long(), s["k"], rounding_mode="floor")]
+    slot = torch.argsort(s["inv"].reshape(-1))  # the slot that each row holds
+    x = s["in_x"].double()[torch.div(slot, s["k"], rounding_mode="floor")]
     blocks = x.reshape(x.shape[0], -1, 32)
     top = blocks.abs().amax(2, keepdim=True)
     scale = torch.where(top > 0, torch.exp2((torch.frexp(top).exponent - 3).clamp(-127, 127).double()),
