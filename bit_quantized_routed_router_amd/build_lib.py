@@ -36,12 +36,18 @@ SOURCES = {
     "dense.hip": [],
     "capi.cpp": ["-x", "hip"],
     "trace.cpp": ["-x", "hip"],
+    "ops/norm.hip": [],
+    "ops/moe.hip": [],
+    "ops/mx.hip": [],
+    "ops/mxprod.hip": [],
+    "ops/mxgrad.hip": [],
+    "ops/capi_ops.cpp": ["-x", "hip"],
 }
 
 
 def _compile(name: str, extra: list[str]) -> str:
     src = os.path.join(CSRC, name)
-    obj = os.path.join(BUILD, name + ".o")
+    obj = os.path.join(BUILD, name.replace("/", "_") + ".o")
     cmd = COMMON + extra + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

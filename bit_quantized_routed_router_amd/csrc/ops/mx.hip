@@ -1,0 +1,122 @@
+// MXFP4 rows of activations (format in include/ds4moe.h): quantisation into a
+// packed matrix, at the rows that a sort gives, and the values back.
+//
+// A lane takes 8 columns, four lanes a block of 32: the block's largest
+// magnitude comes from two exchanges within the quad, as an integer maximum
+// of the bits without their sign (so a NaN counts as the largest), and the
+// conversion instruction rounds to E2M1 to nearest, ties to the even code,
+// beyond 6 to 6.  Codes leave as one word per lane and scales as one byte per
+// quad.
+#include "../trace.h"
+#include "ops.h"
+
+namespace ds4 {
+
+template <int CTRL>
+__device__ inline uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+
+// 2^(sc - 127), by the exponent field (sc = 0: the subnormal 2^-127)
+__device__ inline float pow2_scale(uint32_t sc) {
+  return __builtin_bit_cast(float, sc ? sc << 23 : 0x00400000u);
+}
+
+// E8M0 code of a block whose largest magnitude has the fp32 bits m:
+// floor(log2) - 2 + 127 within 0 .. 254; 255 where the block holds an
+// infinity or a NaN, 0 where all of it is zero.
+__device__ inline uint32_t block_scale(uint32_t m) {
+  if (m >= 0x7F800000u) return 255u;
+  // a subnormal's exponent is below the range's: it gives 0 as well
+  return (uint32_t)max((int)(m >> 23) - 2, 0);
+}
+
+// Codes of -0 become +0, as the format's quantiser has them.
+__device__ inline uint32_t no_minus_zero(uint32_t c) {
+  const uint32_t m = c & 0x77777777u;
+  const uint32_t any = (m | (m >> 1) | (m >> 2)) & 0x11111111u;
+  return m | (c & (any << 3));
+}
+
+// Block b: token b / nb, columns 2048 (b % nb) onward, eight per thread.
+template <bool BF>
+__global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x, const int32_t* __restrict__ inv,
+                                                     int k, int cols, int nb, int rows,
+                                                     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t t = blockIdx.x / nb;
+  const int c = ((blockIdx.x % nb) * 256 + threadIdx.x) * 8;
+  if (c >= cols) return;  // whole quads: cols is a multiple of 32
+  const Raw8<BF> v = ld8<BF>(x, t * cols + c);
+  uint32_t m = 0;
+  float f[8];
+  unpack8(v, f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu);
+  m = dpp_max<0xB1>(m);
+  m = dpp_max<0x4E>(m);
+  const uint32_t sc = block_scale(m);
+  uint32_t w = 0;
+  if (sc != 255u) {
+    const float s = pow2_scale(sc);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[0], f[1], s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], s, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], s, 3);
+    w = no_minus_zero(w);
+  }
+  for (int j = 0; j < k; ++j) {
+    const int64_t p = inv ? inv[t * k + j] : (int)t;
+    if (p < 0 || p >= rows) continue;
+    const int64_t i = p * cols + c;
+    *(uint32_t*)(codes + i / 2) = w;
+    if ((threadIdx.x & 3) == 0) scales[i / 32] = (uint8_t)sc;
+  }
+}
+
+template <bool BF>
+__global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t* __restrict__ codes,
+                                                       const uint8_t* __restrict__ scales, int64_t n8,
+                                                       void* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const uint32_t w = ((const uint32_t*)codes)[i];
+  const uint32_t sc = scales[i / 4];
+  const float s = sc == 255u ? __builtin_nanf("") : pow2_scale(sc);
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t c = (w >> (4 * e)) & 15u;
+    // magnitude: exponent field 0 holds 0 and 0.5, else (1 + m / 2) 2^(e - 1)
+    const uint32_t x2 = (c >> 1) & 3u, m1 = c & 1u;
+    const float mag = x2 ? __builtin_bit_cast(float, ((x2 + 126u) << 23) | (m1 << 22)) : 0.5f * (float)m1;
+    v[e] = (c & 8u ? -mag : mag) * s;
+  }
+  st8<BF>(out, i * 8, v);
+}
+
+hipError_t launch_mx_quantize(const void* x, int dt, int64_t T, const int32_t* inv, int k, int64_t rows, int cols,
+                              void* packed, hipStream_t st) {
+  const int nb = (cols + 2047) / 2048;
+  const dim3 grid((unsigned)(T * nb));
+  uint8_t* codes = (uint8_t*)packed;
+  uint8_t* scales = codes + rows * cols / 2;
+  if (dt == DS4MOE_DT_BF16)
+    DS4_LAUNCH(k_mx_quantize<true>, grid, dim3(256), 0, st, x, inv, k, cols, nb, (int)rows, codes, scales);
+  else
+    DS4_LAUNCH(k_mx_quantize<false>, grid, dim3(256), 0, st, x, inv, k, cols, nb, (int)rows, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const void* packed, int64_t rows, int cols, void* out, int dt, hipStream_t st) {
+  const int64_t n8 = rows * cols / 8;
+  const uint8_t* codes = (const uint8_t*)packed;
+  const uint8_t* scales = codes + rows * cols / 2;
+  const dim3 grid((unsigned)((n8 + 255) / 256));
+  if (dt == DS4MOE_DT_BF16)
+    DS4_LAUNCH(k_mx_dequantize<true>, grid, dim3(256), 0, st, codes, scales, n8, out);
+  else
+    DS4_LAUNCH(k_mx_dequantize<false>, grid, dim3(256), 0, st, codes, scales, n8, out);
+  return hipGetLastError();
+}
+
+}  // namespace ds4

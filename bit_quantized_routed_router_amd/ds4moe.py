@@ -20,6 +20,7 @@ EXPERTS_CB2_Q2K, EXPERTS_MXFP4, EXPERTS_Q4K = 0, 1, 2
 DT_F32, DT_BF16 = 0, 1
 MODE_DECODE, MODE_PREFILL, MODE_ROUTE = 0, 1, 2
 DECODE_MAX_T = 64
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
 
 
 class Ds4moeError(RuntimeError):
@@ -46,6 +47,14 @@ class HcDesc(ctypes.Structure):
         ("n_streams", ctypes.c_int32), ("d_model", ctypes.c_int32), ("sinkhorn_iters", ctypes.c_int32),
         ("eps", ctypes.c_float), ("alpha_pre", ctypes.c_float), ("alpha_post", ctypes.c_float),
         ("alpha_res", ctypes.c_float), ("phi", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+    ]
+
+
+class NormDesc(ctypes.Structure):
+    """Mirror of ds4moe_norm."""
+    _fields_ = [
+        ("d_model", ctypes.c_int32), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float), ("gate", ctypes.c_int32),
+        ("w_pre", ctypes.c_void_p), ("w_post", ctypes.c_void_p), ("w_next", ctypes.c_void_p),
     ]
 
 
@@ -86,6 +95,28 @@ def lib() -> ctypes.CDLL:
         L.ds4moe_hc_pre.argtypes = [HP, P, I64, P, P, P, P, SZ, P]
         L.ds4moe_hc_post.restype = I32
         L.ds4moe_hc_post.argtypes = [HP, P, P, P, I64, P, P]
+        NP, N32 = ctypes.POINTER(NormDesc), ctypes.c_int32
+        L.ds4moe_norm_workspace_bytes.restype = SZ
+        L.ds4moe_norm_workspace_bytes.argtypes = [NP, I64]
+        L.ds4moe_group_workspace_bytes.restype = SZ
+        L.ds4moe_group_workspace_bytes.argtypes = [I64, N32, N32]
+        for name, args in {
+            "norm_pre": [NP, P, I32, I64, P, I32, P],
+            "norm_post": [NP, P, I32, P, I32, P, I64, P, P, I32, P],
+            "norm_pre_grad": [NP, P, I32, P, I32, P, I64, P, P, P, SZ, P],
+            "norm_post_grad": [NP, P, I32, P, I32, P, I64, P, P, P, P, SZ, P],
+            "group": [P, I64, N32, N32, P, P, P, P, P, SZ, P],
+            "dispatch": [P, I32, I64, N32, N32, P, P, I64, P],
+            "combine": [P, I32, I64, P, P, P, I64, N32, N32, P, I32, P],
+            "combine_grad": [P, I32, P, I32, I64, P, P, I64, N32, N32, P, P, P, P],
+            "mx_quantize": [P, I32, I64, P, N32, I64, N32, P, P],
+            "mx_dequantize": [P, I64, N32, P, I32, P],
+            "mx_product": [P, I64, N32, P, P, N32, N32, P, P, I32, P],
+            "mx_product_grad": [P, I32, I64, N32, P, N32, N32, P, P, I32, P],
+        }.items():
+            fn = getattr(L, "ds4moe_" + name)
+            fn.restype = I32
+            fn.argtypes = args
         L.ds4moe_strerror.restype = ctypes.c_char_p
         L.ds4moe_strerror.argtypes = [I32]
         L.ds4moe_trace_enable.restype = I32
@@ -102,7 +133,11 @@ EXPORTS = ["ds4moe_packed_bytes", "ds4moe_quantize", "ds4moe_dequantize", "ds4mo
            "ds4moe_workspace_init",
            "ds4moe_route", "ds4moe_forward_decode", "ds4moe_forward_decode_static", "ds4moe_forward_prefill", "ds4moe_strerror",
            "ds4moe_grid_levels", "ds4moe_trace_enable", "ds4moe_trace_read",
-           "ds4moe_hc_workspace_bytes", "ds4moe_hc_pre", "ds4moe_hc_post"]
+           "ds4moe_hc_workspace_bytes", "ds4moe_hc_pre", "ds4moe_hc_post",
+           "ds4moe_norm_workspace_bytes", "ds4moe_norm_pre", "ds4moe_norm_post", "ds4moe_norm_pre_grad",
+           "ds4moe_norm_post_grad", "ds4moe_group_workspace_bytes", "ds4moe_group", "ds4moe_dispatch",
+           "ds4moe_combine", "ds4moe_combine_grad", "ds4moe_mx_quantize", "ds4moe_mx_dequantize",
+           "ds4moe_mx_product", "ds4moe_mx_product_grad"]
 
 
 def strerror(status: int) -> str:
@@ -208,6 +243,124 @@ class Hc:
         ws = torch.empty(n, dtype=torch.uint8, device="cuda")
         workspace_init(ws, n)
         return ws, n
+
+
+# ---------------------------------------------------------------- operators around the layer
+# Norms, tokens sorted by expert and back, MXFP4 rows and products.  Tensors
+# here are checked to be contiguous and on the current device, since the
+# library sees bare addresses.
+
+def _tens(t, what: str):
+    """Address of a contiguous tensor on the current device (an int passes as
+    it is, None as NULL)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: tensors must be contiguous and on the GPU")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensor on device {t.get_device()}, current device {torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def norm_workspace_bytes(desc: NormDesc, T: int) -> int:
+    return int(lib().ds4moe_norm_workspace_bytes(ctypes.byref(desc), T))
+
+
+def norm_pre(desc, h, h_dtype, T, x, x_dtype, stream=None) -> None:
+    n = "ds4moe_norm_pre"
+    _check(lib().ds4moe_norm_pre(ctypes.byref(desc), _tens(h, n), h_dtype, T, _tens(x, n), x_dtype, _stream(stream)), n)
+
+
+def norm_post(desc, h, h_dtype, y, y_dtype, gate, T, h_out, x_next, x_dtype, stream=None) -> None:
+    n = "ds4moe_norm_post"
+    _check(lib().ds4moe_norm_post(ctypes.byref(desc), _tens(h, n), h_dtype, _tens(y, n), y_dtype, _tens(gate, n), T,
+                                  _tens(h_out, n), _tens(x_next, n), x_dtype, _stream(stream)), n)
+
+
+def norm_pre_grad(desc, h, h_dtype, dx, x_dtype, dh_out, T, dh, dw_pre, ws, ws_bytes, stream=None) -> None:
+    n = "ds4moe_norm_pre_grad"
+    _check(lib().ds4moe_norm_pre_grad(ctypes.byref(desc), _tens(h, n), h_dtype, _tens(dx, n), x_dtype,
+                                      _tens(dh_out, n), T, _tens(dh, n), _tens(dw_pre, n), _tens(ws, n), ws_bytes,
+                                      _stream(stream)), n)
+
+
+def norm_post_grad(desc, dh_out, h_dtype, y, y_dtype, gate, T, dy, dw_post, dgate, ws, ws_bytes, stream=None) -> None:
+    n = "ds4moe_norm_post_grad"
+    _check(lib().ds4moe_norm_post_grad(ctypes.byref(desc), _tens(dh_out, n), h_dtype, _tens(y, n), y_dtype,
+                                       _tens(gate, n), T, _tens(dy, n), _tens(dw_post, n), _tens(dgate, n),
+                                       _tens(ws, n), ws_bytes, _stream(stream)), n)
+
+
+class Norm:
+    """Weights of a block's norms (float32 CUDA tensors [d], or None for ones)
+    plus the ds4moe_norm descriptor."""
+
+    def __init__(self, d, eps=1e-6, res_scale=1.0, gate=GATE_NONE, w_pre=None, w_post=None, w_next=None):
+        self.tensors = dict(w_pre=w_pre, w_post=w_post, w_next=w_next)
+        for name, w in self.tensors.items():
+            if w is not None and (w.dtype != torch.float32 or w.numel() != d):
+                raise ValueError(f"{name}: expected {d} float32 values")
+        self.d = d
+        p = [_tens(w, "Norm") for w in (w_pre, w_post, w_next)]
+        self.desc = NormDesc(d, float(eps), float(res_scale), gate, *p)
+
+    def workspace(self, T: int):
+        n = norm_workspace_bytes(self.desc, T)
+        if n == 0:
+            raise Ds4moeError(ESHAPE, "ds4moe_norm_workspace_bytes")
+        return torch.empty(n, dtype=torch.uint8, device="cuda"), n
+
+
+def group_workspace_bytes(T: int, k: int, n_experts: int) -> int:
+    return int(lib().ds4moe_group_workspace_bytes(T, k, n_experts))
+
+
+def group(topk_idx, T, k, n_experts, counts, offsets, perm, inv, ws, ws_bytes, stream=None) -> None:
+    n = "ds4moe_group"
+    _check(lib().ds4moe_group(_tens(topk_idx, n), T, k, n_experts, _tens(counts, n), _tens(offsets, n), _tens(perm, n),
+                              _tens(inv, n), _tens(ws, n), ws_bytes, _stream(stream)), n)
+
+
+def dispatch(x, x_dtype, T, k, d, inv, xs, n_rows, stream=None) -> None:
+    n = "ds4moe_dispatch"
+    _check(lib().ds4moe_dispatch(_tens(x, n), x_dtype, T, k, d, _tens(inv, n), _tens(xs, n), n_rows, _stream(stream)),
+           n)
+
+
+def combine(ys, ys_dtype, n_rows, inv, topk_w, base, T, k, d, y, y_dtype, stream=None) -> None:
+    n = "ds4moe_combine"
+    _check(lib().ds4moe_combine(_tens(ys, n), ys_dtype, n_rows, _tens(inv, n), _tens(topk_w, n), _tens(base, n), T, k,
+                                d, _tens(y, n), y_dtype, _stream(stream)), n)
+
+
+def combine_grad(dy, y_dtype, ys, ys_dtype, n_rows, inv, topk_w, T, k, d, dys, dw, dlogits, stream=None) -> None:
+    n = "ds4moe_combine_grad"
+    _check(lib().ds4moe_combine_grad(_tens(dy, n), y_dtype, _tens(ys, n), ys_dtype, n_rows, _tens(inv, n),
+                                     _tens(topk_w, n), T, k, d, _tens(dys, n), _tens(dw, n), _tens(dlogits, n),
+                                     _stream(stream)), n)
+
+
+def mx_quantize(x, x_dtype, T, inv, k, n_rows, cols, packed, stream=None) -> None:
+    n = "ds4moe_mx_quantize"
+    _check(lib().ds4moe_mx_quantize(_tens(x, n), x_dtype, T, _tens(inv, n), k, n_rows, cols, _tens(packed, n),
+                                    _stream(stream)), n)
+
+
+def mx_dequantize(packed, n_rows, cols, out, out_dtype, stream=None) -> None:
+    n = "ds4moe_mx_dequantize"
+    _check(lib().ds4moe_mx_dequantize(_tens(packed, n), n_rows, cols, _tens(out, n), out_dtype, _stream(stream)), n)
+
+
+def mx_product(a, n_rows, cols, w, w_up, rows, n_experts, offsets, y, y_dtype, stream=None) -> None:
+    n = "ds4moe_mx_product"
+    _check(lib().ds4moe_mx_product(_tens(a, n), n_rows, cols, _tens(w, n), _tens(w_up, n), rows, n_experts,
+                                   _tens(offsets, n), _tens(y, n), y_dtype, _stream(stream)), n)
+
+
+def mx_product_grad(dy, dy_dtype, n_rows, rows, w, cols, n_experts, offsets, da, da_dtype, stream=None) -> None:
+    n = "ds4moe_mx_product_grad"
+    _check(lib().ds4moe_mx_product_grad(_tens(dy, n), dy_dtype, n_rows, rows, _tens(w, n), cols, n_experts,
+                                        _tens(offsets, n), _tens(da, n), da_dtype, _stream(stream)), n)
 
 
 def trace_enable(on: bool) -> None:

@@ -310,6 +310,155 @@ int ds4moe_hc_pre(const ds4moe_hc *H, const float *X, int64_t T, float *coef, fl
 int ds4moe_hc_post(const ds4moe_hc *H, const float *X, const float *y, const float *coef, int64_t T,
                    float *X_out, void *stream);
 
+/* ----------------------------------------------------------------------
+ * Norms before and after a block, with the block's gate and residual scale.
+ * With the block's input stream h [T][d] and its output y [T][d] (the layer's
+ * y, for one):
+ *   pre    x  = h r w_pre,   r = 1 / sqrt(sum_c h^2 / d + eps)
+ *   post   h' = res_scale h + g (y q w_post),   q = 1 / sqrt(sum_c y^2 / d + eps)
+ *   next   x' = h' r' w_next, the next block's pre-norm, in the same pass
+ *          (of h' before it is rounded to its type)
+ * Sums are fp32; every output is rounded once.  h and h_out share a type, x
+ * and dx, y and dy: each fp32 or bf16 (DS4MOE_DT_*); weights, gates and their
+ * gradients are fp32.  A row's sum of squares must stay in fp32's range
+ * (|h| and |y| below 2^56).  Non-finite values stay within their row, but for the
+ * gradients summed over tokens.  A gate of zero does not hide a non-finite y.
+ * All tensors are contiguous; device pointers 16-byte aligned, a gate per
+ * token and its gradient 4-byte aligned.  1 <= T <= 1048576.
+ * ---------------------------------------------------------------------- */
+/* what the gate g holds a value for: nothing (g = 1), each token [T], each
+ * channel [d], each element [T][d] */
+enum { DS4MOE_GATE_NONE = 0, DS4MOE_GATE_TOKEN = 1, DS4MOE_GATE_CHANNEL = 2, DS4MOE_GATE_FULL = 3 };
+
+typedef struct {
+  int32_t d_model;      /* d: multiple of 256, <= 16384 */
+  float eps;            /* finite, > 0 */
+  float res_scale;      /* finite */
+  int32_t gate;         /* DS4MOE_GATE_* */
+  const float *w_pre;   /* fp32 [d] each, or NULL for ones */
+  const float *w_post;
+  const float *w_next;
+} ds4moe_norm;
+
+/* Workspace bytes the gradient calls need for T tokens (0 on invalid input).
+ * It need not be cleared; calls that share one must be ordered on a stream. */
+size_t ds4moe_norm_workspace_bytes(const ds4moe_norm *N, int64_t T);
+
+/* x [T][d] from h [T][d]. */
+int ds4moe_norm_pre(const ds4moe_norm *N, const void *h, int h_dtype, int64_t T, void *x, int x_dtype, void *stream);
+
+/* h_out [T][d], and x_next [T][d] unless NULL, from h, y and the gate (NULL
+ * exactly with DS4MOE_GATE_NONE).  h_out may equal h; no other overlap. */
+int ds4moe_norm_post(const ds4moe_norm *N, const void *h, int h_dtype, const void *y, int y_dtype, const float *gate,
+                     int64_t T, void *h_out, void *x_next, int x_dtype, void *stream);
+
+/* Gradients of the pre-norm, with the residual path's:
+ *   v = dx w_pre,  dh = res_scale dh_out + r (v - h r^2 sum_c(h v) / d)
+ *   dw_pre = sum_t dx h r
+ * dh_out [T][d] (h's type): the gradient of ds4moe_norm_post's h_out, or NULL
+ * for none; dh may equal it.  dw_pre fp32 [d] or NULL (then ws may be NULL).
+ * Sums over tokens have a fixed order. */
+int ds4moe_norm_pre_grad(const ds4moe_norm *N, const void *h, int h_dtype, const void *dx, int x_dtype,
+                         const void *dh_out, int64_t T, void *dh, float *dw_pre, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/* Gradients of the post-norm:
+ *   u = dh_out g w_post,  dy = q (u - y q^2 sum_c(y u) / d)
+ *   dw_post = sum_t dh_out g y q,  dgate = dh_out y q w_post summed over what a
+ *   gate value is shared by
+ * dy may equal y.  dw_post fp32 [d] or NULL; dgate in the gate's layout or
+ * NULL (NULL with DS4MOE_GATE_NONE).  ws may be NULL when neither dw_post nor
+ * a gate per channel's gradient is asked for.  Where x_next was used too, its
+ * gradient comes first: ds4moe_norm_pre_grad of the next block. */
+int ds4moe_norm_post_grad(const ds4moe_norm *N, const void *dh_out, int h_dtype, const void *y, int y_dtype,
+                          const float *gate, int64_t T, void *dy, float *dw_post, float *dgate, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* ----------------------------------------------------------------------
+ * Tokens sorted by expert and back, for experts outside the layer's own calls
+ * (other formats, adapters, training).  Slots are s = t k + j.  A slot whose
+ * expert lies outside [0, n_experts) -- padding, a slot dropped by a capacity
+ * -- takes no part: it has no row, its weight is never read and its gradients
+ * are zero.  A token may name an expert more than once.  1 <= T <= 1048576,
+ * 1 <= k <= 16, 1 <= n_experts <= 1024; d a multiple of 256, <= 16384; n_rows,
+ * the rows of xs and ys, at most 2^24.  Row types: DS4MOE_DT_F32 or _BF16.
+ * ---------------------------------------------------------------------- */
+
+/* Workspace bytes of ds4moe_group (0 on invalid input).  It need not be
+ * cleared; calls that share one must be ordered on a stream. */
+size_t ds4moe_group_workspace_bytes(int64_t T, int32_t k, int32_t n_experts);
+
+/* Stable sort of the slots by expert (topk_idx [T][k] as ds4moe_route or any
+ * other router gives it):
+ *   counts [E], offsets [E+1]  slots of each expert, and their exclusive scan
+ *   perm [T*k]                 the slot at each position; -1 from offsets[E] on
+ *   inv [T][k]                 the position of each slot; -1 for one without */
+int ds4moe_group(const int32_t *topk_idx, int64_t T, int32_t k, int32_t n_experts, int32_t *counts, int32_t *offsets,
+                 int32_t *perm, int32_t *inv, void *ws, size_t ws_bytes, void *stream);
+
+/* xs[inv[s]] = x[t] for every slot with a row (x [T][d], xs [n_rows][d], one
+ * type).  Rows that no slot has, and positions outside [0, n_rows), are left as they were.
+ * Its gradient is ds4moe_combine with topk_w and base NULL. */
+int ds4moe_dispatch(const void *x, int x_dtype, int64_t T, int32_t k, int32_t d, const int32_t *inv, void *xs,
+                    int64_t n_rows, void *stream);
+
+/* y[t] = base[t] + sum_j topk_w[t][j] ys[inv[t k + j]], j ascending, in fp32,
+ * rounded once.  topk_w NULL: weights of one.  base [T][d] in y's type (the
+ * shared expert's output, say) or NULL; y may equal base.  A token without
+ * any row gets base, or zeros. */
+int ds4moe_combine(const void *ys, int ys_dtype, int64_t n_rows, const int32_t *inv, const float *topk_w,
+                   const void *base, int64_t T, int32_t k, int32_t d, void *y, int y_dtype, void *stream);
+
+/* Gradients of ds4moe_combine (that of base is dy itself):
+ *   dys[inv[s]] = w_s dy[t]                 (ys's type; rows without a slot are left as they were)
+ *   dw[s]       = sum_c dy[t] ys[inv[s]]    fp32 [T][k]
+ *   dlogits[s]  = w_s (dw_s - sum_j w_j dw_j): through the softmax over the
+ *                 token's slots that gave topk_w, fp32 [T][k]
+ * Any of the three may be NULL, not all.  dys may equal ys. */
+int ds4moe_combine_grad(const void *dy, int y_dtype, const void *ys, int ys_dtype, int64_t n_rows, const int32_t *inv,
+                        const float *topk_w, int64_t T, int32_t k, int32_t d, void *dys, float *dw, float *dlogits,
+                        void *stream);
+
+/* ----------------------------------------------------------------------
+ * MXFP4 rows and products (format above; both operands in FP4).  A packed
+ * matrix of n rows is laid out as ds4moe_packed_bytes(DS4MOE_FMT_MXFP4, n,
+ * cols) says; cols a multiple of 256, <= 16384; 1 <= n <= 2^24.
+ * ---------------------------------------------------------------------- */
+
+/* Rows of activations, x [T][cols] fp32 or bf16, quantized as
+ * ds4moe_quantize(DS4MOE_FMT_MXFP4) does and stored at the rows that a sort
+ * gives: row inv[t k + j] of packed [n][cols] takes token t, for each of its
+ * k slots (positions outside [0, n) are skipped, rows that no slot has are
+ * left as they were).  inv NULL: row t takes token t (k = 1, n >= T).  A
+ * block of 32 that holds an infinity or a NaN gets scale code 0xFF: all of
+ * it reads back as NaN. */
+int ds4moe_mx_quantize(const void *x, int x_dtype, int64_t T, const int32_t *inv, int32_t k, int64_t n, int32_t cols,
+                       void *packed, void *stream);
+
+/* The values of a packed matrix, fp32 or bf16 (both exact). */
+int ds4moe_mx_dequantize(const void *packed, int64_t n, int32_t cols, void *out, int out_dtype, void *stream);
+
+/* Products of packed rows a [n][cols] with n_experts packed matrices w, each
+ * [rows][cols], back to back (a layer's gate, up or down in MXFP4):
+ *   w_up NULL:  y[p][r] = sum_c a[p][c] w_e[r][c]
+ *   otherwise:  y[p][r] = silu(g) u, g and u the products with w_e and w_up_e
+ * for the rows p in [offsets[e], offsets[e+1]) of each expert e, offsets
+ * (device, ascending) as ds4moe_group gives them; NULL with n_experts = 1: all
+ * rows.  Offsets are taken as held to [0, n]; rows of y [n][rows] that no
+ * expert has are left as they were.  Products and block scales are exact,
+ * sums fp32, y (fp32 or bf16) is rounded once.  rows: a multiple of 16, <=
+ * 16384; n_experts <= 1024. */
+int ds4moe_mx_product(const void *a, int64_t n, int32_t cols, const void *w, const void *w_up, int32_t rows,
+                      int32_t n_experts, const int32_t *offsets, void *y, int y_dtype, void *stream);
+
+/* Gradient of the product (w_up NULL) to its rows, as if they had not been
+ * rounded to FP4: da[p][c] = sum_r dy[p][r] w_e[r][c], dy [n][rows] and da
+ * [n][cols] fp32 or bf16.  Products are exact for bf16 and to fp32 rounding
+ * for fp32, sums are fp32, da is rounded once.  Rows without an expert are
+ * left as they were. */
+int ds4moe_mx_product_grad(const void *dy, int dy_dtype, int64_t n, int32_t rows, const void *w, int32_t cols,
+                           int32_t n_experts, const int32_t *offsets, void *da, int da_dtype, void *stream);
+
 /* Opt-in per-kernel timing (profiling aid).  While enabled, every kernel
  * the library launches is bracketed by two HIP events on its stream, which
  * adds a little launch overhead.  Thread-safe. */
