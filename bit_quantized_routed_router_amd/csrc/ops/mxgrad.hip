@@ -70,10 +70,10 @@ __global__ __launch_bounds__(256) void k_mx_grad(const void* __restrict__ dy, co
   __shared__ u32x4_t ws[kGradBN * 8];
   __shared__ u32x4_t as[PARTS][BM * 8];
   const int nc = cols / kGradBN;
-  const RowTile rt = find_tile(offsets, E, n, BM, blockIdx.x / nc, lds);
+  const RowTile rt = find_tile(offsets, E, n, BM, nc, lds);
   if (rt.cnt <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, q = lane >> 4;
-  const int c0 = blockIdx.x % nc * kGradBN;
+  const int c0 = rt.part * kGradBN;
   const int rg = tid >> 5, cw = tid & 31;
   const uint8_t* wb = w + (int64_t)rt.e * ((int64_t)rows * cols / 32 * 17);
   const uint8_t* wcode = wb + (c0 + 8 * cw) / 2;

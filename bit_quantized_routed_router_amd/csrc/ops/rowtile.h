@@ -12,11 +12,36 @@ namespace ds4 {
 // Offsets are held within [0, n] and taken as empty where they descend, so a
 // bad one reads and writes nothing out of range.
 struct RowTile {
-  int e, lo, cnt;  // rows lo .. lo + cnt - 1 (cnt <= bm)
+  int e, lo, cnt;  // rows lo .. lo + cnt - 1 (cnt <= bm; 0: no work)
+  int part;        // which of the tile's column parts
 };
-__device__ inline RowTile find_tile(const int32_t* offsets, int E, int n, int bm, int tile, int* lds) {
-  RowTile r{0, tile * bm, min(bm, n - tile * bm)};
-  if (!offsets) return r;
+// The tile and part of item `local` of an expert with m tiles: kPartGroup
+// parts of all its tiles before the next parts, a tile's neighbouring parts
+// next to each other.
+constexpr int kPartGroup = 8;
+__device__ inline void split_item(int local, int m, int parts, int& tile, int& part) {
+  const int g = local / (m * kPartGroup), left = local - g * m * kPartGroup;
+  const int wide = min(kPartGroup, parts - g * kPartGroup);
+  tile = left / wide;
+  part = g * kPartGroup + left - tile * wide;
+}
+
+// The work item of this block among (row tile, part) pairs, `parts` to a row
+// tile.  Blocks are dealt to the 8 XCDs in turn; here each XCD takes a
+// contiguous run of the items there are, in which a few parts' weights meet
+// all tiles of their expert before the next parts', so that what runs
+// together shares both through the XCD's L2.  lds: 16 ints.
+__device__ inline RowTile find_tile(const int32_t* offsets, int E, int n, int bm, int parts, int* lds) {
+  RowTile r{0, 0, 0, 0};
+  int item, t;
+  if (!offsets) {
+    const int m = (n + bm - 1) / bm;
+    if (!xcd_item(m * parts, item)) return r;
+    split_item(item, m, parts, t, r.part);
+    r.lo = t * bm;
+    r.cnt = min(bm, n - r.lo);
+    return r;
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
   const int per = (E + blockDim.x - 1) / blockDim.x, e0 = tid * per;
   int tiles = 0;
@@ -32,29 +57,36 @@ __device__ inline RowTile find_tile(const int32_t* offsets, int E, int n, int bm
     if (lane >= o) x += y;
   }
   if (lane == 63) lds[wave] = x;
-  if (tid == 0) lds[8] = -1;
   __syncthreads();
-  int first = x - tiles;
-  for (int w = 0; w < nw; ++w)
+  int first = x - tiles, total = 0;
+  for (int w = 0; w < nw; ++w) {
     if (w < wave) first += lds[w];
-  if (tile >= first && tile < first + tiles) {
-    int left = tile - first;
+    total += lds[w];
+  }
+  if (!xcd_item(total * parts, item)) return r;
+  if (item >= first * parts && item < (first + tiles) * parts) {
+    int left = item - first * parts;
     for (int i = 0; i < per; ++i) {
       const int lo = min(max(offsets[e0 + i], 0), n), hi = min(max(offsets[e0 + i + 1], 0), n);
       const int m = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-      if (left < m) {
+      if (left < m * parts) {
+        int part;
+        split_item(left, m, parts, t, part);
         lds[8] = e0 + i;
-        lds[9] = lo + left * bm;
-        lds[10] = min(bm, hi - lo - left * bm);
+        lds[9] = lo + t * bm;
+        lds[10] = min(bm, hi - lo - t * bm);
+        lds[11] = part;
         break;
       }
-      left -= m;
+      left -= m * parts;
     }
   }
   __syncthreads();
-  r.e = lds[8];
-  r.lo = lds[9];
-  r.cnt = r.e < 0 ? 0 : lds[10];
+  // the same in every lane: keep them in scalar registers
+  r.e = __builtin_amdgcn_readfirstlane(lds[8]);
+  r.lo = __builtin_amdgcn_readfirstlane(lds[9]);
+  r.cnt = __builtin_amdgcn_readfirstlane(lds[10]);
+  r.part = __builtin_amdgcn_readfirstlane(lds[11]);
   return r;
 }
 

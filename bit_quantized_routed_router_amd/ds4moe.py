@@ -255,11 +255,17 @@ def _tens(t, what: str):
     it is, None as NULL)."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: tensors must be contiguous and on the GPU")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what}: tensor on device {t.get_device()}, current device {torch.cuda.current_device()}")
+    if not t.is_contiguous() or not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{what}: tensors must be contiguous and on the current GPU")
     return t.data_ptr()
+
+
+def _queue(stream):
+    """The stream's handle; the current stream's without building the Stream
+    object that torch.cuda.current_stream() returns (0.2 us against 2.8)."""
+    if stream is None and torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _stream(stream)
 
 
 def norm_workspace_bytes(desc: NormDesc, T: int) -> int:
@@ -268,27 +274,27 @@ def norm_workspace_bytes(desc: NormDesc, T: int) -> int:
 
 def norm_pre(desc, h, h_dtype, T, x, x_dtype, stream=None) -> None:
     n = "ds4moe_norm_pre"
-    _check(lib().ds4moe_norm_pre(ctypes.byref(desc), _tens(h, n), h_dtype, T, _tens(x, n), x_dtype, _stream(stream)), n)
+    _check(lib().ds4moe_norm_pre(ctypes.byref(desc), _tens(h, n), h_dtype, T, _tens(x, n), x_dtype, _queue(stream)), n)
 
 
 def norm_post(desc, h, h_dtype, y, y_dtype, gate, T, h_out, x_next, x_dtype, stream=None) -> None:
     n = "ds4moe_norm_post"
     _check(lib().ds4moe_norm_post(ctypes.byref(desc), _tens(h, n), h_dtype, _tens(y, n), y_dtype, _tens(gate, n), T,
-                                  _tens(h_out, n), _tens(x_next, n), x_dtype, _stream(stream)), n)
+                                  _tens(h_out, n), _tens(x_next, n), x_dtype, _queue(stream)), n)
 
 
 def norm_pre_grad(desc, h, h_dtype, dx, x_dtype, dh_out, T, dh, dw_pre, ws, ws_bytes, stream=None) -> None:
     n = "ds4moe_norm_pre_grad"
     _check(lib().ds4moe_norm_pre_grad(ctypes.byref(desc), _tens(h, n), h_dtype, _tens(dx, n), x_dtype,
                                       _tens(dh_out, n), T, _tens(dh, n), _tens(dw_pre, n), _tens(ws, n), ws_bytes,
-                                      _stream(stream)), n)
+                                      _queue(stream)), n)
 
 
 def norm_post_grad(desc, dh_out, h_dtype, y, y_dtype, gate, T, dy, dw_post, dgate, ws, ws_bytes, stream=None) -> None:
     n = "ds4moe_norm_post_grad"
     _check(lib().ds4moe_norm_post_grad(ctypes.byref(desc), _tens(dh_out, n), h_dtype, _tens(y, n), y_dtype,
                                        _tens(gate, n), T, _tens(dy, n), _tens(dw_post, n), _tens(dgate, n),
-                                       _tens(ws, n), ws_bytes, _stream(stream)), n)
+                                       _tens(ws, n), ws_bytes, _queue(stream)), n)
 
 
 class Norm:
@@ -318,49 +324,49 @@ def group_workspace_bytes(T: int, k: int, n_experts: int) -> int:
 def group(topk_idx, T, k, n_experts, counts, offsets, perm, inv, ws, ws_bytes, stream=None) -> None:
     n = "ds4moe_group"
     _check(lib().ds4moe_group(_tens(topk_idx, n), T, k, n_experts, _tens(counts, n), _tens(offsets, n), _tens(perm, n),
-                              _tens(inv, n), _tens(ws, n), ws_bytes, _stream(stream)), n)
+                              _tens(inv, n), _tens(ws, n), ws_bytes, _queue(stream)), n)
 
 
 def dispatch(x, x_dtype, T, k, d, inv, xs, n_rows, stream=None) -> None:
     n = "ds4moe_dispatch"
-    _check(lib().ds4moe_dispatch(_tens(x, n), x_dtype, T, k, d, _tens(inv, n), _tens(xs, n), n_rows, _stream(stream)),
+    _check(lib().ds4moe_dispatch(_tens(x, n), x_dtype, T, k, d, _tens(inv, n), _tens(xs, n), n_rows, _queue(stream)),
            n)
 
 
 def combine(ys, ys_dtype, n_rows, inv, topk_w, base, T, k, d, y, y_dtype, stream=None) -> None:
     n = "ds4moe_combine"
     _check(lib().ds4moe_combine(_tens(ys, n), ys_dtype, n_rows, _tens(inv, n), _tens(topk_w, n), _tens(base, n), T, k,
-                                d, _tens(y, n), y_dtype, _stream(stream)), n)
+                                d, _tens(y, n), y_dtype, _queue(stream)), n)
 
 
 def combine_grad(dy, y_dtype, ys, ys_dtype, n_rows, inv, topk_w, T, k, d, dys, dw, dlogits, stream=None) -> None:
     n = "ds4moe_combine_grad"
     _check(lib().ds4moe_combine_grad(_tens(dy, n), y_dtype, _tens(ys, n), ys_dtype, n_rows, _tens(inv, n),
                                      _tens(topk_w, n), T, k, d, _tens(dys, n), _tens(dw, n), _tens(dlogits, n),
-                                     _stream(stream)), n)
+                                     _queue(stream)), n)
 
 
 def mx_quantize(x, x_dtype, T, inv, k, n_rows, cols, packed, stream=None) -> None:
     n = "ds4moe_mx_quantize"
     _check(lib().ds4moe_mx_quantize(_tens(x, n), x_dtype, T, _tens(inv, n), k, n_rows, cols, _tens(packed, n),
-                                    _stream(stream)), n)
+                                    _queue(stream)), n)
 
 
 def mx_dequantize(packed, n_rows, cols, out, out_dtype, stream=None) -> None:
     n = "ds4moe_mx_dequantize"
-    _check(lib().ds4moe_mx_dequantize(_tens(packed, n), n_rows, cols, _tens(out, n), out_dtype, _stream(stream)), n)
+    _check(lib().ds4moe_mx_dequantize(_tens(packed, n), n_rows, cols, _tens(out, n), out_dtype, _queue(stream)), n)
 
 
 def mx_product(a, n_rows, cols, w, w_up, rows, n_experts, offsets, y, y_dtype, stream=None) -> None:
     n = "ds4moe_mx_product"
     _check(lib().ds4moe_mx_product(_tens(a, n), n_rows, cols, _tens(w, n), _tens(w_up, n), rows, n_experts,
-                                   _tens(offsets, n), _tens(y, n), y_dtype, _stream(stream)), n)
+                                   _tens(offsets, n), _tens(y, n), y_dtype, _queue(stream)), n)
 
 
 def mx_product_grad(dy, dy_dtype, n_rows, rows, w, cols, n_experts, offsets, da, da_dtype, stream=None) -> None:
     n = "ds4moe_mx_product_grad"
     _check(lib().ds4moe_mx_product_grad(_tens(dy, n), dy_dtype, n_rows, rows, _tens(w, n), cols, n_experts,
-                                        _tens(offsets, n), _tens(da, n), da_dtype, _stream(stream)), n)
+                                        _tens(offsets, n), _tens(da, n), da_dtype, _queue(stream)), n)
 
 
 def trace_enable(on: bool) -> None:
