@@ -35,265 +35,329 @@ __device__ inline float4_t mfma_mx(u32x4_t a, u32x4_t b, float4_t c, uint32_t sa
 // quotient, which the output's rounding or the sum's own error covers.
 __device__ inline float silu_rcp(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+template <int SEL>
+__device__ inline float16_t mfma_mx32(u32x4_t a, u32x4_t b, float16_t c, uint32_t sa, uint32_t sb) {
+  const i32x8_t av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8_t bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, SEL, (int)sa, SEL, (int)sb);
+}
+
+// Bytes of LDS in which a wave turns 32 rows of NOW outputs.
+template <int NOW, bool BF>
+constexpr int turn_bytes() {
+  return 32 * (NOW * (BF ? 2 : 4) + 16);
+}
+// Stores a wave's 32 rows (p0 onward of the tile) by 32 NF / (GLU ? 2 : 1)
+// outputs (r0 onward): the accumulators leave four neighbouring outputs in a
+// lane, so the wave turns them through its share of LDS and stores whole runs
+// of each row.  GLU: the fragments' first half is gate, the second up.
+template <int NF, bool GLU, bool BF>
+__device__ __attribute__((always_inline)) inline void store_tile(const float16_t (&acc)[NF], uint8_t* turn,
+                                                                 const RowTile& rt, int p0, int r0, int rows,
+                                                                 int lane, void* y) {
+  constexpr int NO = GLU ? NF / 2 : NF, ES = BF ? 2 : 4, RB = 32 * NO * ES, PITCH = RB + 16;
+  const int c = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int f = 0; f < NO; ++f)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float4_t o;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        o[v] = acc[f][4 * g + v];
+        if constexpr (GLU) o[v] = silu_rcp(o[v]) * acc[f + NO][4 * g + v];
+      }
+      uint8_t* at = turn + c * PITCH + (32 * f + 8 * g + 4 * h) * ES;
+      if constexpr (BF)
+        *(u32x2_t*)at = u32x2_t{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+      else
+        *(float4_t*)at = o;
+    }
+  __builtin_amdgcn_wave_barrier();
+  constexpr int LPR = RB / 16;  // lanes of a row
+#pragma unroll
+  for (int x = 0; x < 32 * LPR / 64; ++x) {
+    const int row = x * (64 / LPR) + lane / LPR, ch = lane % LPR;
+    const int p = p0 + row, r = r0 + ch * (16 / ES);
+    const u32x4_t v = *(const u32x4_t*)(turn + row * PITCH + ch * 16);
+    if (p < rt.cnt && r < rows) *(u32x4_t*)((uint8_t*)y + ((int64_t)(rt.lo + p) * rows + r) * ES) = v;
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------- few rows
-// A block takes 16 outputs of a tile of up to 16 NT rows; its four waves each
-// take every fourth piece of 512 columns and add up through LDS.
-template <int NT, bool GLU, bool BF>
+// A block takes 32 weight rows (GLU: 16 gate and the same 16 up) and a tile
+// of up to 16 rows; its four waves each take a quarter of the columns, a
+// piece of 256 at a time, and add up through LDS.  The weights pass through
+// the wave's own LDS, four pieces in flight, because the lanes of the matrix
+// instruction hold 16 different rows side by side and a load in that order
+// moves 15 bytes a cycle against the copies' 52 (8 lanes to a row).  The few
+// rows themselves are loaded straight into registers.
+constexpr int kRowsAhead = 2;                             // pieces in flight
+constexpr int kRowsWave = kRowsAhead * 4096 + 2 * 1024;  // their codes, scales of two groups of four pieces
+template <bool GLU, bool BF>
 __global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* __restrict__ a, const uint8_t* __restrict__ w,
                                                  const uint8_t* __restrict__ w2, const int32_t* __restrict__ offsets,
                                                  int n, int rows, int cols, int E, void* __restrict__ y) {
-  constexpr int NM = GLU ? 2 : 1;
+  constexpr int NO = GLU ? 16 : 32;
   __shared__ int lds[16];
-  __shared__ float4_t red[3][64][NM * NT];
-  const RowTile rt = find_tile(offsets, E, n, 16 * NT, rows / 16, lds);
+  __shared__ uint8_t smem[4 * kRowsWave];
+  const RowTile rt = find_tile(offsets, E, n, 16, (rows + NO - 1) / NO, lds);
   if (rt.cnt <= 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-  const int r0 = rt.part * 16;
-  const int64_t wb = (int64_t)rt.e * ((int64_t)rows * cols / 32 * 17);
-  const uint8_t* wc[NM];
-  const uint8_t* ws[NM];
-#pragma unroll
-  for (int m = 0; m < NM; ++m) {
-    const uint8_t* base = (m ? w2 : w) + wb;
-    wc[m] = base + (int64_t)(r0 + c) * (cols / 2);
-    ws[m] = base + (int64_t)rows * (cols / 2) + (int64_t)(r0 + c) * (cols / 32);
-  }
-  const uint8_t* ac[NT];
-  const uint8_t* as[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t p = rt.lo + min(16 * i + c, rt.cnt - 1);
-    ac[i] = a + p * (cols / 2);
-    as[i] = a + (int64_t)n * (cols / 2) + p * (cols / 32);
-  }
-  float4_t acc[NM][NT] = {};
-  const int pieces = cols / 512;
-  for (int k = wave; k < pieces; k += 4) {
-    const int oc = k * 256 + q * 16, os = k * 16;
-    u32x4_t wv[NM][4], av[NT][4];
-    u32x2_t wsc[NM][2], asc[NT][2];
-#pragma unroll
-    for (int m = 0; m < NM; ++m) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) wv[m][j] = *(const u32x4_t*)(wc[m] + oc + 64 * j);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) wsc[m][j] = *(const u32x2_t*)(ws[m] + os + 8 * j);
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) av[i][j] = *(const u32x4_t*)(ac[i] + oc + 64 * j);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) asc[i][j] = *(const u32x2_t*)(as[i] + os + 8 * j);
-    }
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[m][i] = mfma_mx(wv[m][j], av[i][j], acc[m][i], wsc[m][j / 2][j & 1] >> (8 * q), asc[i][j / 2][j & 1] >> (8 * q));
-  }
-  if (cols % 512 && wave == pieces % 4) {  // the last 256 columns
-    const int oc = pieces * 256 + q * 16, os = pieces * 16;
-#pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      const u32x2_t sw = *(const u32x2_t*)(ws[m] + os);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const u32x2_t sa = *(const u32x2_t*)(as[i] + os);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[m][i] = mfma_mx(*(const u32x4_t*)(wc[m] + oc + 64 * j), *(const u32x4_t*)(ac[i] + oc + 64 * j), acc[m][i],
-                              sw[j] >> (8 * q), sa[j] >> (8 * q));
-      }
-    }
-  }
-  if (wave > 0) {
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) red[wave - 1][lane][m * NT + i] = acc[m][i];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int v = 0; v < 3; ++v) acc[m][i] += red[v][lane][m * NT + i];
-    if (16 * i + c >= rt.cnt) continue;
-    float4_t o = acc[0][i];
-    if constexpr (GLU) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) o[v] = silu_rcp(o[v]) * acc[1][i][v];
-    }
-    const int64_t at = (int64_t)(rt.lo + 16 * i + c) * rows + r0 + 4 * q;
-    if constexpr (BF)
-      *(u32x2_t*)((uint16_t*)y + at) = u32x2_t{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
-    else
-      *(float4_t*)((float*)y + at) = o;
-  }
-}
-
-// ---------------------------------------------------------------- many rows
-// A block of four waves takes a tile of up to 16 NT rows and 64 NW weight
-// rows (GLU: half of them gate, half up, of the same outputs).  Each wave
-// owns 16 NW weight rows, which come straight into its registers, and all of
-// the tile's rows, which the block shares through LDS (copied there by
-// buffer loads to LDS): a piece of 256 columns at a time, R pieces in the
-// ring.  A row's 128 bytes of a piece are 8 pieces of 16 bytes, XOR-swizzled
-// by row pair so that the 16 rows that a fragment reads cover all banks once.
-template <int NT, int NW, int R, bool GLU, bool BF>
-__device__ __attribute__((always_inline)) inline void mx_tile(const RowTile& rt, uint8_t* smem,
-                                                              const uint8_t* __restrict__ a,
-                                                              const uint8_t* __restrict__ w,
-                                                              const uint8_t* __restrict__ w2, int n, int rows, int cols,
-                                                              void* __restrict__ y) {
-  constexpr int NO = GLU ? NW / 2 : NW;                // fragments of outputs per wave
-  constexpr int CI = (NT + 1) / 2, SI = (NT + 7) / 8;  // copies of codes and scales per thread
-  constexpr int kLoads = 3 * NW + CI + SI;             // vector loads per lane and piece
-  constexpr int kSlot = CI * 4096 + SI * 1024;
-  static_assert((R - 1) * kLoads <= 63, "ring depth");
-  static_assert(!GLU || NW % 2 == 0, "gate and up fragments come in pairs");
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, q = lane >> 4;
-  const int r0 = rt.part * (64 * NO) + wave * (16 * NO);  // the wave's first output
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r0 = rt.part * NO;
   const int64_t mat = (int64_t)rows * cols / 32 * 17;
-  // Offsets within a matrix or a tile of rows fit 32 bits.  Weight rows past
-  // the last are read within the matrix, and past it the buffers give zeros;
-  // they are not stored.
   const __amdgpu_buffer_rsrc_t wr[2] = {buf_rsrc(w + rt.e * mat, (uint32_t)mat),
                                         buf_rsrc((GLU ? w2 : w) + rt.e * mat, (uint32_t)mat)};
   const __amdgpu_buffer_rsrc_t ar = buf_rsrc(a + (int64_t)rt.lo * (cols / 2), (uint32_t)rt.cnt * (cols / 2));
   const __amdgpu_buffer_rsrc_t sr =
       buf_rsrc(a + (int64_t)n * (cols / 2) + (int64_t)rt.lo * (cols / 32), (uint32_t)rt.cnt * (cols / 32));
-  const uint32_t wvo = (uint32_t)c * (cols / 2) + q * 16;
-  const uint32_t wso = (uint32_t)rows * (cols / 2) + (uint32_t)c * (cols / 32);
-  // copies: thread i of copy u fills 16-byte slot s = 256 u + i, which holds
-  // piece (s ^ (row / 2)) & 7 of row s / 8; rows past the tile's read nothing
-  const int prow = tid >> 3;
-  const uint32_t avo = (uint32_t)prow * (cols / 2) + ((tid ^ (prow >> 1)) & 7) * 16;
-  const uint32_t svo = (uint32_t)(tid >> 1) * (cols / 32) + (tid & 1) * 4;
-
-  float4_t acc[NW][NT] = {};
-  u32x4_t W[R][NW][2];
-  u32x2_t S[R][NW];
-
-  const int pieces = cols / 256;
-  auto issue = [&](int k, int u) __attribute__((always_inline)) {
+  // the wave's pieces: k0 .. k1 - 1
+  const int pieces = cols / 256, k0 = pieces * wave / 4, k1 = pieces * (wave + 1) / 4;
+  uint8_t* const wl = smem + wave * kRowsWave;
+  const int prow = lane >> 3;
+  // copies take 8 rows by 128 bytes, swizzled by row pair (rows 8 i + prow)
+  auto copy_codes = [&](int k) __attribute__((always_inline)) {
+    uint8_t* dst = wl + ((k - k0) & (kRowsAhead - 1)) * 4096;
 #pragma unroll
-    for (int f = 0; f < NW; ++f) {
-      const int r = r0 + 16 * (GLU ? f / 2 : f), m = GLU ? f & 1 : 0;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) W[u][f][j] = buf_ld128(wr[m], wvo + 64 * j, r * (cols / 2) + k * 128);
-      S[u][f] = buf_ld64(wr[m], wso, r * (cols / 32) + k * 8);
+    for (int i = 0; i < 4; ++i) {
+      const int m = GLU && i >= 2, r = r0 + 8 * i - 16 * m;
+      const uint32_t vo = (uint32_t)prow * (cols / 2) + (((lane & 7) ^ (4 * i + (prow >> 1))) & 7) * 16;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[m], (__attribute__((address_space(3))) void*)(dst + i * 1024), 16,
+                                               k < k1 ? (int)vo : (int)kOob, r * (cols / 2) + k * 128, 0, 0);
     }
-    uint8_t* dst = smem + u * kSlot + wave * 1024;
-#pragma unroll
-    for (int i = 0; i < CI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (__attribute__((address_space(3))) void*)(dst + i * 4096), 16,
-                                               (int)avo, i * 32 * (cols / 2) + k * 128, 0, 0);
-    dst = smem + u * kSlot + CI * 4096 + wave * 256;
-#pragma unroll
-    for (int i = 0; i < SI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (__attribute__((address_space(3))) void*)(dst + i * 1024), 4,
-                                               (int)svo, i * 128 * (cols / 32) + k * 8, 0, 0);
   };
-  auto compute = [&](int u) __attribute__((always_inline)) {
-    const uint8_t* src = smem + u * kSlot;
+  // scales of four pieces: 32 bytes of each of 32 rows, two lanes to a row
+  auto copy_scales = [&](int k) __attribute__((always_inline)) {
+    uint8_t* dst = wl + kRowsAhead * 4096 + (((k - k0) >> 2) & 1) * 1024;
+    const uint32_t vo = (uint32_t)((lane >> 1) & (GLU ? 15 : 31)) * (cols / 32) + (lane & 1) * 16;
+    const uint32_t so = rows * (cols / 2) + r0 * (cols / 32) + k * 8;
+    const bool on = k < k1;
+    if constexpr (GLU) {  // half of the lanes from each matrix; a copy fills what its active lanes name
+      if (lane < 32)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[0], (__attribute__((address_space(3))) void*)dst, 16,
+                                                 on ? (int)vo : (int)kOob, so, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[1], (__attribute__((address_space(3))) void*)dst, 16,
+                                                 on ? (int)vo : (int)kOob, so, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[0], (__attribute__((address_space(3))) void*)dst, 16,
+                                               on ? (int)vo : (int)kOob, so, 0, 0);
+    }
+  };
+  u32x4_t A[kRowsAhead][2];
+  u32x2_t AS[kRowsAhead];
+  auto load_rows = [&](int k, int u) __attribute__((always_inline)) {  // rows past the tile's: zeros
+    const bool on = c < rt.cnt && k < k1;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint8_t* rp = src + (16 * i + c) * 128;
-      const u32x2_t sa = *(const u32x2_t*)(src + CI * 4096 + (16 * i + c) * 8);
+    for (int j = 0; j < 2; ++j)
+      A[u][j] = buf_ld128(ar, on ? (uint32_t)c * (cols / 2) + q * 16 + 64 * j : kOob, k * 128);
+    AS[u] = buf_ld64(sr, on ? (uint32_t)c * (cols / 32) : kOob, k * 8);
+  };
+  constexpr int kCopies = 4 + 3;  // loads per piece
+  float4_t acc[2] = {};
+  copy_scales(k0);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u32x4_t av = *(const u32x4_t*)(rp + (((4 * j + q) ^ (c >> 1)) * 16));
-        const uint32_t sj = sa[j] >> (8 * q);
+  for (int u = 0; u < kRowsAhead; ++u) {
+    copy_codes(k0 + u);
+    load_rows(k0 + u, u);
+  }
+#pragma unroll 1
+  for (int kb = k0; kb < k1; kb += 4) {
+    // the next group's scales, behind everything that this group waits for
+    copy_scales(kb + 4);
 #pragma unroll
-        for (int f = 0; f < NW; ++f) acc[f][i] = mfma_mx(W[u][f][j], av, acc[f][i], S[u][f][j] >> (8 * q), sj);
+    for (int u = 0; u < 4; ++u) {
+      const int k = kb + u, v = u % kRowsAhead;
+      // past the last piece the rows are zeros and what LDS holds does not count
+      pin();
+      vm_wait<(kRowsAhead - 1) * kCopies + 1>();
+      asm volatile("" ::: "memory");
+      pin();
+      u32x4_t wv[2][2];
+      u32x2_t ws[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int row = 16 * f + c;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          wv[f][j] = *(const u32x4_t*)(wl + v * 4096 + row * 128 + (((4 * j + q) ^ (row >> 1)) & 7) * 16);
+        ws[f] = *(const u32x2_t*)(wl + kRowsAhead * 4096 + (((kb - k0) >> 2) & 1) * 1024 + row * 32 + u * 8);
       }
+      if (k < k1) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) acc[f] = mfma_mx(wv[f][j], A[v][j], acc[f], ws[f][j] >> (8 * q), AS[v][j] >> (8 * q));
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
+      pin();
+      copy_codes(k + kRowsAhead);
+      load_rows(k + kRowsAhead, v);
     }
+  }
+  vm_wait<0>();
+  // sums of the four waves
+  __syncthreads();
+  float4_t(*red)[64][2] = (float4_t(*)[64][2])smem;
+  if (wave > 0) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f) red[wave - 1][lane][f] = acc[f];
+  }
+  __syncthreads();
+  if (wave > 0 || c >= rt.cnt) return;
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int v = 0; v < 3; ++v) acc[f] += red[v][lane][f];
+  const int64_t at = (int64_t)(rt.lo + c) * rows + r0 + 4 * q;
+#pragma unroll
+  for (int f = 0; f < (GLU ? 1 : 2); ++f) {
+    if (r0 + 16 * f >= rows) continue;
+    float4_t o = acc[f];
+    if constexpr (GLU) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) o[v] = silu_rcp(o[v]) * acc[1][v];
+    }
+    if constexpr (BF)
+      *(u32x2_t*)((uint16_t*)y + at + 16 * f) = u32x2_t{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+    else
+      *(float4_t*)((float*)y + at + 16 * f) = o;
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+// A block of four waves takes a tile of up to 64 NT rows and 128 weight rows
+// (GLU: 64 gate and the same 64 up); a wave takes 64 of the weight rows (32
+// of each) and half of the rows.  Both operands pass through LDS, a piece of
+// 256 columns at a time with R pieces in the ring, and their scales two
+// pieces at a time.
+template <int NT>
+constexpr int mid_slot() {
+  return (128 + 64 * NT) * 128;
+}
+template <int NT>
+constexpr int mid_scales() {
+  return (128 + 64 * NT) * 16;
+}
+template <int NT, int R>
+constexpr int mid_lds() {
+  return R * mid_slot<NT>() + 2 * mid_scales<NT>() + 1024;
+}
+template <int NT, int R, bool GLU, bool BF>
+__global__ __launch_bounds__(256, 2) void k_mx_mid(const uint8_t* __restrict__ a, const uint8_t* __restrict__ w,
+                                                   const uint8_t* __restrict__ w2,
+                                                   const int32_t* __restrict__ offsets, int n, int rows, int cols,
+                                                   int E, void* __restrict__ y) {
+  constexpr int BM = 64 * NT, NOB = GLU ? 64 : 128;
+  extern __shared__ uint8_t smem[];
+  __shared__ int lds[16];
+  const RowTile rt = find_tile(offsets, E, n, BM, (rows + NOB - 1) / NOB, lds);
+  if (rt.cnt <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int r0 = rt.part * NOB;
+  const int64_t mat = (int64_t)rows * cols / 32 * 17;
+  const __amdgpu_buffer_rsrc_t wr[2] = {buf_rsrc(w + rt.e * mat, (uint32_t)mat),
+                                        buf_rsrc((GLU ? w2 : w) + rt.e * mat, (uint32_t)mat)};
+  const __amdgpu_buffer_rsrc_t ar = buf_rsrc(a + (int64_t)rt.lo * (cols / 2), (uint32_t)rt.cnt * (cols / 2));
+  const __amdgpu_buffer_rsrc_t sr =
+      buf_rsrc(a + (int64_t)n * (cols / 2) + (int64_t)rt.lo * (cols / 32), (uint32_t)rt.cnt * (cols / 32));
+  const int pieces = cols / 256;
+  // copies of codes: row 32 i + tid / 8, swizzled by row pair
+  const int prow = tid >> 3;
+  const uint32_t cvo = (uint32_t)prow * (cols / 2) + ((tid ^ (prow >> 1)) & 7) * 16;
+  // Copies of scales: waves 0 and 1 take the weights' 128 rows, the next NT
+  // the rows' (64 lanes each); a wave without any reads nothing into a spare
+  // KB, so that all waves count the same loads.
+  uint8_t* const scales = smem + R * mid_slot<NT>();
+  const bool up = GLU && wave == 1, of_w = wave < 2, idle = wave >= 2 + NT;
+  const __amdgpu_buffer_rsrc_t scr = of_w ? wr[up] : sr;
+  const uint32_t scv = idle ? kOob : (uint32_t)lane * (cols / 32);
+  const uint32_t sco = of_w ? (uint32_t)rows * (cols / 2) + (uint32_t)(r0 + (!GLU && wave == 1 ? 64 : 0)) * (cols / 32)
+                            : (uint32_t)(wave - 2) * 64 * (cols / 32);
+  constexpr int kCopies = 4 + 2 * NT;
+  auto issue = [&](int k, int u) __attribute__((always_inline)) {
+    if (!(k & 1)) {
+      uint8_t* dst = idle ? scales + 2 * mid_scales<NT>() : scales + ((k >> 1) & 1) * mid_scales<NT>() + wave * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(scr, (__attribute__((address_space(3))) void*)dst, 16, (int)scv,
+                                               sco + k * 8, 0, 0);
+    }
+    uint8_t* dst = smem + u * mid_slot<NT>() + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = GLU && i >= 2, r = r0 + 32 * i - 64 * m;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[m], (__attribute__((address_space(3))) void*)(dst + i * 4096), 16,
+                                               (int)cvo, r * (cols / 2) + k * 128, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (__attribute__((address_space(3))) void*)(dst + 16384 + i * 4096), 16,
+                                               (int)cvo, 32 * i * (cols / 2) + k * 128, 0, 0);
   };
-  // At each step a wave waits for its own loads of the piece, the barrier
-  // makes everyone's copies visible and shows that all waves are done with
-  // the piece before, whose slot then takes the piece R - 1 ahead.
+  auto wrow = [&](int f) __attribute__((always_inline)) { return GLU ? 64 * f + 32 * wm + c : 64 * wm + 32 * f + c; };
+  const int arow = 32 * NT * wn + c;
+  const bool none = 32 * NT * wn >= rt.cnt;  // no rows for this wave
+  float16_t acc[2][NT] = {};
+  auto compute = [&](int k, int u) __attribute__((always_inline)) {
+    const uint8_t* slot = smem + u * mid_slot<NT>();
+    const uint8_t* sc = scales + ((k >> 1) & 1) * mid_scales<NT>() + (k & 1) * 8;
+    u32x2_t sw[2], sa[NT];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) sw[f] = *(const u32x2_t*)(sc + wrow(f) * 16) >> (8 * h);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sa[i] = *(const u32x2_t*)(sc + 2048 + (arow + 32 * i) * 16) >> (8 * h);
+    auto step = [&](auto J) __attribute__((always_inline)) {
+      constexpr int j = decltype(J)::value;
+      const int ph = ((2 * j + h) ^ ((c >> 1) & 7)) * 16;
+      u32x4_t wv[2], av[NT];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) wv[f] = *(const u32x4_t*)(slot + wrow(f) * 128 + ph);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) av[i] = *(const u32x4_t*)(slot + 16384 + (arow + 32 * i) * 128 + ph);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          acc[f][i] = mfma_mx32<(j & 1) * 2>(wv[f], av[i], acc[f][i], sw[f][j / 2], sa[i][j / 2]);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  };
+  // At each step a wave waits for its own copies of the piece, the barrier
+  // makes everyone's visible and shows that all waves are done with the piece
+  // before, whose slot then takes the piece R - 1 ahead.
 #pragma unroll
   for (int u = 0; u < R - 1; ++u)
     if (u < pieces) issue(u, u);
-  for (int k0 = 0; k0 < pieces; k0 += R) {
-#pragma unroll
-    for (int u = 0; u < R; ++u) {
-      const int k = k0 + u;
-      if (k >= pieces) break;
-      pin();
-      if (k + R - 2 < pieces) vm_wait<(R - 2) * kLoads>();
-      else vm_wait<0>();
-      ring_barrier();
-      pin();
-      if (k + R - 1 < pieces) issue(k + R - 1, (u + R - 1) % R);
-      pin();
-      compute(u);
-    }
+  int u = 0;
+#pragma unroll 1
+  for (int k = 0; k < pieces; ++k) {
+    pin();
+    if (k + R - 2 < pieces) vm_wait<(R - 2) * kCopies>();
+    else vm_wait<0>();
+    ring_barrier();
+    pin();
+    if (k + R - 1 < pieces) issue(k + R - 1, u == 0 ? R - 1 : u - 1);
+    pin();
+    if (!none) compute(k, u);
+    u = u + 1 == R ? 0 : u + 1;
   }
-
+  ring_barrier();
+  constexpr int NOW = GLU ? 32 : 64;
+  static_assert(4 * turn_bytes<NOW, BF>() <= mid_lds<NT, R>(), "the waves' shares fit");
+  if (none) return;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    if (16 * i + c >= rt.cnt) continue;
-    const int64_t at = (int64_t)(rt.lo + 16 * i + c) * rows;
-#pragma unroll
-    for (int f = 0; f < NO; ++f) {
-      const int r = r0 + 16 * f + 4 * q;
-      if (r >= rows) continue;
-      float4_t o = acc[GLU ? 2 * f : f][i];
-      if constexpr (GLU) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) o[v] = silu_rcp(o[v]) * acc[2 * f + 1][i][v];
-      }
-      if constexpr (BF)
-        *(u32x2_t*)((uint16_t*)y + at + r) = u32x2_t{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
-      else
-        *(float4_t*)((float*)y + at + r) = o;
-    }
+    float16_t o[2] = {acc[0][i], acc[1][i]};
+    store_tile<2, GLU, BF>(o, smem + wave * turn_bytes<NOW, BF>(), rt, 32 * NT * wn + 32 * i, r0 + wm * NOW, rows, lane, y);
   }
-}
-
-// Rings are as deep as the registers and LDS of the block's largest form allow.
-constexpr size_t ring_bytes(int nt, int r) { return (size_t)r * ((nt + 1) / 2 * 4096 + (nt + 7) / 8 * 1024); }
-
-template <int NT, int NW, int R, bool GLU, bool BF, int WPE>
-__global__ __launch_bounds__(256, WPE) void k_mx_tiles(const uint8_t* __restrict__ a, const uint8_t* __restrict__ w,
-                                                       const uint8_t* __restrict__ w2,
-                                                       const int32_t* __restrict__ offsets, int n, int rows, int cols,
-                                                       int E, void* __restrict__ y) {
-  constexpr int NO = GLU ? NW / 2 : NW;
-  extern __shared__ uint8_t smem[];
-  __shared__ int lds[16];
-  const RowTile rt = find_tile(offsets, E, n, 16 * NT, (rows + 64 * NO - 1) / (64 * NO), lds);
-  if (rt.cnt <= 0) return;
-  if (NT == 4 && rt.cnt <= 16)
-    mx_tile<1, NW, R, GLU, BF>(rt, smem, a, w, w2, n, rows, cols, y);
-  else if (NT == 4 && rt.cnt <= 32)
-    mx_tile<2, NW, R, GLU, BF>(rt, smem, a, w, w2, n, rows, cols, y);
-  else
-    mx_tile<NT, NW, R, GLU, BF>(rt, smem, a, w, w2, n, rows, cols, y);
-}
-
-template <int NT, int NW, int R, bool GLU, bool BF, int WPE>
-static hipError_t launch_tiles(const MxProduct& p) {
-  constexpr int no = GLU ? NW / 2 : NW;
-  constexpr size_t shmem = ring_bytes(NT, R);
-  const int64_t parts = (p.rows + 64 * no - 1) / (64 * no);
-  const int64_t blocks = parts * max_tiles(p.n, p.E, p.offsets != nullptr, 16 * NT);
-  DS4_LAUNCH((k_mx_tiles<NT, NW, R, GLU, BF, WPE>), dim3((unsigned)blocks), dim3(256), shmem, p.st, p.a, p.w, p.w2,
-             p.offsets, (int)p.n, p.rows, p.cols, p.E, p.out);
-  return hipGetLastError();
-}
-template <int NT, int NW, int R, int WPE>
-static hipError_t tiles(const MxProduct& p) {
-  const bool b16 = p.out_dt == DS4MOE_DT_BF16;
-  if (p.w2) return b16 ? launch_tiles<NT, NW, R, true, true, WPE>(p) : launch_tiles<NT, NW, R, true, false, WPE>(p);
-  return b16 ? launch_tiles<NT, NW, R, false, true, WPE>(p) : launch_tiles<NT, NW, R, false, false, WPE>(p);
 }
 
 // ---------------------------------------------------------------- large tiles
@@ -305,15 +369,6 @@ static hipError_t tiles(const MxProduct& p) {
 // because FP4 products outrun what feeds them: per 256 columns it loads 68 KB
 // for 2048 cycles of products (33 of a CU's 64 bytes a cycle from the L2),
 // and its fragment reads take half of the LDS rate.
-typedef float float16_t __attribute__((ext_vector_type(16)));
-
-template <int SEL>
-__device__ inline float16_t mfma_mx32(u32x4_t a, u32x4_t b, float16_t c, uint32_t sa, uint32_t sb) {
-  const i32x8_t av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const i32x8_t bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, SEL, (int)sa, SEL, (int)sb);
-}
-
 constexpr int kBig = 256;                        // rows, and weight rows, of a block
 constexpr int kBigSlot = 2 * kBig * 128;         // bytes of a piece's codes of both
 constexpr int kBigScales = 2 * kBig * 16;        // bytes of the scales of two pieces
@@ -463,41 +518,12 @@ __global__ __launch_bounds__(256, 1) void k_mx_big(const uint8_t* __restrict__ a
   vm_wait<0>();
   ring_barrier();
 
-  // A wave turns 32 rows of its outputs at a time through its share of LDS,
-  // so that they leave as whole runs of a row.
-  constexpr int NOW = GLU ? 64 : 128, ES = BF ? 2 : 4;  // outputs of a wave, bytes of one
-  constexpr int RB = NOW * ES, PITCH = RB + 16;
-  uint8_t* turn = smem + wave * (32 * PITCH);
-  static_assert(4 * 32 * PITCH <= kBigLds, "the waves' shares fit");
-  const int rw = r0 + wm * NOW;
+  constexpr int NOW = GLU ? 64 : 128;
+  static_assert(4 * turn_bytes<NOW, BF>() <= kBigLds, "the waves' shares fit");
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int f = 0; f < NOW / 32; ++f)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float4_t o;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          o[v] = acc[f][i][4 * g + v];
-          if constexpr (GLU) o[v] = silu_rcp(o[v]) * acc[f + 2][i][4 * g + v];
-        }
-        uint8_t* at = turn + c * PITCH + (32 * f + 8 * g + 4 * h) * ES;
-        if constexpr (BF)
-          *(u32x2_t*)at = u32x2_t{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
-        else
-          *(float4_t*)at = o;
-      }
-    __builtin_amdgcn_wave_barrier();
-    constexpr int LPR = RB / 16;  // lanes of a row
-#pragma unroll
-    for (int x = 0; x < 32 * LPR / 64; ++x) {
-      const int row = x * (64 / LPR) + lane / LPR, ch = lane % LPR;
-      const int p = wn * 128 + 32 * i + row, r = rw + ch * (16 / ES);
-      const u32x4_t v = *(const u32x4_t*)(turn + row * PITCH + ch * 16);
-      if (p < rt.cnt && r < rows) *(u32x4_t*)((uint8_t*)y + ((int64_t)(rt.lo + p) * rows + r) * ES) = v;
-    }
-    __builtin_amdgcn_wave_barrier();
+    float16_t o[4] = {acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+    store_tile<4, GLU, BF>(o, smem + wave * turn_bytes<NOW, BF>(), rt, wn * 128 + 32 * i, r0 + wm * NOW, rows, lane, y);
   }
 }
 
@@ -510,22 +536,54 @@ static hipError_t launch_big(const MxProduct& p) {
   return hipGetLastError();
 }
 
-hipError_t launch_mx_product(const MxProduct& p) {
-  if (p.n >= 256 * (int64_t)p.E) {
-    if (p.w2) return p.out_dt == DS4MOE_DT_BF16 ? launch_big<true, true>(p) : launch_big<true, false>(p);
-    return p.out_dt == DS4MOE_DT_BF16 ? launch_big<false, true>(p) : launch_big<false, false>(p);
-  }
-  if (p.n > 16 * (int64_t)p.E) return tiles<4, 2, 3, 2>(p);
-  const bool glu = p.w2 != nullptr, b16 = p.out_dt == DS4MOE_DT_BF16;
-  const dim3 grid((unsigned)(p.rows / 16 * max_tiles(p.n, p.E, p.offsets != nullptr, 16)));
-#define DS4_MXROWS(NT, GLU, BF)                                                                                      \
-  DS4_LAUNCH((k_mx_rows<NT, GLU, BF>), grid, dim3(256), 0, p.st, p.a, p.w, p.w2, p.offsets, (int)p.n, p.rows, p.cols, \
-             p.E, p.out)
-  if (glu && b16) DS4_MXROWS(1, true, true);
-  else if (glu) DS4_MXROWS(1, true, false);
-  else if (b16) DS4_MXROWS(1, false, true);
-  else DS4_MXROWS(1, false, false);
+template <bool GLU, bool BF>
+static hipError_t launch_rows(const MxProduct& p) {
+  const int no = GLU ? 16 : 32;
+  const int64_t blocks = (p.rows + no - 1) / no * max_tiles(p.n, p.E, p.offsets != nullptr, 16);
+  DS4_LAUNCH((k_mx_rows<GLU, BF>), dim3((unsigned)blocks), dim3(256), 0, p.st, p.a, p.w, p.w2, p.offsets, (int)p.n,
+             p.rows, p.cols, p.E, p.out);
   return hipGetLastError();
+}
+template <int NT, int R, bool GLU, bool BF>
+static hipError_t launch_mid(const MxProduct& p) {
+  const int nob = GLU ? 64 : 128;
+  const int64_t blocks = (p.rows + nob - 1) / nob * max_tiles(p.n, p.E, p.offsets != nullptr, 64 * NT);
+  DS4_LAUNCH((k_mx_mid<NT, R, GLU, BF>), dim3((unsigned)blocks), dim3(256), (mid_lds<NT, R>()), p.st, p.a, p.w, p.w2,
+             p.offsets, (int)p.n, p.rows, p.cols, p.E, p.out);
+  return hipGetLastError();
+}
+
+// Which form: by the blocks that each would have (the experts' last, partly
+// filled tiles counted as a half each) and the rows an expert has on average.
+// Times of 4096 x 4096 weights on one expert, in us: rows / 64-row / 128-row /
+// 256-row tiles.
+//   few rows   while its blocks fit the chip at once (four on each of 256
+//              CUs): 32 rows 6.6 / 11.7 / 13.3 / 26.6, 128 rows 13.7 / 12.2
+//   256 rows   when its blocks, one to a CU, fill at least 3/4 of their last
+//              round: 4096 rows (256 blocks) 63 / 50 / 40, 2000 rows (128
+//              blocks) 32 / 26.6 / 32.5
+//   128 rows   with rows to fill the tiles and more 64-row blocks than two to
+//              a CU: 1500 rows 27.9 / 22.7, 600 rows (320 blocks) 14.6 / 15.7;
+//              256 experts with 48 rows each 277 / 284
+template <bool GLU, bool BF>
+static hipError_t product(const MxProduct& p) {
+  constexpr int kCus = 256;
+  const int64_t E = p.offsets ? p.E : 1, mean = p.n / E;
+  auto blocks = [&](int64_t outputs, int64_t bm) {
+    return (p.rows + outputs - 1) / outputs * std::max<int64_t>(1, p.n / bm + (E > 1 ? E / 2 : p.n % bm != 0));
+  };
+  constexpr int g = GLU ? 2 : 1;  // weight rows per output
+  if ((p.rows + 32 / g - 1) / (32 / g) * max_tiles(p.n, p.E, p.offsets != nullptr, 16) <= 4 * kCus)
+    return launch_rows<GLU, BF>(p);
+  const int64_t big = blocks(kBig / g, kBig);
+  if (mean >= 192 && 4 * big >= 3 * ((big + kCus - 1) / kCus * kCus)) return launch_big<GLU, BF>(p);
+  if (mean >= 96 && blocks(128 / g, 64) > 2 * kCus) return launch_mid<2, 2, GLU, BF>(p);
+  return launch_mid<1, 3, GLU, BF>(p);
+}
+hipError_t launch_mx_product(const MxProduct& p) {
+  const bool b16 = p.out_dt == DS4MOE_DT_BF16;
+  if (p.w2) return b16 ? product<true, true>(p) : product<true, false>(p);
+  return b16 ? product<false, true>(p) : product<false, false>(p);
 }
 
 }  // namespace ds4
