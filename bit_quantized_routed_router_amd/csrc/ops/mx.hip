@@ -81,16 +81,20 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t* __restrict
   if (i >= n8) return;
   const uint32_t w = ((const uint32_t*)codes)[i];
   const uint32_t sc = scales[i / 4];
-  const float s = sc == 255u ? __builtin_nanf("") : pow2_scale(sc);
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t c = (w >> (4 * e)) & 15u;
-    // magnitude: exponent field 0 holds 0 and 0.5, else (1 + m / 2) 2^(e - 1)
-    const uint32_t x2 = (c >> 1) & 3u, m1 = c & 1u;
-    const float mag = x2 ? __builtin_bit_cast(float, ((x2 + 126u) << 23) | (m1 << 22)) : 0.5f * (float)m1;
-    v[e] = (c & 8u ? -mag : mag) * s;
+  // the conversion takes the exponent field as an E8M0 code: 0 is 2^-127, 255 NaN
+  const float s = __builtin_bit_cast(float, sc << 23);
+  if constexpr (BF) {
+    u32x4_t o;
+    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+    o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+    o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+    ((u32x4_t*)out)[i] = o;
+    return;
   }
+  const float2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
+  const float2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
+  const float v[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
   st8<BF>(out, i * 8, v);
 }
 

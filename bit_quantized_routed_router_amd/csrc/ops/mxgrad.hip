@@ -14,6 +14,13 @@
 // are read in.  16-byte pieces are XOR-swizzled so that both the writes (a
 // column step of 8 between lanes) and the reads (16 neighbouring columns)
 // spread over the banks.
+//
+// 2001 rows over 32 experts of 2048 x 4096: 97 us, 1.7 TB/s of the bytes that
+// it needs (a copy moves 4.5) and 0.35 PFLOP/s.  What bounds it is the chain
+// of a step within a block (load, decode, LDS, barrier, products) with two
+// blocks to a CU.  Tried and left: one LDS slot and three blocks (98 us),
+// codes through LDS copies (98 us), decode beside the products of the same
+// wave with one block (153 us).
 #include "../trace.h"
 #include "ops.h"
 #include "rowtile.h"
@@ -33,9 +40,10 @@ __device__ inline float4_t mfma_bf16(u32x4_t a, u32x4_t b, float4_t c) {
 __device__ inline int swz_w(int c, int piece) { return c * 8 + (piece ^ ((c ^ (c >> 3)) & 7)); }
 __device__ inline int swz_a(int p, int piece) { return p * 8 + (piece ^ (p & 7)); }
 
-// the 8 elements of a code word as four bfloat16 pairs
+// The 8 elements of a code word as four bfloat16 pairs.  The instruction takes
+// the scale's exponent field as an E8M0 code: 0 is 2^-127, 255 NaN.
 __device__ inline u32x4_t mx_bf16(uint32_t w, uint32_t sc) {
-  const float s = sc == 255u ? __builtin_nanf("") : __builtin_bit_cast(float, sc ? sc << 23 : 0x00400000u);
+  const float s = __builtin_bit_cast(float, sc << 23);
   u32x4_t r;
   r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
   r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
@@ -60,60 +68,68 @@ __device__ inline void split3(float x, uint32_t (&h)[3]) {
   h[2] = __builtin_bit_cast(uint32_t, r2) >> 16;
 }
 
-// BM: rows of a tile (16 or 64); PARTS: 1 (bfloat16 dY) or 3 (fp32 dY)
-template <int BM, int PARTS, bool OB>
-__global__ __launch_bounds__(256) void k_mx_grad(const void* __restrict__ dy, const uint8_t* __restrict__ w,
-                                                 const int32_t* __restrict__ offsets, int n, int rows, int cols,
-                                                 int E, void* __restrict__ out) {
-  constexpr int NF = BM / 16;
-  __shared__ int lds[16];
-  __shared__ u32x4_t ws[kGradBN * 8];
-  __shared__ u32x4_t as[PARTS][BM * 8];
-  const int nc = cols / kGradBN;
-  const RowTile rt = find_tile(offsets, E, n, BM, nc, lds);
-  if (rt.cnt <= 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, q = lane >> 4;
-  const int c0 = rt.part * kGradBN;
-  const int rg = tid >> 5, cw = tid & 31;
-  const uint8_t* wb = w + (int64_t)rt.e * ((int64_t)rows * cols / 32 * 17);
-  const uint8_t* wcode = wb + (c0 + 8 * cw) / 2;
-  const uint8_t* wscale = wb + (int64_t)rows * (cols / 2) + (c0 + 8 * cw) / 32;
-  float4_t acc[4][NF] = {};
-  for (int r0 = 0; r0 < rows; r0 += kGradKC) {
-    uint32_t cd[8], sc[8];
+// Bytes of LDS of one step: the weights, then the parts of the rows.
+constexpr int grad_slot(int nf, int parts) { return kGradBN * 128 + parts * nf * 16 * 128; }
+
+// One tile of up to 16 NF rows.  PARTS: 1 (bfloat16 dY) or 3 (fp32 dY).
+// Two steps take turns in LDS: while one is multiplied the next is on its
+// way into registers, from which it is decoded into the other.
+template <int NF, int PARTS, bool OB>
+__device__ __attribute__((always_inline)) inline void grad_tile(const RowTile& rt, uint8_t* smem,
+                                                                const void* __restrict__ dy,
+                                                                const uint8_t* __restrict__ w, int rows, int cols,
+                                                                void* __restrict__ out) {
+  constexpr int BM = 16 * NF, AP = (BM * 8 + 255) / 256;  // 16-byte pieces of the rows per thread
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c0 = rt.part * kGradBN, rg = tid >> 5, cw = tid & 31;
+  const int64_t mat = (int64_t)rows * cols / 32 * 17;
+  const __amdgpu_buffer_rsrc_t wr = buf_rsrc(w + rt.e * mat, (uint32_t)mat);
+  const uint32_t wo = (uint32_t)(8 * rg) * (cols / 2) + 4 * cw, so = (uint32_t)(8 * rg) * (cols / 32) + cw / 4;
+  uint32_t cd[8], sc[8];
+  Raw8<PARTS == 1> av[AP];
+  auto load = [&](int r0) __attribute__((always_inline)) {
+    // rows is a multiple of 16, so a thread's eight weight rows are all there
+    // or none is; none reads as zeros
+    const bool on = r0 + 8 * rg < rows;
+    const uint32_t vo = on ? wo : kOob, vs = on ? so : kOob;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // rows is a multiple of 16, so eight rows are all there or none is
-      const int64_t r = min(r0 + 8 * rg, rows - 8) + i;
-      cd[i] = *(const uint32_t*)(wcode + r * (cols / 2));
-      sc[i] = wscale[r * (cols / 32)];
+    for (int i = 0; i < 8; ++i) {
+      cd[i] = buf_ld32(wr, vo, (r0 + i) * (cols / 2) + c0 / 2);
+      sc[i] = (uint32_t)__builtin_bit_cast(
+          uint8_t, __builtin_amdgcn_raw_buffer_load_b8(wr, (int)vs, rows * (cols / 2) + (r0 + i) * (cols / 32) + c0 / 32, 0));
     }
-    const bool past = r0 + 8 * rg >= rows;
-    __syncthreads();  // the previous step's reads are done
-    {
-      u32x4_t col[8];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const u32x4_t a = mx_bf16(cd[i], sc[i]), b = mx_bf16(cd[i + 1], sc[i + 1]);
+    for (int i = 0; i < AP; ++i) {
+      const int p = (tid + 256 * i) >> 3, r = r0 + 8 * (tid & 7);
+      av[i] = Raw8<PARTS == 1>{};
+      if (p < rt.cnt && r < rows) av[i] = ld8<PARTS == 1>(dy, (int64_t)(rt.lo + p) * rows + r);
+    }
+  };
+  auto store = [&](uint8_t* slot) __attribute__((always_inline)) {
+    u32x4_t* ws = (u32x4_t*)slot;
+    u32x4_t* as = ws + kGradBN * 8;
+    u32x4_t col[8];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          col[2 * p][i / 2] = past ? 0u : __builtin_amdgcn_perm(b[p], a[p], 0x05040100u);
-          col[2 * p + 1][i / 2] = past ? 0u : __builtin_amdgcn_perm(b[p], a[p], 0x07060302u);
-        }
+    for (int i = 0; i < 8; i += 2) {
+      const u32x4_t a = mx_bf16(cd[i], sc[i]), b = mx_bf16(cd[i + 1], sc[i + 1]);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        col[2 * p][i / 2] = __builtin_amdgcn_perm(b[p], a[p], 0x05040100u);
+        col[2 * p + 1][i / 2] = __builtin_amdgcn_perm(b[p], a[p], 0x07060302u);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ws[swz_w(8 * cw + j, rg)] = col[j];
     }
-    for (int i = tid; i < BM * 8; i += 256) {
-      const int p = i >> 3, piece = i & 7;
-      const int r = r0 + 8 * piece;
-      const int64_t at = (int64_t)(rt.lo + min(p, rt.cnt - 1)) * rows + r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ws[swz_w(8 * cw + j, rg)] = col[j];
+#pragma unroll
+    for (int i = 0; i < AP; ++i) {
+      const int p = (tid + 256 * i) >> 3, piece = tid & 7;
+      if (p >= BM) break;
       if constexpr (PARTS == 1) {
-        u32x4_t v = {0u, 0u, 0u, 0u};
-        if (r < rows) v = *(const u32x4_t*)((const uint16_t*)dy + at);
-        as[0][swz_a(p, piece)] = v;
+        as[swz_a(p, piece)] = av[i].a;
       } else {
-        float v[8] = {};
-        if (r < rows) unpack8(ld8<false>(dy, at), v);
+        float v[8];
+        unpack8(av[i], v);
         u32x4_t o[3];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -124,10 +140,21 @@ __global__ __launch_bounds__(256) void k_mx_grad(const void* __restrict__ dy, co
           for (int s = 0; s < 3; ++s) o[s][e / 2] = x[s] | (y[s] << 16);
         }
 #pragma unroll
-        for (int s = 0; s < 3; ++s) as[s][swz_a(p, piece)] = o[s];
+        for (int s = 0; s < 3; ++s) as[s * BM * 8 + swz_a(p, piece)] = o[s];
       }
     }
-    __syncthreads();
+  };
+  float4_t acc[4][NF] = {};
+  load(0);
+  store(smem);
+  __syncthreads();
+  int slot = 0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += kGradKC) {
+    load(r0 + kGradKC);
+    pin();
+    const u32x4_t* ws = (const u32x4_t*)(smem + slot);
+    const u32x4_t* as = ws + kGradBN * 8;
 #pragma unroll
     for (int kk = 0; kk < kGradKC / 32; ++kk) {
       u32x4_t wf[4];
@@ -137,11 +164,15 @@ __global__ __launch_bounds__(256) void k_mx_grad(const void* __restrict__ dy, co
       for (int s = PARTS - 1; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
-          const u32x4_t af = as[s][swz_a(16 * i + c, 4 * kk + q)];
+          const u32x4_t af = as[s * BM * 8 + swz_a(16 * i + c, 4 * kk + q)];
 #pragma unroll
           for (int f = 0; f < 4; ++f) acc[f][i] = mfma_bf16(wf[f], af, acc[f][i]);
         }
     }
+    pin();
+    slot ^= grad_slot(NF, PARTS);
+    if (r0 + kGradKC < rows) store(smem + slot);
+    __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < NF; ++i) {
@@ -158,23 +189,36 @@ __global__ __launch_bounds__(256) void k_mx_grad(const void* __restrict__ dy, co
   }
 }
 
-hipError_t launch_mx_product_grad(const MxProduct& p) {
-  const bool f32 = p.dy_dt == DS4MOE_DT_F32, ob = p.out_dt == DS4MOE_DT_BF16;
-  const int bm = p.n > 16 * (int64_t)p.E ? 64 : 16;
-  const dim3 grid((unsigned)(p.cols / kGradBN * max_tiles(p.n, p.E, p.offsets != nullptr, bm)));
-#define DS4_MXGRAD(BM, PARTS, OB)                                                                                 \
-  DS4_LAUNCH((k_mx_grad<BM, PARTS, OB>), grid, dim3(256), 0, p.st, p.dy, p.w, p.offsets, (int)p.n, p.rows, p.cols, \
-             p.E, p.out)
-#define DS4_MXGRAD_T(BM)                      \
-  do {                                        \
-    if (f32 && ob) DS4_MXGRAD(BM, 3, true);   \
-    else if (f32) DS4_MXGRAD(BM, 3, false);   \
-    else if (ob) DS4_MXGRAD(BM, 1, true);     \
-    else DS4_MXGRAD(BM, 1, false);            \
-  } while (0)
-  if (bm == 64) DS4_MXGRAD_T(64);
-  else DS4_MXGRAD_T(16);
+template <int NF, int PARTS, bool OB>
+__global__ __launch_bounds__(256, 2) void k_mx_grad(const void* __restrict__ dy, const uint8_t* __restrict__ w,
+                                                    const int32_t* __restrict__ offsets, int n, int rows, int cols,
+                                                    int E, void* __restrict__ out) {
+  extern __shared__ uint8_t smem[];  // two slots of 40 KB: exactly two blocks to a CU
+  const RowTile rt = find_tile(offsets, E, n, 16 * NF, cols / kGradBN, (int*)smem);
+  if (rt.cnt <= 0) return;
+  __syncthreads();  // everyone has read the tile
+  if (NF > 1 && rt.cnt <= 16)
+    grad_tile<1, PARTS, OB>(rt, smem, dy, w, rows, cols, out);
+  else
+    grad_tile<NF, PARTS, OB>(rt, smem, dy, w, rows, cols, out);
+}
+
+template <int NF, int PARTS, bool OB>
+static hipError_t launch_grad(const MxProduct& p) {
+  const int64_t blocks = p.cols / kGradBN * max_tiles(p.n, p.E, p.offsets != nullptr, 16 * NF);
+  DS4_LAUNCH((k_mx_grad<NF, PARTS, OB>), dim3((unsigned)blocks), dim3(256), 2 * grad_slot(NF, PARTS), p.st, p.dy, p.w,
+             p.offsets, (int)p.n, p.rows, p.cols, p.E, p.out);
   return hipGetLastError();
+}
+template <int NF>
+static hipError_t grad(const MxProduct& p) {
+  const bool ob = p.out_dt == DS4MOE_DT_BF16;
+  if (p.dy_dt == DS4MOE_DT_F32) return ob ? launch_grad<NF, 3, true>(p) : launch_grad<NF, 3, false>(p);
+  return ob ? launch_grad<NF, 1, true>(p) : launch_grad<NF, 1, false>(p);
+}
+
+hipError_t launch_mx_product_grad(const MxProduct& p) {
+  return p.n > 16 * (int64_t)p.E ? grad<4>(p) : grad<1>(p);
 }
 
 }  // namespace ds4
