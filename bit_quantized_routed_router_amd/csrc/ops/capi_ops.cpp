@@ -27,7 +27,7 @@ static int check_gate(const ds4moe_norm* N, const float* gate) {
   if ((N->gate != DS4MOE_GATE_NONE) != (gate != nullptr)) return DS4MOE_EINVAL;
   return al(gate, N->gate == DS4MOE_GATE_TOKEN ? 4 : 16) ? DS4MOE_OK : DS4MOE_EALIGN;
 }
-static size_t norm_ws(const ds4moe_norm& N, int64_t T) { return (size_t)2 * norm_parts(T) * N.d_model * sizeof(float); }
+static size_t norm_ws(const ds4moe_norm& N, int64_t T) { return (size_t)2 * norm_parts(N.d_model, T) * N.d_model * sizeof(float); }
 static int check_norm_ws(const ds4moe_norm& N, int64_t T, const void* ws, size_t ws_bytes) {
   if (!ws) return DS4MOE_EINVAL;
   if (!al(ws, 256)) return DS4MOE_EALIGN;

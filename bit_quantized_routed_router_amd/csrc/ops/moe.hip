@@ -56,32 +56,37 @@ __device__ inline int block_scan(int v, int* tmp, int* total) {
   return before + x - v;
 }
 
-// A chunk of slots per block, a contiguous run of 64 * PER of them per wave.
-constexpr int kSortPer = 8;
-constexpr int kSortT = 512;
-constexpr int kSortWaves = kSortT / 64;
-constexpr int kSortChunk = kSortT * kSortPer;
-
 __device__ inline int expert_key(const int32_t* idx, int64_t s, int64_t S, int E) {
   if (s >= S) return -1;
   const int e = idx[s];
   return e >= 0 && e < E ? e : E;
 }
 
+// Slots that one block sorts by itself, with one wave or sixteen, and those
+// of a chunk when there are more.
+constexpr int kSortWaveT = 64, kSortWavePer = 8;
+constexpr int kSortBlockT = 1024, kSortBlockPer = 4;
+constexpr int kSortChunkT = 512, kSortChunkPer = 4;
+constexpr int kSortChunk = kSortChunkT * kSortChunkPer;
+constexpr int kSortFew = 32;  // chunks up to which each block adds up the ones before it itself
+// where k_group_place has the slots of earlier chunks from: there are none,
+// the chunks' counters, or those already scanned
+enum { kSortOne = 0, kSortCounted = 1, kSortScanned = 2 };
+
 // Slots of every expert in each chunk: hist[chunk][E].
-__global__ __launch_bounds__(kSortT) void k_group_hist(const int32_t* __restrict__ idx, int64_t S, int E,
-                                                       int32_t* __restrict__ hist) {
+__global__ __launch_bounds__(kSortChunkT) void k_group_hist(const int32_t* __restrict__ idx, int64_t S, int E,
+                                                            int32_t* __restrict__ hist) {
   __shared__ int cnt[kMaxE + 1];
-  for (int e = threadIdx.x; e <= E; e += kSortT) cnt[e] = 0;
+  for (int e = threadIdx.x; e <= E; e += kSortChunkT) cnt[e] = 0;
   __syncthreads();
   const int64_t s0 = (int64_t)blockIdx.x * kSortChunk;
 #pragma unroll
-  for (int u = 0; u < kSortPer; ++u) {
-    const int key = expert_key(idx, s0 + u * kSortT + threadIdx.x, S, E);
+  for (int u = 0; u < kSortChunkPer; ++u) {
+    const int key = expert_key(idx, s0 + u * kSortChunkT + threadIdx.x, S, E);
     if (key >= 0) atomicAdd(&cnt[key], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kSortT) hist[(int64_t)blockIdx.x * E + e] = cnt[e];
+  for (int e = threadIdx.x; e < E; e += kSortChunkT) hist[(int64_t)blockIdx.x * E + e] = cnt[e];
 }
 
 // hist -> slots of the expert in earlier chunks; counts.  A block takes 16
@@ -114,116 +119,147 @@ __global__ __launch_bounds__(256) void k_group_scan(int32_t* __restrict__ hist, 
   }
 }
 
-// Positions of the block's chunk of slots.  The chunk's slots are ranked
-// stably: each wave counts its own run, the waves' counts are added up in
-// order, and each wave then goes through its run again, 64 slots at a time,
-// a slot's rank among equal keys being the count of lower lanes that hold
-// the same key.  ONE: there is only this chunk, and counts come from here.
-// LDS holds kSortWaves counters per expert.
-template <bool ONE>
-__global__ __launch_bounds__(kSortT) void k_group_place(const int32_t* __restrict__ idx, int64_t S, int E, int bits,
-                                                        const int32_t* __restrict__ hist,
-                                                        int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
-                                                        int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
+// Positions of the block's slots, stable.  Each wave takes a contiguous run,
+// 64 slots at a time in order: the lanes with a key find each other by
+// ballots, their first one adds their number to the wave's counter of the key
+// and so learns how many of the run came before.  The counters are then added
+// up over the waves and scanned over the experts, and a slot's position is
+// its wave's start for the key plus its place in the run.  Dynamic LDS: a
+// counter per wave and expert.
+template <int NT, int PER, int FROM>
+__global__ __launch_bounds__(NT) void k_group_place(const int32_t* __restrict__ idx, int64_t S, int E, int bits,
+                                                    const int32_t* __restrict__ hist, int chunks,
+                                                    int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+                                                    int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
+  constexpr int NW = NT / 64, EP = kMaxE / NT > 0 ? kMaxE / NT : 1;  // experts of a thread in the scan
   extern __shared__ int lds[];
-  __shared__ int tmp[kSortWaves];
+  __shared__ int tmp[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t s0 = (int64_t)blockIdx.x * kSortChunk + wave * (64 * kSortPer) + lane;
-  for (int i = tid; i < kSortWaves * E; i += kSortT) lds[i] = 0;
-  int key[kSortPer];
+  const int64_t c0 = (int64_t)blockIdx.x * (NT * PER), c1 = min(c0 + NT * PER, S);
+  const int steps = (int)((c1 - c0 + NT - 1) / NT);  // 64 slots of every wave each
+  const int64_t s0 = c0 + wave * (64 * steps) + lane;
+  int key[PER], place[PER];
 #pragma unroll
-  for (int u = 0; u < kSortPer; ++u) key[u] = expert_key(idx, s0 + u * 64, S, E);
-  __syncthreads();
+  for (int u = 0; u < PER; ++u) key[u] = u < steps ? expert_key(idx, s0 + u * 64, c1, E) : -1;
+  // the expert's slots in earlier chunks, and in all
+  int earlier[EP], total[EP];
 #pragma unroll
-  for (int u = 0; u < kSortPer; ++u)
-    if (key[u] >= 0 && key[u] < E) atomicAdd(&lds[wave * E + key[u]], 1);
-  __syncthreads();
-  // a thread takes up to two neighbouring experts: kMaxE == 2 kSortT
-  static_assert(kMaxE == 2 * kSortT, "experts per thread of the scan");
-  int c[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * tid + i;
-    if (e >= E) continue;
-    if (ONE) {
-      int sum = 0;
-      for (int w = 0; w < kSortWaves; ++w) {
-        const int v = lds[w * E + e];
-        lds[w * E + e] = sum;
-        sum += v;
+  for (int i = 0; i < EP; ++i) {
+    const int e = EP * tid + i;
+    earlier[i] = total[i] = 0;
+    if (FROM == kSortScanned && e < E) {
+      earlier[i] = hist[(int64_t)blockIdx.x * E + e];
+      total[i] = counts[e];
+    }
+    if (FROM == kSortCounted && e < E) {
+#pragma unroll 8
+      for (int c = 0; c < chunks; ++c) {
+        const int v = hist[c * E + e];
+        if (c < (int)blockIdx.x) earlier[i] += v;
+        total[i] += v;
       }
-      c[i] = sum;
-      counts[e] = sum;
-    } else {
-      int sum = hist[(int64_t)blockIdx.x * E + e];
-      for (int w = 0; w < kSortWaves; ++w) {
-        const int v = lds[w * E + e];
-        lds[w * E + e] = sum;
-        sum += v;
-      }
-      c[i] = counts[e];
     }
   }
-  int live;
-  const int off = block_scan<kSortT>(c[0] + c[1], tmp, &live);
+  for (int i = tid; i < NW * E; i += NT) lds[i] = 0;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * tid + i, o = off + (i ? c[0] : 0);
-    if (e >= E) continue;
-    for (int w = 0; w < kSortWaves; ++w) lds[w * E + e] += o;
-    if (blockIdx.x == 0) {
-      offsets[e] = o;
-      if (e == E - 1) offsets[E] = o + c[i];
+  for (int u = 0; u < PER; ++u) {
+    if (u < steps) {
+      // lanes past the last slot join those without an expert
+      const uint64_t m = same_key(key[u] < 0 ? E : key[u], bits);
+      const int leader = __ffsll((unsigned long long)m) - 1;
+      int before = 0;
+      if (lane == leader && key[u] >= 0 && key[u] < E) before = atomicAdd(&lds[wave * E + key[u]], __popcll(m));
+      place[u] = __shfl(before, leader) + __popcll(m & ((1ull << lane) - 1));
     }
   }
   __syncthreads();
+  // a thread takes EP neighbouring experts
+  int v[EP][NW], sum = 0;
 #pragma unroll
-  for (int u = 0; u < kSortPer; ++u) {
-    const int64_t s = s0 + u * 64;
-    // keys of lanes past the last slot match nothing that is counted
-    const uint64_t m = same_key(key[u] < 0 ? E : key[u], bits);
-    const int leader = __ffsll((unsigned long long)m) - 1;
-    const bool mine = key[u] >= 0 && key[u] < E;
-    int base = 0;
-    if (mine && lane == leader) base = atomicAdd(&lds[wave * E + key[u]], __popcll(m));
-    base = __shfl(base, leader);
-    if (key[u] < 0) continue;
-    int pos = -1;
-    if (mine) {
-      pos = base + __popcll(m & ((1ull << lane) - 1));
-      perm[pos] = (int)s;
+  for (int i = 0; i < EP; ++i) {
+    const int e = EP * tid + i;
+    if (e < E) {
+      int all = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v[i][w] = lds[w * E + e];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const int x = v[i][w];
+        v[i][w] = all;
+        all += x;
+      }
+      if (FROM == kSortOne) total[i] = all;
+      if (FROM != kSortScanned && blockIdx.x == 0) counts[e] = total[i];
     }
-    inv[s] = pos;
+    sum += total[i];
   }
-  // positions without a slot
+  int live, off = block_scan<NT>(sum, tmp, &live);
 #pragma unroll
-  for (int u = 0; u < kSortPer; ++u) {
+  for (int i = 0; i < EP; ++i) {
+    const int e = EP * tid + i;
+    if (e < E) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) lds[w * E + e] = off + earlier[i] + v[i][w];
+      if (blockIdx.x == 0) {
+        offsets[e] = off;
+        if (e == E - 1) offsets[E] = off + total[i];
+      }
+    }
+    off += total[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
     const int64_t s = s0 + u * 64;
-    if (s < S && s >= live) perm[s] = -1;
+    if (key[u] >= 0) {
+      int pos = -1;
+      if (key[u] < E) {
+        pos = lds[wave * E + key[u]] + place[u];
+        perm[pos] = (int)s;
+      }
+      inv[s] = pos;
+      if (s >= live) perm[s] = -1;  // positions without a slot
+    }
   }
 }
 
 // counters of the chunks, when there is more than one
+static bool sorts_alone(int64_t S) { return S <= kSortBlockT * kSortBlockPer; }
 size_t group_ws_bytes(int64_t S, int E) {
-  const int64_t chunks = (S + kSortChunk - 1) / kSortChunk;
-  return (size_t)((chunks > 1 ? chunks * E * 4 : 0) + 256 + 255) & ~(size_t)255;
+  const int64_t chunks = sorts_alone(S) ? 0 : (S + kSortChunk - 1) / kSortChunk;
+  return (size_t)(chunks * E * 4 + 256 + 255) & ~(size_t)255;
 }
 
+// 256 experts, kernel times: 96 slots GW us with one wave; 4084 slots of 64
+// experts GB with sixteen; 12288 slots GC in two launches (one block of
+// sixteen waves: 21.8, bound by its one CU).
 hipError_t launch_group(const int32_t* idx, int64_t S, int E, int32_t* counts, int32_t* offsets, int32_t* perm,
                         int32_t* inv, int32_t* ws, hipStream_t st) {
-  const int chunks = (int)((S + kSortChunk - 1) / kSortChunk);
   int bits = 0;
   while ((1 << bits) <= E) ++bits;
-  const size_t shmem = (size_t)kSortWaves * E * 4;
-  if (chunks == 1) {
-    DS4_LAUNCH(k_group_place<true>, dim3(1), dim3(kSortT), shmem, st, idx, S, E, bits, (const int32_t*)nullptr, counts,
-               offsets, perm, inv);
+  const int32_t* none = nullptr;
+  if (S <= kSortWaveT * kSortWavePer) {
+    DS4_LAUNCH((k_group_place<kSortWaveT, kSortWavePer, kSortOne>), dim3(1), dim3(kSortWaveT), (size_t)E * 4, st, idx, S,
+               E, bits, none, 1, counts, offsets, perm, inv);
     return hipGetLastError();
   }
-  DS4_LAUNCH(k_group_hist, dim3(chunks), dim3(kSortT), 0, st, idx, S, E, ws);
+  if (sorts_alone(S)) {
+    DS4_LAUNCH((k_group_place<kSortBlockT, kSortBlockPer, kSortOne>), dim3(1), dim3(kSortBlockT),
+               (size_t)(kSortBlockT / 64) * E * 4, st, idx, S, E, bits, none, 1, counts, offsets, perm, inv);
+    return hipGetLastError();
+  }
+  const int chunks = (int)((S + kSortChunk - 1) / kSortChunk);
+  const size_t shmem = (size_t)(kSortChunkT / 64) * E * 4;
+  DS4_LAUNCH(k_group_hist, dim3(chunks), dim3(kSortChunkT), 0, st, idx, S, E, ws);
+  if (chunks <= kSortFew) {
+    DS4_LAUNCH((k_group_place<kSortChunkT, kSortChunkPer, kSortCounted>), dim3(chunks), dim3(kSortChunkT), shmem, st, idx,
+               S, E, bits, (const int32_t*)ws, chunks, counts, offsets, perm, inv);
+    return hipGetLastError();
+  }
   DS4_LAUNCH(k_group_scan, dim3((E + 15) / 16), dim3(256), 0, st, ws, chunks, E, counts);
-  DS4_LAUNCH(k_group_place<false>, dim3(chunks), dim3(kSortT), shmem, st, idx, S, E, bits, (const int32_t*)ws, counts,
-             offsets, perm, inv);
+  DS4_LAUNCH((k_group_place<kSortChunkT, kSortChunkPer, kSortScanned>), dim3(chunks), dim3(kSortChunkT), shmem, st, idx,
+             S, E, bits, (const int32_t*)ws, chunks, counts, offsets, perm, inv);
   return hipGetLastError();
 }
 

@@ -108,7 +108,7 @@ struct NormCall {
   float *dw, *dgate, *part;
   hipStream_t st;
 };
-int norm_parts(int64_t T);  // partial rows of the gradients summed over tokens
+int norm_parts(int d, int64_t T);  // partial rows of the gradients summed over tokens
 hipError_t launch_norm_pre(const NormCall& c);
 hipError_t launch_norm_post(const NormCall& c);
 hipError_t launch_norm_pre_grad(const NormCall& c);
