@@ -10,7 +10,10 @@
 // A slot whose expert lies outside [0, E) has no position: inv is -1, its
 // weight and rows are never read, and its gradients are zero.  The row
 // kernels go by token, so a token's row is read once for all its slots, and
-// no sum depends on the order in which blocks run.
+// no sum depends on the order in which blocks run.  They are bound by memory:
+// 2048 tokens of 4096, 6 slots each: dispatch 117 MB in 21 us (5.5 TB/s),
+// combine 168 MB in 30 us (5.6 TB/s); combine_grad in fp32 (1021 tokens of
+// 2048, 4 slots) 72 MB in 12.6 us (5.7 TB/s).  A large copy moves 4.5 TB/s.
 #include <algorithm>
 
 #include "../trace.h"
@@ -231,9 +234,10 @@ size_t group_ws_bytes(int64_t S, int E) {
   return (size_t)(chunks * E * 4 + 256 + 255) & ~(size_t)255;
 }
 
-// 256 experts, kernel times: 96 slots GW us with one wave; 4084 slots of 64
-// experts GB with sixteen; 12288 slots GC in two launches (one block of
-// sixteen waves: 21.8, bound by its one CU).
+// Kernel times: 96 slots of 256 experts 4.9 us with one wave (7.4 with eight);
+// 4084 slots of 64 experts 7.5 us with sixteen; 12288 slots of 256 experts 4.7
+// + 8.3 us in two launches (one block of sixteen waves: 21.8, bound by its one
+// CU; scanning in a launch of its own: 17 in three).
 hipError_t launch_group(const int32_t* idx, int64_t S, int E, int32_t* counts, int32_t* offsets, int32_t* perm,
                         int32_t* inv, int32_t* ws, hipStream_t st) {
   int bits = 0;

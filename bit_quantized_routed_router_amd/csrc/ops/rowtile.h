@@ -30,14 +30,25 @@ __device__ inline void split_item(int local, int m, int parts, int& tile, int& p
 // tile.  Blocks are dealt to the 8 XCDs in turn; here each XCD takes a
 // contiguous run of the items there are, in which a few parts' weights meet
 // all tiles of their expert before the next parts', so that what runs
-// together shares both through the XCD's L2.  lds: 16 ints.
+// together shares both through the XCD's L2.  Items are counted in 64 bits:
+// runs of bad offsets may overlap and add up to more than the rows have.
+__device__ inline bool block_item(int64_t count, int64_t& item) {
+  const int b = blockIdx.x, x = b & 7, i = b >> 3;
+  const int64_t base = count >> 3;
+  const int rem = (int)(count & 7);
+  item = x * base + min(x, rem) + i;
+  return b < count;
+}
+
+// lds: 16 ints.
 __device__ inline RowTile find_tile(const int32_t* offsets, int E, int n, int bm, int parts, int* lds) {
   RowTile r{0, 0, 0, 0};
-  int item, t;
+  int64_t item;
+  int t;
   if (!offsets) {
     const int m = (n + bm - 1) / bm;
-    if (!xcd_item(m * parts, item)) return r;
-    split_item(item, m, parts, t, r.part);
+    if (!block_item((int64_t)m * parts, item)) return r;
+    split_item((int)item, m, parts, t, r.part);
     r.lo = t * bm;
     r.cnt = min(bm, n - r.lo);
     return r;
@@ -63,22 +74,23 @@ __device__ inline RowTile find_tile(const int32_t* offsets, int E, int n, int bm
     if (w < wave) first += lds[w];
     total += lds[w];
   }
-  if (!xcd_item(total * parts, item)) return r;
-  if (item >= first * parts && item < (first + tiles) * parts) {
-    int left = item - first * parts;
+  if (!block_item((int64_t)total * parts, item)) return r;
+  const int64_t mine = item - (int64_t)first * parts;  // from this thread's first tile on
+  if (mine >= 0 && mine < (int64_t)tiles * parts) {
+    int64_t left = mine;
     for (int i = 0; i < per; ++i) {
       const int lo = min(max(offsets[e0 + i], 0), n), hi = min(max(offsets[e0 + i + 1], 0), n);
       const int m = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-      if (left < m * parts) {
+      if (left < (int64_t)m * parts) {
         int part;
-        split_item(left, m, parts, t, part);
+        split_item((int)left, m, parts, t, part);
         lds[8] = e0 + i;
         lds[9] = lo + t * bm;
         lds[10] = min(bm, hi - lo - t * bm);
         lds[11] = part;
         break;
       }
-      left -= m * parts;
+      left -= (int64_t)m * parts;
     }
   }
   __syncthreads();

@@ -324,7 +324,8 @@ int ds4moe_hc_post(const ds4moe_hc *H, const float *X, const float *y, const flo
  * (|h| and |y| below 2^56).  Non-finite values stay within their row, but for the
  * gradients summed over tokens.  A gate of zero does not hide a non-finite y.
  * All tensors are contiguous; device pointers 16-byte aligned, a gate per
- * token and its gradient 4-byte aligned.  1 <= T <= 1048576.
+ * token and its gradient 4-byte aligned.  1 <= T <= 1048576.  Here and in
+ * the calls below no buffers overlap but where a call says so.
  * ---------------------------------------------------------------------- */
 /* what the gate g holds a value for: nothing (g = 1), each token [T], each
  * channel [d], each element [T][d] */
