@@ -4,15 +4,23 @@
 //   y[p][r] = sum_c A[p][c] W_e[r][c]        rows p of expert e
 //   y[p][r] = silu(g) u                      g, u: the products with two matrices
 //
-// v_mfma_scale_f32_16x16x128_f8f6f4 with both operands in FP4: lane l holds
-// row (l & 15) and the block of 32 number q = l >> 4 of a step's 128 columns
-// (16 bytes), and its scale code in the low byte of a register; the products
-// and the scales are exact and the sum is fp32.  A step's loads cover 64
-// consecutive bytes of each of 16 rows.  The scale codes of a row's four
-// steps (512 columns, a piece) are read as four words, of which each lane
-// shifts down the byte of its block.
-// The weights are the first operand, so a lane ends with four neighbouring
-// outputs 4 q .. 4 q + 3 of one row p = l & 15.
+// v_mfma_scale_f32_16x16x128_f8f6f4 (few rows) and _32x32x64_ (the rest) with
+// both operands in FP4: a lane holds one row and one block of 32 columns of a
+// step, 16 bytes, and the block's scale code in a byte of a register; the
+// products and the scales are exact and the sum is fp32.  A row's scale codes
+// are read as whole words, of which each lane shifts down the bytes of its
+// blocks.  The weights are the first operand, so a lane ends with runs of four
+// neighbouring outputs of one row.
+//
+// The lanes hold different rows side by side, and loads in that order move 15
+// bytes a cycle and CU (hot in the L2), against 52 for copies into LDS with
+// eight lanes to a row: so everything but a few rows goes through LDS, its 16
+// byte pieces XOR-swizzled by row pair.
+//
+// Measured: 6 rows of 256 experts, gate and up, 53 MB in 11.6 us (4.6 TB/s);
+// 12288 rows of 256 experts, down, 1.36 GB in 280 us (4.8 TB/s: bound by
+// reading the weights, a large copy moves 4.5); 4001 rows of one expert, gate
+// and up 4096 x 4096, 77 us (3.5 PFLOP/s).
 #include <algorithm>
 #include <type_traits>
 

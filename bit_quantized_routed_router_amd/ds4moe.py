@@ -246,26 +246,29 @@ class Hc:
 
 
 # ---------------------------------------------------------------- operators around the layer
-# Norms, tokens sorted by expert and back, MXFP4 rows and products.  Tensors
-# here are checked to be contiguous and on the current device, since the
-# library sees bare addresses.
+# Norms, tokens sorted by expert and back, MXFP4 rows and products: thin calls
+# of the C functions of the same names.  Tensors here are checked to be
+# contiguous and on the current device, since the library sees bare addresses
+# (an int is taken as an address, None as NULL).
 
-def _tens(t, what: str):
-    """Address of a contiguous tensor on the current device (an int passes as
-    it is, None as NULL)."""
-    if t is None or isinstance(t, int):
-        return t
-    if not t.is_contiguous() or not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{what}: tensors must be contiguous and on the current GPU")
-    return t.data_ptr()
-
-
-def _queue(stream):
-    """The stream's handle; the current stream's without building the Stream
-    object that torch.cuda.current_stream() returns (0.2 us against 2.8)."""
-    if stream is None and torch.cuda.is_initialized():
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return _stream(stream)
+def _call(name: str, stream, *args) -> None:
+    """Run a C function: tensors as their addresses, the stream last.  The
+    current stream's handle is taken without building the Stream object that
+    torch.cuda.current_stream() returns (0.2 us against 2.8)."""
+    L = lib()
+    gpu = torch.cuda.is_initialized()
+    dev = torch._C._cuda_getDevice() if gpu else 0
+    flat = []
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            if a.get_device() != dev or not a.is_contiguous():
+                raise ValueError(f"{name}: tensors must be contiguous and on the current GPU")
+            a = a.data_ptr()
+        flat.append(a)
+    flat.append(torch._C._cuda_getCurrentRawStream(dev) if stream is None and gpu else _stream(stream))
+    status = getattr(L, name)(*flat)
+    if status != OK:
+        raise Ds4moeError(status, name)
 
 
 def norm_workspace_bytes(desc: NormDesc, T: int) -> int:
@@ -273,28 +276,21 @@ def norm_workspace_bytes(desc: NormDesc, T: int) -> int:
 
 
 def norm_pre(desc, h, h_dtype, T, x, x_dtype, stream=None) -> None:
-    n = "ds4moe_norm_pre"
-    _check(lib().ds4moe_norm_pre(ctypes.byref(desc), _tens(h, n), h_dtype, T, _tens(x, n), x_dtype, _queue(stream)), n)
+    _call("ds4moe_norm_pre", stream, ctypes.byref(desc), h, h_dtype, T, x, x_dtype)
 
 
 def norm_post(desc, h, h_dtype, y, y_dtype, gate, T, h_out, x_next, x_dtype, stream=None) -> None:
-    n = "ds4moe_norm_post"
-    _check(lib().ds4moe_norm_post(ctypes.byref(desc), _tens(h, n), h_dtype, _tens(y, n), y_dtype, _tens(gate, n), T,
-                                  _tens(h_out, n), _tens(x_next, n), x_dtype, _queue(stream)), n)
+    _call("ds4moe_norm_post", stream, ctypes.byref(desc), h, h_dtype, y, y_dtype, gate, T, h_out, x_next, x_dtype)
 
 
 def norm_pre_grad(desc, h, h_dtype, dx, x_dtype, dh_out, T, dh, dw_pre, ws, ws_bytes, stream=None) -> None:
-    n = "ds4moe_norm_pre_grad"
-    _check(lib().ds4moe_norm_pre_grad(ctypes.byref(desc), _tens(h, n), h_dtype, _tens(dx, n), x_dtype,
-                                      _tens(dh_out, n), T, _tens(dh, n), _tens(dw_pre, n), _tens(ws, n), ws_bytes,
-                                      _queue(stream)), n)
+    _call("ds4moe_norm_pre_grad", stream, ctypes.byref(desc), h, h_dtype, dx, x_dtype, dh_out, T, dh, dw_pre, ws,
+          ws_bytes)
 
 
 def norm_post_grad(desc, dh_out, h_dtype, y, y_dtype, gate, T, dy, dw_post, dgate, ws, ws_bytes, stream=None) -> None:
-    n = "ds4moe_norm_post_grad"
-    _check(lib().ds4moe_norm_post_grad(ctypes.byref(desc), _tens(dh_out, n), h_dtype, _tens(y, n), y_dtype,
-                                       _tens(gate, n), T, _tens(dy, n), _tens(dw_post, n), _tens(dgate, n),
-                                       _tens(ws, n), ws_bytes, _queue(stream)), n)
+    _call("ds4moe_norm_post_grad", stream, ctypes.byref(desc), dh_out, h_dtype, y, y_dtype, gate, T, dy, dw_post, dgate,
+          ws, ws_bytes)
 
 
 class Norm:
@@ -304,11 +300,10 @@ class Norm:
     def __init__(self, d, eps=1e-6, res_scale=1.0, gate=GATE_NONE, w_pre=None, w_post=None, w_next=None):
         self.tensors = dict(w_pre=w_pre, w_post=w_post, w_next=w_next)
         for name, w in self.tensors.items():
-            if w is not None and (w.dtype != torch.float32 or w.numel() != d):
-                raise ValueError(f"{name}: expected {d} float32 values")
+            if w is not None and (w.dtype != torch.float32 or w.numel() != d or not w.is_cuda or not w.is_contiguous()):
+                raise ValueError(f"{name}: expected {d} contiguous float32 values on the GPU")
         self.d = d
-        p = [_tens(w, "Norm") for w in (w_pre, w_post, w_next)]
-        self.desc = NormDesc(d, float(eps), float(res_scale), gate, *p)
+        self.desc = NormDesc(d, float(eps), float(res_scale), gate, _ptr(w_pre), _ptr(w_post), _ptr(w_next))
 
     def workspace(self, T: int):
         n = norm_workspace_bytes(self.desc, T)
@@ -322,51 +317,35 @@ def group_workspace_bytes(T: int, k: int, n_experts: int) -> int:
 
 
 def group(topk_idx, T, k, n_experts, counts, offsets, perm, inv, ws, ws_bytes, stream=None) -> None:
-    n = "ds4moe_group"
-    _check(lib().ds4moe_group(_tens(topk_idx, n), T, k, n_experts, _tens(counts, n), _tens(offsets, n), _tens(perm, n),
-                              _tens(inv, n), _tens(ws, n), ws_bytes, _queue(stream)), n)
+    _call("ds4moe_group", stream, topk_idx, T, k, n_experts, counts, offsets, perm, inv, ws, ws_bytes)
 
 
 def dispatch(x, x_dtype, T, k, d, inv, xs, n_rows, stream=None) -> None:
-    n = "ds4moe_dispatch"
-    _check(lib().ds4moe_dispatch(_tens(x, n), x_dtype, T, k, d, _tens(inv, n), _tens(xs, n), n_rows, _queue(stream)),
-           n)
+    _call("ds4moe_dispatch", stream, x, x_dtype, T, k, d, inv, xs, n_rows)
 
 
 def combine(ys, ys_dtype, n_rows, inv, topk_w, base, T, k, d, y, y_dtype, stream=None) -> None:
-    n = "ds4moe_combine"
-    _check(lib().ds4moe_combine(_tens(ys, n), ys_dtype, n_rows, _tens(inv, n), _tens(topk_w, n), _tens(base, n), T, k,
-                                d, _tens(y, n), y_dtype, _queue(stream)), n)
+    _call("ds4moe_combine", stream, ys, ys_dtype, n_rows, inv, topk_w, base, T, k, d, y, y_dtype)
 
 
 def combine_grad(dy, y_dtype, ys, ys_dtype, n_rows, inv, topk_w, T, k, d, dys, dw, dlogits, stream=None) -> None:
-    n = "ds4moe_combine_grad"
-    _check(lib().ds4moe_combine_grad(_tens(dy, n), y_dtype, _tens(ys, n), ys_dtype, n_rows, _tens(inv, n),
-                                     _tens(topk_w, n), T, k, d, _tens(dys, n), _tens(dw, n), _tens(dlogits, n),
-                                     _queue(stream)), n)
+    _call("ds4moe_combine_grad", stream, dy, y_dtype, ys, ys_dtype, n_rows, inv, topk_w, T, k, d, dys, dw, dlogits)
 
 
 def mx_quantize(x, x_dtype, T, inv, k, n_rows, cols, packed, stream=None) -> None:
-    n = "ds4moe_mx_quantize"
-    _check(lib().ds4moe_mx_quantize(_tens(x, n), x_dtype, T, _tens(inv, n), k, n_rows, cols, _tens(packed, n),
-                                    _queue(stream)), n)
+    _call("ds4moe_mx_quantize", stream, x, x_dtype, T, inv, k, n_rows, cols, packed)
 
 
 def mx_dequantize(packed, n_rows, cols, out, out_dtype, stream=None) -> None:
-    n = "ds4moe_mx_dequantize"
-    _check(lib().ds4moe_mx_dequantize(_tens(packed, n), n_rows, cols, _tens(out, n), out_dtype, _queue(stream)), n)
+    _call("ds4moe_mx_dequantize", stream, packed, n_rows, cols, out, out_dtype)
 
 
 def mx_product(a, n_rows, cols, w, w_up, rows, n_experts, offsets, y, y_dtype, stream=None) -> None:
-    n = "ds4moe_mx_product"
-    _check(lib().ds4moe_mx_product(_tens(a, n), n_rows, cols, _tens(w, n), _tens(w_up, n), rows, n_experts,
-                                   _tens(offsets, n), _tens(y, n), y_dtype, _queue(stream)), n)
+    _call("ds4moe_mx_product", stream, a, n_rows, cols, w, w_up, rows, n_experts, offsets, y, y_dtype)
 
 
 def mx_product_grad(dy, dy_dtype, n_rows, rows, w, cols, n_experts, offsets, da, da_dtype, stream=None) -> None:
-    n = "ds4moe_mx_product_grad"
-    _check(lib().ds4moe_mx_product_grad(_tens(dy, n), dy_dtype, n_rows, rows, _tens(w, n), cols, n_experts,
-                                        _tens(offsets, n), _tens(da, n), da_dtype, _queue(stream)), n)
+    _call("ds4moe_mx_product_grad", stream, dy, dy_dtype, n_rows, rows, w, cols, n_experts, offsets, da, da_dtype)
 
 
 def trace_enable(on: bool) -> None:
