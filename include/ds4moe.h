@@ -380,7 +380,8 @@ int ds4moe_norm_post_grad(const ds4moe_norm *N, const void *dh_out, int h_dtype,
  * (other formats, adapters, training).  Slots are s = t k + j.  A slot whose
  * expert lies outside [0, n_experts) -- padding, a slot dropped by a capacity
  * -- takes no part: it has no row, its weight is never read and its gradients
- * are zero.  A token may name an expert more than once.  1 <= T <= 1048576,
+ * are zero; nor does a position outside [0, n_rows) have one.  A token may
+ * name an expert more than once.  1 <= T <= 1048576,
  * 1 <= k <= 16, 1 <= n_experts <= 1024; d a multiple of 256, <= 16384; n_rows,
  * the rows of xs and ys, at most 2^24.  Row types: DS4MOE_DT_F32 or _BF16.
  * ---------------------------------------------------------------------- */

@@ -319,3 +319,57 @@ def test_product_grad_extreme_values():
     assert got[2].isnan().all()
     assert not torch.isfinite(got[3]).any()
     assert torch.isfinite(got[[1, 4, 5]]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_product_grad_scale_codes(kind):
+    """Scale codes from 0 (weights down to 2^-128, bfloat16's subnormal numbers)
+    to 220, with dY of a size that brings every product near one (2^120 at
+    most, and down to 2^-95, where an fp32 value's three parts are all normal);
+    a block marked NaN makes its 32 columns NaN and no others."""
+    n, rows, cols = 24, 224, 512
+    b = Back(n, rows, cols, kind=kind)
+    half = rows * cols // 2
+    sc = torch.arange(rows).clamp(max=220)[:, None].repeat(1, cols // 32)
+    b.w[half:] = sc.reshape(-1).to(torch.uint8)
+    code = torch.stack([b.w[:half] & 15, b.w[:half] >> 4], 1).reshape(rows, cols).long()
+    b.w64[0] = mx_values(code, sc)
+    b.dy = (b.dy.float().clamp(-3, 3) * torch.exp2((127 - sc[:, 0]).clamp(max=118).float())).to(b.dy.dtype)
+    b.check(offsets=False)
+    b.w.view(torch.uint8)[half + 5 * (cols // 32) + 3] = 255
+    got = b.run(offsets=False).cpu()
+    assert got[:, 96:128].isnan().all()
+    assert torch.isfinite(got[:, :96]).all() and torch.isfinite(got[:, 128:]).all()
+
+
+def test_product_grad_bad_offsets_stay_in_range():
+    n = 40
+    b = Back(n, 48, 256, 6, offsets=[-5, 3, 3, 30, 20, 99, 2 ** 31 - 1])
+    got = b.run().cpu()
+    off = b.offsets.clamp(0, n).tolist()
+    hit = torch.zeros(n, dtype=torch.int)
+    owner = torch.zeros(n, dtype=torch.int)
+    for e in range(6):
+        hit[off[e]:max(off[e], off[e + 1])] += 1
+        owner[off[e]:max(off[e], off[e + 1])] = e
+    for p in range(n):
+        if hit[p] == 0:
+            assert (got[p] == 55).all()
+        elif hit[p] == 1:
+            W = b.w64[int(owner[p])]
+            close(got[p], b.dy[p].double() @ W, b.dy[p].double().abs() @ W.abs(), 2 * 48, f"row {p}")
+
+
+@pytest.mark.parametrize("n,E", [(3000, 1024), (20000, 1024), (9000, 300)])
+def test_product_many_experts(n, E):
+    """Up to 1024 experts (four to a thread in the search for a tile), most of
+    the rows with one of them."""
+    g = gen(n)
+    cut = torch.randint(0, n, (E - 1,), generator=g).sort().values
+    cut[E // 2:] = torch.maximum(cut[E // 2:], torch.tensor(n - E))
+    cut[:E // 2] = cut[:E // 2].clamp(max=E)
+    off = [0] + cut.sort().values.tolist() + [n]
+    p = Product(n, 16, 256, E, offsets=off)
+    p.check(("f32",))
+    b = Back(n, 16, 256, E, offsets=off)
+    b.check(("f32",))
