@@ -204,6 +204,8 @@ __global__ __launch_bounds__(256, PARTS == 3 ? 2 : NF == 2 ? 4 : 3) void k_mx_gr
   __syncthreads();  // everyone has read the tile
   if (rt.cnt <= 16)
     grad_tile<1, PARTS, OB>(rt, smem, dy, w, rows, cols, out);
+  else if (NF > 2 && rt.cnt <= 32)
+    grad_tile<2, PARTS, OB>(rt, smem, dy, w, rows, cols, out);
   else
     grad_tile<NF, PARTS, OB>(rt, smem, dy, w, rows, cols, out);
 }
@@ -215,15 +217,17 @@ static hipError_t launch_grad(const MxProduct& p) {
              p.offsets, (int)p.n, p.rows, p.cols, p.E, p.out);
   return hipGetLastError();
 }
-// Tiles of 32 rows (36 KB, four blocks to a CU), or 64 (40 KB, three) where an
-// expert has rows for them on average, so that a decoded weight serves twice
-// as many: 2001 rows over 32 experts 87 / 96 us, 4000 rows of one 121 / 96.
-// fp32 dY: 32 rows (44 KB, three blocks), 138 us on the first; 16 or 64 take
-// 167 and 182.
+// Tiles of 32 rows (36 KB, four blocks to a CU), or of 64 (40 KB, three; 32 or
+// 16 where a tile has no more) so that a decoded weight serves twice as many:
+// where an expert has rows for them on average, or where there are two rounds
+// of them anyway.  2001 rows over 32 experts 88 / 94 us, 12288 rows over 256
+// experts 273 / 245, 4000 rows of one 121 / 96.  fp32 dY: 32 rows (44 KB), 138
+// us on the first; 16 or 64 take 167 and 182.
 hipError_t launch_mx_product_grad(const MxProduct& p) {
   const bool ob = p.out_dt == DS4MOE_DT_BF16;
   if (p.dy_dt == DS4MOE_DT_F32) return ob ? launch_grad<2, 3, true>(p) : launch_grad<2, 3, false>(p);
-  if (p.n < 128 * (int64_t)(p.offsets ? p.E : 1)) return ob ? launch_grad<2, 1, true>(p) : launch_grad<2, 1, false>(p);
+  const int64_t E = p.offsets ? p.E : 1, blocks = (p.n / 64 + E / 2) * (p.cols / kGradBN);
+  if (p.n < 128 * E && blocks <= 2 * 3 * 256) return ob ? launch_grad<2, 1, true>(p) : launch_grad<2, 1, false>(p);
   return ob ? launch_grad<4, 1, true>(p) : launch_grad<4, 1, false>(p);
 }
 

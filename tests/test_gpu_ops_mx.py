@@ -360,6 +360,12 @@ def test_product_grad_bad_offsets_stay_in_range():
             close(got[p], b.dy[p].double() @ W, b.dy[p].double().abs() @ W.abs(), 2 * 48, f"row {p}")
 
 
+@pytest.mark.parametrize("n,rows,cols,E", [(300, 48, 256, 1), (4100, 32, 4096, 40), (2600, 64, 1024, 20)])
+def test_product_grad_every_tile_size(n, rows, cols, E):
+    """Tiles of 32 and of 64 rows, partly filled ones among them."""
+    Back(n, rows, cols, E, 5).check(("bf16",))
+
+
 @pytest.mark.parametrize("n,E", [(3000, 1024), (20000, 1024), (9000, 300)])
 def test_product_many_experts(n, E):
     """Up to 1024 experts (four to a thread in the search for a tile), most of
