@@ -127,14 +127,14 @@ __global__ __launch_bounds__(256) void k_group_scan(int32_t* __restrict__ hist, 
 // ballots, their first one adds their number to the wave's counter of the key
 // and so learns how many of the run came before.  The counters are then added
 // up over the waves and scanned over the experts, and a slot's position is
-// its wave's start for the key plus its place in the run.  Dynamic LDS: a
-// counter per wave and expert.
-template <int NT, int PER, int FROM>
+// its wave's start for the key plus its place in the run.  EP: experts of a
+// thread in the scan.  Dynamic LDS: a counter per wave and expert.
+template <int NT, int PER, int EP, int FROM>
 __global__ __launch_bounds__(NT) void k_group_place(const int32_t* __restrict__ idx, int64_t S, int E, int bits,
                                                     const int32_t* __restrict__ hist, int chunks,
                                                     int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                     int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
-  constexpr int NW = NT / 64, EP = kMaxE / NT > 0 ? kMaxE / NT : 1;  // experts of a thread in the scan
+  constexpr int NW = NT / 64;
   extern __shared__ int lds[];
   __shared__ int tmp[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -242,28 +242,27 @@ hipError_t launch_group(const int32_t* idx, int64_t S, int E, int32_t* counts, i
                         int32_t* inv, int32_t* ws, hipStream_t st) {
   int bits = 0;
   while ((1 << bits) <= E) ++bits;
-  const int32_t* none = nullptr;
+#define DS4_PLACE(NT, PER, EP, FROM, blocks, hist, chunks)                                                     \
+  DS4_LAUNCH((k_group_place<NT, PER, EP, FROM>), dim3(blocks), dim3(NT), (size_t)(NT / 64) * E * 4, st, idx, S, E, \
+             bits, (const int32_t*)(hist), chunks, counts, offsets, perm, inv)
   if (S <= kSortWaveT * kSortWavePer) {
-    DS4_LAUNCH((k_group_place<kSortWaveT, kSortWavePer, kSortOne>), dim3(1), dim3(kSortWaveT), (size_t)E * 4, st, idx, S,
-               E, bits, none, 1, counts, offsets, perm, inv);
+    if (E <= 4 * kSortWaveT) DS4_PLACE(kSortWaveT, kSortWavePer, 4, kSortOne, 1, nullptr, 1);
+    else DS4_PLACE(kSortWaveT, kSortWavePer, kMaxE / kSortWaveT, kSortOne, 1, nullptr, 1);
     return hipGetLastError();
   }
   if (sorts_alone(S)) {
-    DS4_LAUNCH((k_group_place<kSortBlockT, kSortBlockPer, kSortOne>), dim3(1), dim3(kSortBlockT),
-               (size_t)(kSortBlockT / 64) * E * 4, st, idx, S, E, bits, none, 1, counts, offsets, perm, inv);
+    DS4_PLACE(kSortBlockT, kSortBlockPer, kMaxE / kSortBlockT, kSortOne, 1, nullptr, 1);
     return hipGetLastError();
   }
   const int chunks = (int)((S + kSortChunk - 1) / kSortChunk);
-  const size_t shmem = (size_t)(kSortChunkT / 64) * E * 4;
   DS4_LAUNCH(k_group_hist, dim3(chunks), dim3(kSortChunkT), 0, st, idx, S, E, ws);
   if (chunks <= kSortFew) {
-    DS4_LAUNCH((k_group_place<kSortChunkT, kSortChunkPer, kSortCounted>), dim3(chunks), dim3(kSortChunkT), shmem, st, idx,
-               S, E, bits, (const int32_t*)ws, chunks, counts, offsets, perm, inv);
+    DS4_PLACE(kSortChunkT, kSortChunkPer, kMaxE / kSortChunkT, kSortCounted, chunks, ws, chunks);
     return hipGetLastError();
   }
   DS4_LAUNCH(k_group_scan, dim3((E + 15) / 16), dim3(256), 0, st, ws, chunks, E, counts);
-  DS4_LAUNCH((k_group_place<kSortChunkT, kSortChunkPer, kSortScanned>), dim3(chunks), dim3(kSortChunkT), shmem, st, idx,
-             S, E, bits, (const int32_t*)ws, chunks, counts, offsets, perm, inv);
+  DS4_PLACE(kSortChunkT, kSortChunkPer, kMaxE / kSortChunkT, kSortScanned, chunks, ws, chunks);
+#undef DS4_PLACE
   return hipGetLastError();
 }
 
@@ -274,11 +273,12 @@ __global__ __launch_bounds__(256) void k_dispatch(const void* __restrict__ x, co
                                                   int d, int nb, int rows, void* __restrict__ xs) {
   const int64_t t = blockIdx.x / nb;
   const int c = ((blockIdx.x % nb) * 256 + threadIdx.x) * 8;
-  if (c >= d) return;
+  const int pos = slot_positions(inv, t, k, rows);
+  if (c >= d) return;  // (whole waves or their upper lanes, so lanes 0 .. 15 stay: d is a multiple of 256)
   const Raw8<BF> v = ld8<BF>(x, t * d + c);
   for (int j = 0; j < k; ++j) {
-    const int p = inv[t * k + j];
-    if (p < 0 || p >= rows) continue;
+    const int p = __builtin_amdgcn_readlane(pos, j);
+    if (p < 0) continue;
     if constexpr (BF) {
       *(u32x4_t*)((uint16_t*)xs + (int64_t)p * d + c) = v.a;
     } else {
@@ -289,38 +289,37 @@ __global__ __launch_bounds__(256) void k_dispatch(const void* __restrict__ x, co
   }
 }
 
-// Loads of up to four slots' rows are in flight at once.
+// The rows of up to eight slots are in flight at once.
 template <bool SB, bool YB>
 __global__ __launch_bounds__(256) void k_combine_rows(const void* __restrict__ ys, const int32_t* __restrict__ inv,
                                                       const float* __restrict__ w, const void* base, int k, int d,
                                                       int nb, int rows, void* y) {
+  constexpr int B = 8;
   const int64_t t = blockIdx.x / nb;
   const int c = ((blockIdx.x % nb) * 256 + threadIdx.x) * 8;
+  const int pos = slot_positions(inv, t, k, rows);
+  float weight = 1.0f;
+  if (w && pos >= 0) weight = w[t * k + min((int)(threadIdx.x & 63), k - 1)];
   if (c >= d) return;
   float acc[8] = {};
   if (base) unpack8(ld8<YB>(base, t * d + c), acc);
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    Raw8<SB> v[4];
-    float wj[4];
-    bool on[4];
+  for (int j0 = 0; j0 < k; j0 += B) {
+    Raw8<SB> v[B];
+    bool on[B];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = min(j0 + u, k - 1);
-      const int p = inv[t * k + j];
-      on[u] = j0 + u < k && p >= 0 && p < rows;
-      wj[u] = 1.0f;
-      if (on[u]) {
-        v[u] = ld8<SB>(ys, (int64_t)p * d + c);
-        if (w) wj[u] = w[t * k + j];
-      }
+    for (int u = 0; u < B; ++u) {
+      const int p = __builtin_amdgcn_readlane(pos, min(j0 + u, k - 1));
+      on[u] = j0 + u < k && p >= 0;
+      if (on[u]) v[u] = ld8<SB>(ys, (int64_t)p * d + c);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < B; ++u) {
       if (!on[u]) continue;
+      const float wj = lane_float(weight, j0 + u);
       float f[8];
       unpack8(v[u], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(wj[u], f[e], acc[e]);
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(wj, f[e], acc[e]);
     }
   }
   st8<YB>(y, t * d + c, acc);

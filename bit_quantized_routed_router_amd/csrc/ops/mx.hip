@@ -47,7 +47,8 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x,
                                                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const int64_t t = blockIdx.x / nb;
   const int c = ((blockIdx.x % nb) * 256 + threadIdx.x) * 8;
-  if (c >= cols) return;  // whole quads: cols is a multiple of 32
+  const int pos = inv ? slot_positions(inv, t, k, rows) : (int)t;
+  if (c >= cols) return;  // whole half waves: cols is a multiple of 256
   const Raw8<BF> v = ld8<BF>(x, t * cols + c);
   uint32_t m = 0;
   float f[8];
@@ -67,8 +68,8 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x,
     w = no_minus_zero(w);
   }
   for (int j = 0; j < k; ++j) {
-    const int64_t p = inv ? inv[t * k + j] : (int)t;
-    if (p < 0 || p >= rows) continue;
+    const int64_t p = __builtin_amdgcn_readlane(pos, j);
+    if (p < 0) continue;
     const int64_t i = p * cols + c;
     *(uint32_t*)(codes + i / 2) = w;
     if ((threadIdx.x & 3) == 0) scales[i / 32] = (uint8_t)sc;

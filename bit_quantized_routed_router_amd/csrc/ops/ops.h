@@ -97,6 +97,19 @@ __device__ inline float wave_sum(float v) {
   return (r0 + r1) + (r2 + r3);
 }
 
+// ---------------------------------------------------------------- a token's slots
+// Lane j holds the position of the token's slot j (k <= 16 of them; -1 for
+// none or one outside [0, rows)): one load for all, read back lane by lane,
+// where a loop of scalar loads would wait for each in turn.
+__device__ inline int slot_positions(const int32_t* inv, int64_t t, int k, int rows) {
+  const int j = min((int)(threadIdx.x & 63), k - 1);
+  const int p = inv[t * k + j];
+  return p >= 0 && p < rows ? p : -1;
+}
+__device__ inline float lane_float(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
 // ---------------------------------------------------------------- launchers
 struct NormCall {
   ds4moe_norm N;
