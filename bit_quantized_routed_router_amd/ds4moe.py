@@ -251,24 +251,34 @@ class Hc:
 # contiguous and on the current device, since the library sees bare addresses
 # (an int is taken as an address, None as NULL).
 
+_Tensor = torch.Tensor
+
+
 def _call(name: str, stream, *args) -> None:
     """Run a C function: tensors as their addresses, the stream last.  The
     current stream's handle is taken without building the Stream object that
     torch.cuda.current_stream() returns (0.2 us against 2.8)."""
-    L = lib()
-    gpu = torch.cuda.is_initialized()
-    dev = torch._C._cuda_getDevice() if gpu else 0
+    dev = _current_gpu()
     flat = []
     for a in args:
-        if isinstance(a, torch.Tensor):
+        if isinstance(a, _Tensor):
             if a.get_device() != dev or not a.is_contiguous():
                 raise ValueError(f"{name}: tensors must be contiguous and on the current GPU")
             a = a.data_ptr()
         flat.append(a)
-    flat.append(torch._C._cuda_getCurrentRawStream(dev) if stream is None and gpu else _stream(stream))
-    status = getattr(L, name)(*flat)
+    flat.append(_stream(stream) if stream is not None or dev < 0 else torch._C._cuda_getCurrentRawStream(dev))
+    status = getattr(_lib or lib(), name)(*flat)
     if status != OK:
         raise Ds4moeError(status, name)
+
+
+def _current_gpu() -> int:
+    """The current device's index; -2, which no tensor has, before anything has used the GPU."""
+    global _current_gpu
+    if not torch.cuda.is_initialized():
+        return -2
+    _current_gpu = torch._C._cuda_getDevice  # from now on without the question
+    return _current_gpu()
 
 
 def norm_workspace_bytes(desc: NormDesc, T: int) -> int:
