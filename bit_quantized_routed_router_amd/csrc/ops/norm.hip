@@ -69,7 +69,7 @@ __device__ inline void ld_gate(const float* g, int mode, int64_t t, int d, int c
 
 // ---------------------------------------------------------------- forward
 // One block of NT threads per row; thread i holds columns 8 (i + s NT) .. + 7
-// for s < NS.  (256 threads and up to 8 steps for every width.)
+// for s < NS.
 template <int NT, int NS, bool HB, bool XB>
 __global__ __launch_bounds__(NT) void k_norm_pre(const void* __restrict__ h, const float* __restrict__ w, int d,
                                                  float eps, void* __restrict__ x) {
@@ -384,27 +384,25 @@ __global__ __launch_bounds__(256) void k_norm_colsum(const float* __restrict__ p
 }
 
 // ---------------------------------------------------------------- launchers
-// Steps of NT threads x 8 columns that cover d, rounded up to a power of two.
-static int steps(int d, int nt) {
-  int s = 1;
-  while (s * nt * 8 < d) s *= 2;
-  return s;
-}
-#define DS4_STEPS(ns, ...)                          \
-  do {                                              \
-    if (ns == 1) {                                  \
-      constexpr int NS = 1;                         \
-      __VA_ARGS__                                   \
-    } else if (ns == 2) {                           \
-      constexpr int NS = 2;                         \
-      __VA_ARGS__                                   \
-    } else if (ns == 4) {                           \
-      constexpr int NS = 4;                         \
-      __VA_ARGS__                                   \
-    } else {                                        \
-      constexpr int NS = 8;                         \
-      __VA_ARGS__                                   \
-    }                                               \
+// Threads of a row and their steps of 8 columns.  256 threads keep more rows
+// on a CU (2048 rows of 4096: 14.1 us, 15.2 with 512); above 8 K columns 512
+// halve the longest part of a row (2048 rows of 16384 67.8 us, 73.8 with 256;
+// one row 6.3 and 8.4).
+#define DS4_ROW(d, ...)                  \
+  do {                                   \
+    if (d <= 2048) {                     \
+      constexpr int NT = 256, NS = 1;    \
+      __VA_ARGS__                        \
+    } else if (d <= 4096) {              \
+      constexpr int NT = 256, NS = 2;    \
+      __VA_ARGS__                        \
+    } else if (d <= 8192) {              \
+      constexpr int NT = 256, NS = 4;    \
+      __VA_ARGS__                        \
+    } else {                             \
+      constexpr int NT = 512, NS = 4;    \
+      __VA_ARGS__                        \
+    }                                    \
   } while (0)
 #define DS4_BOOL(cond, NAME, ...) \
   do {                            \
@@ -422,8 +420,8 @@ static bool bf(int dt) { return dt == DS4MOE_DT_BF16; }
 hipError_t launch_norm_pre(const NormCall& c) {
   const int d = c.N.d_model;
   const dim3 grid((unsigned)c.T);
-  DS4_STEPS(steps(d, 256), DS4_BOOL(bf(c.h_dt), HB, DS4_BOOL(bf(c.x_dt), XB, {
-    DS4_LAUNCH((k_norm_pre<256, NS, HB, XB>), grid, dim3(256), 0, c.st, c.h, c.N.w_pre, d, c.N.eps, c.x);
+  DS4_ROW(d, DS4_BOOL(bf(c.h_dt), HB, DS4_BOOL(bf(c.x_dt), XB, {
+    DS4_LAUNCH((k_norm_pre<NT, NS, HB, XB>), grid, dim3(NT), 0, c.st, c.h, c.N.w_pre, d, c.N.eps, c.x);
   });););
   return hipGetLastError();
 }
@@ -431,8 +429,8 @@ hipError_t launch_norm_pre(const NormCall& c) {
 hipError_t launch_norm_post(const NormCall& c) {
   const int d = c.N.d_model;
   const dim3 grid((unsigned)c.T);
-  DS4_STEPS(steps(d, 256), DS4_BOOL(bf(c.h_dt), HB, DS4_BOOL(bf(c.y_dt), YB, DS4_BOOL(bf(c.x_dt), XB, {
-    DS4_LAUNCH((k_norm_post<256, NS, HB, YB, XB>), grid, dim3(256), 0, c.st, c.h, c.y, c.gate, c.N.gate, c.N.w_post,
+  DS4_ROW(d, DS4_BOOL(bf(c.h_dt), HB, DS4_BOOL(bf(c.y_dt), YB, DS4_BOOL(bf(c.x_dt), XB, {
+    DS4_LAUNCH((k_norm_post<NT, NS, HB, YB, XB>), grid, dim3(NT), 0, c.st, c.h, c.y, c.gate, c.N.gate, c.N.w_post,
                c.N.w_next, d, c.N.eps, c.N.res_scale, c.h_out, c.x);
   }););););
   return hipGetLastError();
