@@ -45,6 +45,25 @@ def test_group(T, k, E, repeat):
     check_group(draw_idx(gen(T * k + E), T, k, E, 0.2, repeat or k > E), E, f"T={T} k={k} E={E}")
 
 
+def test_group_largest():
+    """2^20 tokens of 16 slots and 1024 experts, against a stable library sort."""
+    T, k, E = 1 << 20, 16, 1024
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    idx = torch.randint(-40, E + 40, (T, k), dtype=torch.int32, device="cuda", generator=g)
+    counts, offsets, perm, inv = group(idx, E)
+    flat = idx.reshape(-1).long()
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    order = torch.sort(key, stable=True).indices
+    assert torch.equal(counts.long(), torch.bincount(key, minlength=E + 1)[:E])
+    assert torch.equal(offsets[1:].long(), counts.long().cumsum(0)) and int(offsets[0]) == 0
+    live = int(offsets[E])
+    assert torch.equal(perm[:live].long(), order[:live]) and (perm[live:] == -1).all()
+    want = torch.full((T * k,), -1, dtype=torch.int64, device="cuda")
+    want[order[:live]] = torch.arange(live, device="cuda")
+    assert torch.equal(inv.reshape(-1).long(), want)
+
+
 @pytest.mark.parametrize("T", [5, 3000])
 def test_group_one_expert_and_none(T):
     check_group(torch.full((T, 3), 9, dtype=torch.int32), 16, "one expert")

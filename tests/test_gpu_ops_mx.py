@@ -379,3 +379,28 @@ def test_product_many_experts(n, E):
     p.check(("f32",))
     b = Back(n, 16, 256, E, offsets=off)
     b.check(("f32",))
+
+
+@pytest.mark.parametrize("n", [5, 90, 1500])
+def test_largest_matrix(n):
+    """16384 x 16384 weights: the first and last outputs, and the gradient's
+    first and last columns, of every tile size's forms."""
+    m = 16384
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    draw = lambda k: torch.randint(0, 256, (k,), dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    scale = lambda k: torch.randint(112, 124, (k,), dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    w = torch.cat([draw(m * m // 2), scale(m * m // 32)])
+    a = torch.cat([draw(n * m // 2), scale(n * m // 32)])
+    w16, a16 = (torch.empty(k, m, dtype=torch.bfloat16, device="cuda") for k in (m, n))
+    D.mx_dequantize(w, m, m, w16, D.DT_BF16)
+    D.mx_dequantize(a, n, m, a16, D.DT_BF16)
+    pick = torch.cat([torch.arange(40), torch.arange(m - 40, m)]).cuda()
+    y = torch.empty(n, m, device="cuda")
+    D.mx_product(a, n, m, w, None, m, 1, None, y, D.DT_F32)
+    ws, a64 = w16[pick].double(), a16.double()
+    close(y[:, pick], a64 @ ws.t().contiguous(), a64.abs() @ ws.abs().t().contiguous(), 2 * m, "product")
+    da = torch.empty(n, m, device="cuda")
+    D.mx_product_grad(a16, D.DT_BF16, n, m, w, m, 1, None, da, D.DT_F32)
+    wc = w16[:, pick].double()
+    close(da[:, pick], a64 @ wc, a64.abs() @ wc.abs(), 2 * m, "gradient")

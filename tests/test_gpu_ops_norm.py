@@ -142,7 +142,7 @@ def test_norm_types_and_gates(gate, h, y, x):
 
 
 @pytest.mark.parametrize("T,d", [(1, 256), (2, 256), (1, 4096), (3, 2048), (7, 2304), (2, 4352), (3, 8192), (2, 16384),
-                                 (513, 256), (1100, 512), (511, 1792)])
+                                 (513, 256), (1100, 512), (511, 1792), (20001, 256), (257, 12544)])
 def test_norm_sizes(T, d):
     Case(T, d, "bf16", "f32", "bf16", "channel" if T % 2 else "token", rho=0.5).check()
 
