@@ -257,7 +257,8 @@ hipError_t launch_group(const int32_t* idx, int64_t S, int E, int32_t* counts, i
   const int chunks = (int)((S + kSortChunk - 1) / kSortChunk);
   DS4_LAUNCH(k_group_hist, dim3(chunks), dim3(kSortChunkT), 0, st, idx, S, E, ws);
   if (chunks <= kSortFew) {
-    DS4_PLACE(kSortChunkT, kSortChunkPer, kMaxE / kSortChunkT, kSortCounted, chunks, ws, chunks);
+    if (E <= kSortChunkT) DS4_PLACE(kSortChunkT, kSortChunkPer, 1, kSortCounted, chunks, ws, chunks);
+    else DS4_PLACE(kSortChunkT, kSortChunkPer, kMaxE / kSortChunkT, kSortCounted, chunks, ws, chunks);
     return hipGetLastError();
   }
   DS4_LAUNCH(k_group_scan, dim3((E + 15) / 16), dim3(256), 0, st, ws, chunks, E, counts);
