@@ -234,9 +234,9 @@ size_t group_ws_bytes(int64_t S, int E) {
   return (size_t)(chunks * E * 4 + 256 + 255) & ~(size_t)255;
 }
 
-// Kernel times: 96 slots of 256 experts 4.9 us with one wave (7.4 with eight);
+// Kernel times: 96 slots of 256 experts 3.7 us with one wave (7.4 with eight);
 // 4084 slots of 64 experts 7.5 us with sixteen; 12288 slots of 256 experts 4.7
-// + 8.3 us in two launches (one block of sixteen waves: 21.8, bound by its one
+// + 7.7 us in two launches (one block of sixteen waves: 21.8, bound by its one
 // CU; scanning in a launch of its own: 17 in three).
 hipError_t launch_group(const int32_t* idx, int64_t S, int E, int32_t* counts, int32_t* offsets, int32_t* perm,
                         int32_t* inv, int32_t* ws, hipStream_t st) {

@@ -15,8 +15,9 @@
 // column step of 8 between lanes) and the reads (16 neighbouring columns)
 // spread over the banks.
 //
-// 2001 rows over 32 experts of 2048 x 4096: 87 us, 1.9 TB/s of the bytes that
-// it needs (a copy moves 4.5) and 0.38 PFLOP/s.  What bounds it is the chain
+// 2001 rows over 32 experts of 2048 x 4096: 95 us, 1.8 TB/s of the bytes that
+// it needs (a copy moves 4.5) and 0.35 PFLOP/s; 85 us where a pass before left
+// the weights in the last-level cache.  What bounds it is the chain
 // of a step within a block (load, barrier, decode, barrier, products).  Tried
 // and left: codes through LDS copies (98 us), the next step's decode beside
 // the products of the same wave with one block to a CU (153 us).
