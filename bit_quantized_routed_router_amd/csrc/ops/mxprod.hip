@@ -182,7 +182,10 @@ __global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* __restrict__ a, 
       const int k = kb + u, v = u % kRowsAhead;
       // past the last piece the rows are zeros and what LDS holds does not count
       pin();
-      vm_wait<(kRowsAhead - 1) * kCopies + 1>();
+      // younger than piece k: the pieces ahead, and the scales if piece k was
+      // under way before them
+      if (u < kRowsAhead) vm_wait<(kRowsAhead - 1) * kCopies + 1>();
+      else vm_wait<(kRowsAhead - 1) * kCopies>();
       asm volatile("" ::: "memory");
       pin();
       u32x4_t wv[2][2];
