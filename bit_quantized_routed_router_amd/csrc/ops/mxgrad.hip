@@ -38,7 +38,7 @@ __device__ inline float4_t mfma_bf16(u32x4_t a, u32x4_t b, float4_t c) {
                                                  0, 0);
 }
 // pieces of 16 bytes (8 r) of row i within the 128 bytes of a step
-__device__ inline int swz_w(int c, int piece) { return c * 8 + (piece ^ ((c ^ (c >> 3)) & 7)); }
+__device__ inline int swz_w(int c, int piece) { return c * 8 + (piece ^ (((c >> 1) ^ (c >> 3)) & 7)); }
 __device__ inline int swz_a(int p, int piece) { return p * 8 + (piece ^ (p & 7)); }
 
 // The 8 elements of a code word as four bfloat16 pairs.  The instruction takes
