@@ -20,7 +20,8 @@
 // the weights in the last-level cache.  What bounds it is the chain
 // of a step within a block (load, barrier, decode, barrier, products).  Tried
 // and left: codes through LDS copies (98 us), the next step's decode beside
-// the products of the same wave with one block to a CU (153 us).
+// the products of the same wave with one block to a CU (153 us), scale codes
+// as words handed out by lane exchange (102 us where bytes take 90).
 #include "../trace.h"
 #include "ops.h"
 #include "rowtile.h"
