@@ -29,7 +29,6 @@ template <int NV, int NW>
 __device__ inline void team_sum(float (&v)[NV], float* red, int wave) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
-  if (NW == 1) return;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) red[i * NW + wave] = v[i];

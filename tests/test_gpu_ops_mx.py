@@ -190,6 +190,15 @@ def test_product_every_tile_size(n, rows, cols, E, tail, glu):
     Product(n, rows // 2 // 16 * 16 if glu else rows, cols, E, tail, glu).check(("bf16",))
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("n,rows,cols,E", [(3100, 4112, 512, 1), (3100, 4096, 768, 1), (3000, 4096, 256, 3)])
+def test_product_largest_tiles(n, rows, cols, E, glu, kind):
+    """Enough tiles of 256 rows by 256 weight rows to fill the chip, an odd
+    number of column pieces and parts past the last output among them."""
+    Product(n, rows // 32 * 16 + 16 * (rows % 32 > 0) if glu else rows, cols, E, 3, glu).check((kind,))
+
+
 def test_product_bad_offsets_stay_in_range():
     """Offsets below zero, past the rows or descending: held to the rows, runs
     that descend are empty."""
