@@ -1,4 +1,5 @@
-"""Build libds4moe.so (HIP, gfx950) in-tree with hipcc.
+"""Build libds4moe.so (HIP, gfx950) in-tree with hipcc, and _tensor_args.so
+(the Python binding's argument checks, host code against torch's headers).
 
     python -m bit_quantized_routed_router_amd.build_lib
 
@@ -19,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libds4moe.so")
+ARGS = os.path.join(PKG, "_tensor_args.so")
 
 ARCH = os.environ.get("DS4MOE_ARCH", "gfx950")
 COMMON = [
@@ -59,10 +61,29 @@ def _compile(name: str, extra: list[str]) -> str:
     return obj
 
 
+def _build_args() -> None:
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = ARGS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding", "tensor_args.cpp"), "-o", tmp,
+           "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for tensor_args.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ARGS)
+
+
 def build(jobs: int = 8) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(jobs) as ex:
+        args = ex.submit(_build_args)
         objs = list(ex.map(lambda kv: _compile(*kv), SOURCES.items()))
+        args.result()
     tmp = LIB + ".tmp"
     cmd = ["hipcc", f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

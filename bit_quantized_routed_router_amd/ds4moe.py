@@ -52,6 +52,7 @@ class HcDesc(ctypes.Structure):
 
 class NormDesc(ctypes.Structure):
     """Mirror of ds4moe_norm."""
+    gpu = None  # the device that the weights are known to be on
     _fields_ = [
         ("d_model", ctypes.c_int32), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float), ("gate", ctypes.c_int32),
         ("w_pre", ctypes.c_void_p), ("w_post", ctypes.c_void_p), ("w_next", ctypes.c_void_p),
@@ -247,29 +248,48 @@ class Hc:
 
 # ---------------------------------------------------------------- operators around the layer
 # Norms, tokens sorted by expert and back, MXFP4 rows and products: thin calls
-# of the C functions of the same names.  Tensors here are checked to be
-# contiguous and on the current device, since the library sees bare addresses
-# (an int is taken as an address, None as NULL).
+# of the C functions of the same names.  The library sees bare addresses, so a
+# tensor's device, layout, type and size are checked here against what the
+# call reads and writes (an int is taken as an address, None as NULL: those go
+# unchecked).
 
-_Tensor = torch.Tensor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# what a tensor holds beside the type codes' values (bfloat16 also as its bits)
+_I32, _BYTES = 100, 101
+_addresses = None
+
+
+def _checker():
+    """The native checker (csrc/binding/tensor_args.cpp)."""
+    global _addresses
+    if _addresses is None:
+        try:
+            from ._tensor_args import addresses
+        except ImportError as e:
+            raise RuntimeError("the binding's _tensor_args.so is missing or does not load: build it with "
+                               "`python -m bit_quantized_routed_router_amd.build_lib`") from e
+        _addresses = addresses
+    return _addresses
 
 
 def _call(name: str, stream, *args) -> None:
-    """Run a C function: tensors as their addresses, the stream last.  The
+    """Run a C function, the stream last.  A tensor comes as (tensor, count,
+    what it holds): it has to hold at least `count` values, or bytes.  The
     current stream's handle is taken without building the Stream object that
     torch.cuda.current_stream() returns (0.2 us against 2.8)."""
     dev = _current_gpu()
-    flat = []
-    for a in args:
-        if isinstance(a, _Tensor):
-            if a.get_device() != dev or not a.is_contiguous():
-                raise ValueError(f"{name}: tensors must be contiguous and on the current GPU")
-            a = a.data_ptr()
-        flat.append(a)
-    flat.append(_stream(stream) if stream is not None or dev < 0 else torch._C._cuda_getCurrentRawStream(dev))
+    flat = (_addresses or _checker())(name, dev, args)
+    flat.append(_stream(stream) if stream is not None or dev < 0 else _raw_stream(dev))
     status = getattr(_lib or lib(), name)(*flat)
     if status != OK:
         raise Ds4moeError(status, name)
+
+
+def _on_gpu(desc):
+    """A norm's descriptor, if its weights are on the current GPU."""
+    if desc.gpu is not None and desc.gpu != _current_gpu():
+        raise ValueError("the norm's weights are not on the current GPU")
+    return desc
 
 
 def _current_gpu() -> int:
@@ -281,39 +301,56 @@ def _current_gpu() -> int:
     return _current_gpu()
 
 
+def _gate(desc, gate, T):
+    return gate, (0, T, desc.d_model, T * desc.d_model)[desc.gate] if 0 <= desc.gate <= GATE_FULL else 0, DT_F32
+
+
 def norm_workspace_bytes(desc: NormDesc, T: int) -> int:
     return int(lib().ds4moe_norm_workspace_bytes(ctypes.byref(desc), T))
 
 
 def norm_pre(desc, h, h_dtype, T, x, x_dtype, stream=None) -> None:
-    _call("ds4moe_norm_pre", stream, ctypes.byref(desc), h, h_dtype, T, x, x_dtype)
+    n = T * desc.d_model
+    _call("ds4moe_norm_pre", stream, _on_gpu(desc), (h, n, h_dtype), h_dtype, T, (x, n, x_dtype), x_dtype)
 
 
 def norm_post(desc, h, h_dtype, y, y_dtype, gate, T, h_out, x_next, x_dtype, stream=None) -> None:
-    _call("ds4moe_norm_post", stream, ctypes.byref(desc), h, h_dtype, y, y_dtype, gate, T, h_out, x_next, x_dtype)
+    n = T * desc.d_model
+    _call("ds4moe_norm_post", stream, _on_gpu(desc), (h, n, h_dtype), h_dtype, (y, n, y_dtype), y_dtype,
+          _gate(desc, gate, T), T, (h_out, n, h_dtype), (x_next, n, x_dtype), x_dtype)
 
 
 def norm_pre_grad(desc, h, h_dtype, dx, x_dtype, dh_out, T, dh, dw_pre, ws, ws_bytes, stream=None) -> None:
-    _call("ds4moe_norm_pre_grad", stream, ctypes.byref(desc), h, h_dtype, dx, x_dtype, dh_out, T, dh, dw_pre, ws,
-          ws_bytes)
+    n = T * desc.d_model
+    _call("ds4moe_norm_pre_grad", stream, _on_gpu(desc), (h, n, h_dtype), h_dtype, (dx, n, x_dtype), x_dtype,
+          (dh_out, n, h_dtype), T, (dh, n, h_dtype), (dw_pre, desc.d_model, DT_F32), (ws, ws_bytes, _BYTES), ws_bytes)
 
 
 def norm_post_grad(desc, dh_out, h_dtype, y, y_dtype, gate, T, dy, dw_post, dgate, ws, ws_bytes, stream=None) -> None:
-    _call("ds4moe_norm_post_grad", stream, ctypes.byref(desc), dh_out, h_dtype, y, y_dtype, gate, T, dy, dw_post, dgate,
-          ws, ws_bytes)
+    n = T * desc.d_model
+    _call("ds4moe_norm_post_grad", stream, _on_gpu(desc), (dh_out, n, h_dtype), h_dtype, (y, n, y_dtype), y_dtype,
+          _gate(desc, gate, T), T, (dy, n, y_dtype), (dw_post, desc.d_model, DT_F32), _gate(desc, dgate, T),
+          (ws, ws_bytes, _BYTES), ws_bytes)
 
 
 class Norm:
-    """Weights of a block's norms (float32 CUDA tensors [d], or None for ones)
-    plus the ds4moe_norm descriptor."""
+    """Weights of a block's norms (float32 CUDA tensors [d] on one GPU, or None
+    for ones) plus the ds4moe_norm descriptor."""
 
     def __init__(self, d, eps=1e-6, res_scale=1.0, gate=GATE_NONE, w_pre=None, w_post=None, w_next=None):
         self.tensors = dict(w_pre=w_pre, w_post=w_post, w_next=w_next)
+        gpu = None
         for name, w in self.tensors.items():
-            if w is not None and (w.dtype != torch.float32 or w.numel() != d or not w.is_cuda or not w.is_contiguous()):
+            if w is None:
+                continue
+            if w.dtype != torch.float32 or w.numel() != d or not w.is_cuda or not w.is_contiguous():
                 raise ValueError(f"{name}: expected {d} contiguous float32 values on the GPU")
+            if gpu is not None and gpu != w.get_device():
+                raise ValueError(f"{name}: expected the weights on one GPU")
+            gpu = w.get_device()
         self.d = d
         self.desc = NormDesc(d, float(eps), float(res_scale), gate, _ptr(w_pre), _ptr(w_post), _ptr(w_next))
+        self.desc.gpu = gpu
 
     def workspace(self, T: int):
         n = norm_workspace_bytes(self.desc, T)
@@ -327,35 +364,53 @@ def group_workspace_bytes(T: int, k: int, n_experts: int) -> int:
 
 
 def group(topk_idx, T, k, n_experts, counts, offsets, perm, inv, ws, ws_bytes, stream=None) -> None:
-    _call("ds4moe_group", stream, topk_idx, T, k, n_experts, counts, offsets, perm, inv, ws, ws_bytes)
+    s = T * k
+    _call("ds4moe_group", stream, (topk_idx, s, _I32), T, k, n_experts, (counts, n_experts, _I32),
+          (offsets, n_experts + 1, _I32), (perm, s, _I32), (inv, s, _I32), (ws, ws_bytes, _BYTES), ws_bytes)
 
 
 def dispatch(x, x_dtype, T, k, d, inv, xs, n_rows, stream=None) -> None:
-    _call("ds4moe_dispatch", stream, x, x_dtype, T, k, d, inv, xs, n_rows)
+    _call("ds4moe_dispatch", stream, (x, T * d, x_dtype), x_dtype, T, k, d, (inv, T * k, _I32), (xs, n_rows * d, x_dtype),
+          n_rows)
 
 
 def combine(ys, ys_dtype, n_rows, inv, topk_w, base, T, k, d, y, y_dtype, stream=None) -> None:
-    _call("ds4moe_combine", stream, ys, ys_dtype, n_rows, inv, topk_w, base, T, k, d, y, y_dtype)
+    s, n = T * k, T * d
+    _call("ds4moe_combine", stream, (ys, n_rows * d, ys_dtype), ys_dtype, n_rows, (inv, s, _I32),
+          (topk_w, s, DT_F32), (base, n, y_dtype), T, k, d, (y, n, y_dtype), y_dtype)
 
 
 def combine_grad(dy, y_dtype, ys, ys_dtype, n_rows, inv, topk_w, T, k, d, dys, dw, dlogits, stream=None) -> None:
-    _call("ds4moe_combine_grad", stream, dy, y_dtype, ys, ys_dtype, n_rows, inv, topk_w, T, k, d, dys, dw, dlogits)
+    s, rows = T * k, n_rows * d
+    _call("ds4moe_combine_grad", stream, (dy, T * d, y_dtype), y_dtype, (ys, rows, ys_dtype), ys_dtype, n_rows,
+          (inv, s, _I32), (topk_w, s, DT_F32), T, k, d, (dys, rows, ys_dtype), (dw, s, DT_F32), (dlogits, s, DT_F32))
+
+
+def _mx_bytes(n, cols):
+    return n * cols * 17 // 32
 
 
 def mx_quantize(x, x_dtype, T, inv, k, n_rows, cols, packed, stream=None) -> None:
-    _call("ds4moe_mx_quantize", stream, x, x_dtype, T, inv, k, n_rows, cols, packed)
+    _call("ds4moe_mx_quantize", stream, (x, T * cols, x_dtype), x_dtype, T, (inv, T * k, _I32), k, n_rows,
+          cols, (packed, _mx_bytes(n_rows, cols), _BYTES))
 
 
 def mx_dequantize(packed, n_rows, cols, out, out_dtype, stream=None) -> None:
-    _call("ds4moe_mx_dequantize", stream, packed, n_rows, cols, out, out_dtype)
+    _call("ds4moe_mx_dequantize", stream, (packed, _mx_bytes(n_rows, cols), _BYTES), n_rows, cols,
+          (out, n_rows * cols, out_dtype), out_dtype)
 
 
 def mx_product(a, n_rows, cols, w, w_up, rows, n_experts, offsets, y, y_dtype, stream=None) -> None:
-    _call("ds4moe_mx_product", stream, a, n_rows, cols, w, w_up, rows, n_experts, offsets, y, y_dtype)
+    m = n_experts * _mx_bytes(rows, cols)
+    _call("ds4moe_mx_product", stream, (a, _mx_bytes(n_rows, cols), _BYTES), n_rows, cols, (w, m, _BYTES),
+          (w_up, m, _BYTES), rows, n_experts, (offsets, n_experts + 1, _I32),
+          (y, n_rows * rows, y_dtype), y_dtype)
 
 
 def mx_product_grad(dy, dy_dtype, n_rows, rows, w, cols, n_experts, offsets, da, da_dtype, stream=None) -> None:
-    _call("ds4moe_mx_product_grad", stream, dy, dy_dtype, n_rows, rows, w, cols, n_experts, offsets, da, da_dtype)
+    _call("ds4moe_mx_product_grad", stream, (dy, n_rows * rows, dy_dtype), dy_dtype, n_rows, rows,
+          (w, n_experts * _mx_bytes(rows, cols), _BYTES), cols, n_experts, (offsets, n_experts + 1, _I32),
+          (da, n_rows * cols, da_dtype), da_dtype)
 
 
 def trace_enable(on: bool) -> None:
