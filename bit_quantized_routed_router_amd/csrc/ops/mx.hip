@@ -9,6 +9,8 @@
 // quad.  Both kernels are bound by memory: 2048 bf16 tokens of 4096 to 6 rows
 // each 44 MB in 10.7 us, back to bf16 127 MB in 19 us (6.6 TB/s); six rows 2.6
 // and 2.3 us.
+#include <algorithm>
+
 #include "../trace.h"
 #include "ops.h"
 
@@ -115,14 +117,21 @@ hipError_t launch_mx_quantize(const void* x, int dt, int64_t T, const int32_t* i
 }
 
 hipError_t launch_mx_dequantize(const void* packed, int64_t rows, int cols, void* out, int dt, hipStream_t st) {
-  const int64_t n8 = rows * cols / 8;
+  // a launch takes fewer than 2^32 threads: 2^31 words of 8 values each
+  constexpr int64_t kWords = 1ll << 31;
+  const int64_t words = rows * cols / 8;
   const uint8_t* codes = (const uint8_t*)packed;
   const uint8_t* scales = codes + rows * cols / 2;
-  const dim3 grid((unsigned)((n8 + 255) / 256));
-  if (dt == DS4MOE_DT_BF16)
-    DS4_LAUNCH(k_mx_dequantize<true>, grid, dim3(256), 0, st, codes, scales, n8, out);
-  else
-    DS4_LAUNCH(k_mx_dequantize<false>, grid, dim3(256), 0, st, codes, scales, n8, out);
+  for (int64_t i = 0; i < words; i += kWords) {
+    const int64_t n8 = std::min(words - i, kWords);
+    const dim3 grid((unsigned)((n8 + 255) / 256));
+    if (dt == DS4MOE_DT_BF16)
+      DS4_LAUNCH(k_mx_dequantize<true>, grid, dim3(256), 0, st, codes + 4 * i, scales + i / 4, n8,
+                 (void*)((uint16_t*)out + 8 * i));
+    else
+      DS4_LAUNCH(k_mx_dequantize<false>, grid, dim3(256), 0, st, codes + 4 * i, scales + i / 4, n8,
+                 (void*)((float*)out + 8 * i));
+  }
   return hipGetLastError();
 }
 
