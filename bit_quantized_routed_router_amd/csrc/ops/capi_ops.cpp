@@ -205,10 +205,9 @@ int ds4moe_combine_grad(const void* dy, int y_dtype, const void* ys, int ys_dtyp
 // ---------------------------------------------------------------- MXFP4 rows
 int ds4moe_mx_quantize(const void* x, int x_dtype, int64_t T, const int32_t* inv, int32_t k, int64_t n, int32_t cols,
                        void* packed, void* stream) {
-  const int rc = check_slots(T, k);
-  if (rc) return rc;
+  if (inv && check_slots(T, k)) return DS4MOE_ESHAPE;
   if (!dim_ok(cols) || n < 1 || n > kOpsMaxRows) return DS4MOE_ESHAPE;
-  if (!inv && (k != 1 || n < T)) return DS4MOE_ESHAPE;
+  if (!inv && (k != 1 || T < 1 || n < T)) return DS4MOE_ESHAPE;
   if (!x || !packed || !dt_ok(x_dtype)) return DS4MOE_EINVAL;
   if (!al(x, 16) || !al(packed, 16) || !al(inv, 4)) return DS4MOE_EALIGN;
   return status(launch_mx_quantize(x, x_dtype, T, inv, k, n, cols, packed, (hipStream_t)stream));

@@ -106,13 +106,20 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t* __restrict
 hipError_t launch_mx_quantize(const void* x, int dt, int64_t T, const int32_t* inv, int k, int64_t rows, int cols,
                               void* packed, hipStream_t st) {
   const int nb = (cols + 2047) / 2048;
-  const dim3 grid((unsigned)(T * nb));
   uint8_t* codes = (uint8_t*)packed;
   uint8_t* scales = codes + rows * cols / 2;
-  if (dt == DS4MOE_DT_BF16)
-    DS4_LAUNCH(k_mx_quantize<true>, grid, dim3(256), 0, st, x, inv, k, cols, nb, (int)rows, codes, scales);
-  else
-    DS4_LAUNCH(k_mx_quantize<false>, grid, dim3(256), 0, st, x, inv, k, cols, nb, (int)rows, codes, scales);
+  // a launch takes fewer than 2^32 threads: 2^20 tokens, as many as a sorted
+  // call has at most
+  for (int64_t t = 0; t < T; t += kOpsMaxT) {
+    const int64_t n = std::min(T - t, kOpsMaxT), i = t * cols;
+    const dim3 grid((unsigned)(n * nb));
+    if (dt == DS4MOE_DT_BF16)
+      DS4_LAUNCH(k_mx_quantize<true>, grid, dim3(256), 0, st, (const void*)((const uint16_t*)x + i), inv, k, cols, nb,
+                 (int)rows, codes + i / 2, scales + i / 32);
+    else
+      DS4_LAUNCH(k_mx_quantize<false>, grid, dim3(256), 0, st, (const void*)((const float*)x + i), inv, k, cols, nb,
+                 (int)rows, codes + i / 2, scales + i / 32);
+  }
   return hipGetLastError();
 }
 

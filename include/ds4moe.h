@@ -431,9 +431,9 @@ int ds4moe_combine_grad(const void *dy, int y_dtype, const void *ys, int ys_dtyp
  * ds4moe_quantize(DS4MOE_FMT_MXFP4) does and stored at the rows that a sort
  * gives: row inv[t k + j] of packed [n][cols] takes token t, for each of its
  * k slots (positions outside [0, n) are skipped, rows that no slot has are
- * left as they were).  inv NULL: row t takes token t (k = 1, n >= T).  A
- * block of 32 that holds an infinity or a NaN gets scale code 0xFF: all of
- * it reads back as NaN. */
+ * left as they were), T and k as for a sorted call above.  inv NULL: row t
+ * takes token t (k = 1, 1 <= T <= n).  A block of 32 that holds an infinity or
+ * a NaN gets scale code 0xFF: all of it reads back as NaN. */
 int ds4moe_mx_quantize(const void *x, int x_dtype, int64_t T, const int32_t *inv, int32_t k, int64_t n, int32_t cols,
                        void *packed, void *stream);
 

@@ -31,3 +31,17 @@ def test_dequantize_more_than_2_to_the_35_values():
                           packed[codes + lo * cols // 32:codes + (lo + 64) * cols // 32]])
         D.mx_dequantize(part, 64, cols, few, BF)
         assert torch.equal(out[lo:lo + 64].view(torch.int16), few.view(torch.int16)), lo
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_quantize_more_rows_than_a_sorted_call_has_tokens(kind):
+    """Row by row: the hidden rows of six slots a token pass 2^20 long before
+    their tokens do."""
+    n, cols = (2 << 20) + 70, 256
+    x = torch.randn(n, cols, dtype=kind, device="cuda", generator=gen(2))
+    packed = torch.full((n * cols * 17 // 32,), 0xA5, dtype=torch.uint8, device="cuda")
+    dt = BF if kind == torch.bfloat16 else D.DT_F32
+    D.mx_quantize(x, dt, n, None, 1, n, cols, packed)
+    ref = torch.empty_like(packed)
+    D.quantize(D.FMT_MXFP4, x.float(), n, cols, ref)
+    assert torch.equal(packed, ref)
