@@ -245,6 +245,7 @@ int ds4moe_mx_product_grad(const void* dy, int dy_dtype, int64_t n, int32_t rows
                            int32_t n_experts, const int32_t* offsets, void* da, int da_dtype, void* stream) {
   const int rc = check_product(n, rows, cols, n_experts, offsets);
   if (rc) return rc;
+  if (n * cols > kOpsMaxGrad) return DS4MOE_ESHAPE;
   if (!dy || !w || !da || !dt_ok(dy_dtype) || !dt_ok(da_dtype)) return DS4MOE_EINVAL;
   if (!al(dy, 16) || !al(w, 16) || !al(da, 16) || !al(offsets, 4)) return DS4MOE_EALIGN;
   MxProduct p{};

@@ -14,6 +14,9 @@ namespace ds4 {
 
 constexpr int64_t kOpsMaxT = 1 << 20;     // tokens of a norm, sort, dispatch or combine call
 constexpr int64_t kOpsMaxRows = 1 << 24;  // rows of an MXFP4 call, and T * top_k of a sorted one
+// values of a product gradient: its blocks of 256 threads take 256 columns and
+// 32 rows (and one more tile an expert), and a launch fewer than 2^32 threads
+constexpr int64_t kOpsMaxGrad = (1ll << 37) - (1ll << 29);
 
 // ---------------------------------------------------------------- typed rows
 // Eight consecutive elements (index i, a multiple of 8) of an fp32 or

@@ -17,3 +17,13 @@ def test_quantize_row_by_row_takes_as_many_rows_as_a_matrix_has():
         assert quant(T) == D.ESHAPE, T
     assert quant(1 << 20, inv=A, k=16) == D.EALIGN
     assert quant(4, inv=A, k=17) == D.ESHAPE and quant(4, k=2) == D.ESHAPE and quant(9, n=8) == D.ESHAPE
+
+
+def test_product_gradient_refuses_more_values_than_a_launch_covers():
+    def back(n, cols, dt=0):
+        return D.lib().ds4moe_mx_product_grad(A, dt, n, 16, A, cols, 1, None, A + 4, 0, None)
+
+    for dt in (D.DT_F32, D.DT_BF16):
+        for n, cols in ((1 << 24, 8192), (1 << 24, 16384), (1 << 23, 16384), ((1 << 24) - 32768, 8192)):
+            assert back(n, cols, dt) == (D.ESHAPE if n * cols > 2 ** 37 - 2 ** 29 else D.EALIGN), (n, cols)
+        assert back((1 << 24) - 65536, 8192, dt) == D.EALIGN
