@@ -106,7 +106,7 @@ __device__ __attribute__((always_inline)) inline void store_tile(const float16_t
 constexpr int kRowsAhead = 2;                             // pieces in flight
 constexpr int kRowsWave = kRowsAhead * 4096 + 2 * 1024;  // their codes, scales of two groups of four pieces
 template <bool GLU, bool BF>
-__global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* __restrict__ a, const uint8_t* __restrict__ w,
+__global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* a, const uint8_t* __restrict__ w,
                                                  const uint8_t* __restrict__ w2, const int32_t* __restrict__ offsets,
                                                  int n, int rows, int cols, int E, void* __restrict__ y) {
   constexpr int NO = GLU ? 16 : 32;
@@ -167,12 +167,18 @@ __global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* __restrict__ a, 
   };
   constexpr int kCopies = 4 + 3;  // loads per piece
   float4_t acc[2] = {};
+  // The waits below count loads in this order.  The fences keep it (and that a
+  // is not __restrict__: loads of what nothing writes may pass them).
+  auto fence = [] { asm volatile("" ::: "memory"); };
   copy_scales(k0);
 #pragma unroll
   for (int u = 0; u < kRowsAhead; ++u) {
+    pin();
+    fence();
     copy_codes(k0 + u);
     load_rows(k0 + u, u);
   }
+  fence();
 #pragma unroll 1
   for (int kb = k0; kb < k1; kb += 4) {
     // the next group's scales, behind everything that this group waits for
