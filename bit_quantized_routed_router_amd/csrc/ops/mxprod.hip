@@ -17,7 +17,7 @@
 // eight lanes to a row: so everything but a few rows goes through LDS, its 16
 // byte pieces XOR-swizzled by row pair.
 //
-// Measured: 6 rows of 256 experts, gate and up, 53 MB in 11.6 us (4.6 TB/s);
+// Measured: 6 rows of 256 experts, gate and up, 53 MB in 11.5 us (4.6 TB/s);
 // 12288 rows of 256 experts, down, 1.36 GB in 280 us (4.8 TB/s: bound by
 // reading the weights, a large copy moves 4.5); 4001 rows of one expert, gate
 // and up 4096 x 4096, 77 us (3.5 PFLOP/s).
@@ -99,19 +99,26 @@ __device__ __attribute__((always_inline)) inline void store_tile(const float16_t
 // A block takes 32 weight rows (GLU: 16 gate and the same 16 up) and a tile
 // of up to 16 rows; its four waves each take a quarter of the columns, a
 // piece of 256 at a time, and add up through LDS.  The weights pass through
-// the wave's own LDS, four pieces in flight, because the lanes of the matrix
+// the wave's own LDS, two pieces in flight, because the lanes of the matrix
 // instruction hold 16 different rows side by side and a load in that order
-// moves 15 bytes a cycle against the copies' 52 (8 lanes to a row).  The few
+// moves 15 bytes a cycle against the copies' 52 (8 lanes to a row).  Their
+// scales come four pieces at a time and wait in registers, so that the next
+// four's copy has the same LDS again: 36 KB, four blocks to a CU.  The few
 // rows themselves are loaded straight into registers.
-constexpr int kRowsAhead = 2;                             // pieces in flight
-constexpr int kRowsWave = kRowsAhead * 4096 + 2 * 1024;  // their codes, scales of two groups of four pieces
+constexpr int kRowsAhead = 2;                        // pieces in flight
+constexpr int kRowsWave = kRowsAhead * 4096 + 1024;  // their codes, scales of four pieces
+constexpr int kRowsBlocks = 4;                       // blocks to a CU
 template <bool GLU, bool BF>
-__global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* a, const uint8_t* __restrict__ w,
-                                                 const uint8_t* __restrict__ w2, const int32_t* __restrict__ offsets,
-                                                 int n, int rows, int cols, int E, void* __restrict__ y) {
+__global__ __launch_bounds__(256, kRowsBlocks) void k_mx_rows(const uint8_t* a, const uint8_t* __restrict__ w,
+                                                              const uint8_t* __restrict__ w2,
+                                                              const int32_t* __restrict__ offsets, int n, int rows,
+                                                              int cols, int E, void* __restrict__ y) {
   constexpr int NO = GLU ? 16 : 32;
+  // (sized at the launch: for an array of fixed size the compiler puts a wait
+  // for the copies under way before reads that it cannot tell apart from them)
+  extern __shared__ uint8_t smem[];
   __shared__ int lds[16];
-  __shared__ uint8_t smem[4 * kRowsWave];
+  static_assert(kRowsBlocks * (sizeof(lds) + 4 * kRowsWave) <= 160 * 1024, "the CU's LDS");
   const RowTile rt = find_tile(offsets, E, n, 16, (rows + NO - 1) / NO, lds);
   if (rt.cnt <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
@@ -139,21 +146,20 @@ __global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* a, const uint8_t
     }
   };
   // scales of four pieces: 32 bytes of each of 32 rows, two lanes to a row
+  uint8_t* const sl = wl + kRowsAhead * 4096;
   auto copy_scales = [&](int k) __attribute__((always_inline)) {
-    uint8_t* dst = wl + kRowsAhead * 4096 + (((k - k0) >> 2) & 1) * 1024;
     const uint32_t vo = (uint32_t)((lane >> 1) & (GLU ? 15 : 31)) * (cols / 32) + (lane & 1) * 16;
     const uint32_t so = rows * (cols / 2) + r0 * (cols / 32) + k * 8;
-    const bool on = k < k1;
+    const int off = k < k1 ? (int)vo : (int)kOob;
+    auto copy = [&](int m) __attribute__((always_inline)) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[m], (__attribute__((address_space(3))) void*)sl, 16, off, so, 0, 0);
+    };
     if constexpr (GLU) {  // half of the lanes from each matrix; a copy fills what its active lanes name
-      if (lane < 32)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[0], (__attribute__((address_space(3))) void*)dst, 16,
-                                                 on ? (int)vo : (int)kOob, so, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[1], (__attribute__((address_space(3))) void*)dst, 16,
-                                                 on ? (int)vo : (int)kOob, so, 0, 0);
+      if (lane < 32) copy(0);
+      asm volatile("" ::: "memory");  // (two copies, not one with a choice of matrix)
+      if (lane >= 32) copy(1);
     } else {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[0], (__attribute__((address_space(3))) void*)dst, 16,
-                                               on ? (int)vo : (int)kOob, so, 0, 0);
+      copy(0);
     }
   };
   u32x4_t A[kRowsAhead][2];
@@ -181,37 +187,40 @@ __global__ __launch_bounds__(256) void k_mx_rows(const uint8_t* a, const uint8_t
   fence();
 #pragma unroll 1
   for (int kb = k0; kb < k1; kb += 4) {
-    // the next group's scales, behind everything that this group waits for
-    copy_scales(kb + 4);
+    u32x4_t ws[2][2];  // scales of the group's pieces, two words a piece
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int k = kb + u, v = u % kRowsAhead;
       // past the last piece the rows are zeros and what LDS holds does not count
       pin();
-      // younger than piece k: the pieces ahead, and the scales if piece k was
-      // under way before them
-      if (u < kRowsAhead) vm_wait<(kRowsAhead - 1) * kCopies + 1>();
+      // Younger than piece k: the pieces ahead, and for the group's second piece
+      // the next group's scales.  This group's are older than its first piece.
+      if (u == 1) vm_wait<(kRowsAhead - 1) * kCopies + 1>();
       else vm_wait<(kRowsAhead - 1) * kCopies>();
       asm volatile("" ::: "memory");
       pin();
       u32x4_t wv[2][2];
-      u32x2_t ws[2];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         const int row = 16 * f + c;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           wv[f][j] = *(const u32x4_t*)(wl + v * 4096 + row * 128 + (((4 * j + q) ^ (row >> 1)) & 7) * 16);
-        ws[f] = *(const u32x2_t*)(wl + kRowsAhead * 4096 + (((kb - k0) >> 2) & 1) * 1024 + row * 32 + u * 8);
+        if (u == 0) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) ws[f][j] = *(const u32x4_t*)(sl + row * 32 + 16 * j);
+        }
       }
       if (k < k1) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int f = 0; f < 2; ++f) acc[f] = mfma_mx(wv[f][j], A[v][j], acc[f], ws[f][j] >> (8 * q), AS[v][j] >> (8 * q));
+          for (int f = 0; f < 2; ++f)
+            acc[f] = mfma_mx(wv[f][j], A[v][j], acc[f], ws[f][u / 2][2 * (u & 1) + j] >> (8 * q), AS[v][j] >> (8 * q));
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot (and the scales) have been read
       pin();
+      if (u == 0) copy_scales(kb + 4);
       copy_codes(k + kRowsAhead);
       load_rows(k + kRowsAhead, v);
     }
@@ -557,8 +566,8 @@ template <bool GLU, bool BF>
 static hipError_t launch_rows(const MxProduct& p) {
   const int no = GLU ? 16 : 32;
   const int64_t blocks = (p.rows + no - 1) / no * max_tiles(p.n, p.E, p.offsets != nullptr, 16);
-  DS4_LAUNCH((k_mx_rows<GLU, BF>), dim3((unsigned)blocks), dim3(256), 0, p.st, p.a, p.w, p.w2, p.offsets, (int)p.n,
-             p.rows, p.cols, p.E, p.out);
+  DS4_LAUNCH((k_mx_rows<GLU, BF>), dim3((unsigned)blocks), dim3(256), 4 * kRowsWave, p.st, p.a, p.w, p.w2, p.offsets,
+             (int)p.n, p.rows, p.cols, p.E, p.out);
   return hipGetLastError();
 }
 template <int NT, int R, bool GLU, bool BF>
@@ -575,7 +584,8 @@ static hipError_t launch_mid(const MxProduct& p) {
 // Times of 4096 x 4096 weights on one expert, in us: rows / 64-row / 128-row /
 // 256-row tiles.
 //   few rows   while its blocks fit the chip at once (four on each of 256
-//              CUs): 32 rows 6.6 / 11.7 / 13.3 / 26.6, 128 rows 13.7 / 12.2
+//              CUs): 32 rows (256 blocks) 5.2 / 11.3, 96 rows (768) 9.7 / 11.6,
+//              128 rows (1024) 11.8 / 11.7
 //   256 rows   when its blocks, one to a CU, fill at least 3/4 of their last
 //              round: 4096 rows (256 blocks) 63 / 50 / 40, 2000 rows (128
 //              blocks) 32 / 26.6 / 32.5
@@ -590,7 +600,7 @@ static hipError_t product(const MxProduct& p) {
     return (p.rows + outputs - 1) / outputs * std::max<int64_t>(1, p.n / bm + (E > 1 ? E / 2 : p.n % bm != 0));
   };
   constexpr int g = GLU ? 2 : 1;  // weight rows per output
-  if ((p.rows + 32 / g - 1) / (32 / g) * max_tiles(p.n, p.E, p.offsets != nullptr, 16) <= 4 * kCus)
+  if ((p.rows + 32 / g - 1) / (32 / g) * max_tiles(p.n, p.E, p.offsets != nullptr, 16) <= kRowsBlocks * kCus)
     return launch_rows<GLU, BF>(p);
   const int64_t big = blocks(kBig / g, kBig);
   if (mean >= 192 && 4 * big >= 3 * ((big + kCus - 1) / kCus * kCus)) return launch_big<GLU, BF>(p);
