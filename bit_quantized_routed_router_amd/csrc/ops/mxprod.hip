@@ -574,8 +574,14 @@ template <int NT, int R, bool GLU, bool BF>
 static hipError_t launch_mid(const MxProduct& p) {
   const int nob = GLU ? 64 : 128;
   const int64_t blocks = (p.rows + nob - 1) / nob * max_tiles(p.n, p.E, p.offsets != nullptr, 64 * NT);
-  DS4_LAUNCH((k_mx_mid<NT, R, GLU, BF>), dim3((unsigned)blocks), dim3(256), (mid_lds<NT, R>()), p.st, p.a, p.w, p.w2,
-             p.offsets, (int)p.n, p.rows, p.cols, p.E, p.out);
+  // (the number of rows as written, so that the timer's names tell the forms apart)
+#define DS4_MID(nt)                                                                                                  \
+  DS4_LAUNCH((k_mx_mid<nt, R, GLU, BF>), dim3((unsigned)blocks), dim3(256), (mid_lds<nt, R>()), p.st, p.a, p.w, p.w2, \
+             p.offsets, (int)p.n, p.rows, p.cols, p.E, p.out)
+  static_assert(NT == 1 || NT == 2, "64 or 128 rows");
+  if constexpr (NT == 1) DS4_MID(1);
+  else DS4_MID(2);
+#undef DS4_MID
   return hipGetLastError();
 }
 
