@@ -457,7 +457,10 @@ int ds4moe_mx_product(const void *a, int64_t n, int32_t cols, const void *w, con
  * rounded to FP4: da[p][c] = sum_r dy[p][r] w_e[r][c], dy [n][rows] and da
  * [n][cols] fp32 or bf16.  Products are exact for bf16 and to fp32 rounding
  * for fp32, sums are fp32, da is rounded once.  Rows without an expert are
- * left as they were.  n cols is at most 2^37 - 2^29 (da of 274 GB in bf16). */
+ * left as they were.  n cols is at most 2^37 - 2^29 (da of 274 GB in bf16).
+ * The SwiGLU form keeps neither g nor u and has no gradient call: to train
+ * through it, take the two products apart (w_up NULL), form silu(g) u and its
+ * derivative in the program, and add the two products' gradients. */
 int ds4moe_mx_product_grad(const void *dy, int dy_dtype, int64_t n, int32_t rows, const void *w, int32_t cols,
                            int32_t n_experts, const int32_t *offsets, void *da, int da_dtype, void *stream);
 
