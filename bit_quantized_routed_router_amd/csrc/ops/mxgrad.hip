@@ -5,8 +5,9 @@
 // so the block-scaled instruction does not apply: the weights become bfloat16
 // (exact: two significant bits and a power of two) and v_mfma_f32_16x16x32_bf16
 // multiplies them.  A bfloat16 dY goes in as it is; an fp32 dY is cut into
-// three bfloat16 parts of 8 significant bits each, which hold it exactly, and
-// takes three instructions.  The sum is fp32.
+// three bfloat16 parts of 8 significant bits each, which hold it exactly
+// (below 2^-110 to less than 2^-133, bfloat16's smallest number), and takes
+// three instructions.  The sum is fp32.
 //
 // A block takes 256 columns and a tile of rows p.  A thread decodes 8 rows r
 // by 8 columns, pairs neighbouring rows by byte permutation and writes, per
@@ -55,7 +56,7 @@ __device__ inline u32x4_t mx_bf16(uint32_t w, uint32_t sc) {
 }
 
 // The bfloat16 values of which x and y are the sum, by truncation (8 + 8 + 8
-// bits), as three pairs.  An infinity or a NaN is its first part (a NaN made
+// bits; what lies under 2^-133 is lost), as three pairs.  An infinity or a NaN is its first part (a NaN made
 // quiet before, so that its upper half says NaN), the others are zero.
 __device__ inline void split3(float x, float y, uint32_t (&h)[3]) {
   x = __builtin_canonicalizef(x);

@@ -455,8 +455,9 @@ int ds4moe_mx_product(const void *a, int64_t n, int32_t cols, const void *w, con
 
 /* Gradient of the product (w_up NULL) to its rows, as if they had not been
  * rounded to FP4: da[p][c] = sum_r dy[p][r] w_e[r][c], dy [n][rows] and da
- * [n][cols] fp32 or bf16.  Products are exact for bf16 and to fp32 rounding
- * for fp32, sums are fp32, da is rounded once.  Rows without an expert are
+ * [n][cols] fp32 or bf16.  Products are exact for bf16; an fp32 dy is held
+ * exactly from 2^-110 up and to less than 2^-133 below, and its products to
+ * fp32 rounding.  Sums are fp32, da is rounded once.  Rows without an expert are
  * left as they were.  n cols is at most 2^37 - 2^29 (da of 274 GB in bf16).
  * The SwiGLU form keeps neither g nor u and has no gradient call: to train
  * through it, take the two products apart (w_up NULL), form silu(g) u and its
