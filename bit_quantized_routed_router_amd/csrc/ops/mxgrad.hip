@@ -201,7 +201,7 @@ template <int NF, int PARTS, bool OB>
 __global__ __launch_bounds__(256, PARTS == 3 ? 2 : NF == 2 ? 4 : 3) void k_mx_grad(const void* __restrict__ dy, const uint8_t* __restrict__ w,
                                                     const int32_t* __restrict__ offsets, int n, int rows, int cols,
                                                     int E, void* __restrict__ out) {
-  extern __shared__ uint8_t smem[];  // two slots of 40 KB: exactly two blocks to a CU
+  extern __shared__ uint8_t smem[];  // one slot: 36 KB (2, 1), 40 (4, 1) or 44 (2, 3)
   const RowTile rt = find_tile(offsets, E, n, 16 * NF, cols / kGradBN, (int*)smem);
   if (rt.cnt <= 0) return;
   __syncthreads();  // everyone has read the tile

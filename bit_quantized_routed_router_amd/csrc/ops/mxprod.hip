@@ -39,8 +39,9 @@ __device__ inline float4_t mfma_mx(u32x4_t a, u32x4_t b, float4_t c, uint32_t sa
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// g / (1 + e^-g) with the reciprocal instruction: within 2 steps of the
-// quotient, which the output's rounding or the sum's own error covers.
+// g / (1 + e^-g) with the reciprocal instruction (within 2 steps of the
+// quotient) and the fast exponential, whose argument is off by |g| half steps:
+// (16 + |g|) half steps in all bound it.
 __device__ inline float silu_rcp(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 typedef float float16_t __attribute__((ext_vector_type(16)));

@@ -415,7 +415,7 @@ int ds4moe_combine(const void *ys, int ys_dtype, int64_t n_rows, const int32_t *
  *   dys[inv[s]] = w_s dy[t]                 (ys's type; rows without a slot are left as they were)
  *   dw[s]       = sum_c dy[t] ys[inv[s]]    fp32 [T][k]
  *   dlogits[s]  = w_s (dw_s - sum_j w_j dw_j): through the softmax over the
- *                 token's slots that gave topk_w, fp32 [T][k]
+ *                 token's slots with a row that gave topk_w, fp32 [T][k]
  * Any of the three may be NULL, not all.  dys may equal ys. */
 int ds4moe_combine_grad(const void *dy, int y_dtype, const void *ys, int ys_dtype, int64_t n_rows, const int32_t *inv,
                         const float *topk_w, int64_t T, int32_t k, int32_t d, void *dys, float *dw, float *dlogits,
@@ -448,7 +448,8 @@ int ds4moe_mx_dequantize(const void *packed, int64_t n, int32_t cols, void *out,
  * (device, ascending) as ds4moe_group gives them; NULL with n_experts = 1: all
  * rows.  Offsets are taken as held to [0, n]; rows of y [n][rows] that no
  * expert has are left as they were.  Products and block scales are exact,
- * sums fp32, y (fp32 or bf16) is rounded once.  rows: a multiple of 16, <=
+ * sums fp32, silu within (16 + |g|) 2^-24 of its value, y (fp32 or bf16) is
+ * rounded once.  rows: a multiple of 16, <=
  * 16384; n_experts <= 1024. */
 int ds4moe_mx_product(const void *a, int64_t n, int32_t cols, const void *w, const void *w_up, int32_t rows,
                       int32_t n_experts, const int32_t *offsets, void *y, int y_dtype, void *stream);
