@@ -12,8 +12,9 @@
 // kernels go by token, so a token's row is read once for all its slots, and
 // no sum depends on the order in which blocks run.  They are bound by memory:
 // 2048 tokens of 4096, 6 slots each: dispatch 117 MB in 21 us (5.5 TB/s),
-// combine 168 MB in 30 us (5.6 TB/s); combine_grad in fp32 (1021 tokens of
-// 2048, 4 slots) 72 MB in 12.6 us (5.7 TB/s).  A large copy moves 4.5 TB/s.
+// combine 168 MB in 31 us (5.4 TB/s); combine_grad in fp32 (1021 tokens of
+// 2048, 4 slots) 72 MB in 13 us (5.5 TB/s).  A 4 GB copy moves 4.5 TB/s, one
+// of 128 MB, which the last-level cache holds, 6.8.
 #include <algorithm>
 
 #include "../trace.h"

@@ -18,9 +18,9 @@
 // byte pieces XOR-swizzled by row pair.
 //
 // Measured: 6 rows of 256 experts, gate and up, 53 MB in 11.5 us (4.6 TB/s);
-// 12288 rows of 256 experts, down, 1.36 GB in 280 us (4.8 TB/s: bound by
-// reading the weights, a large copy moves 4.5); 4001 rows of one expert, gate
-// and up 4096 x 4096, 77 us (3.5 PFLOP/s).
+// 12288 rows of 256 experts, down, 1.36 GB in 280 us (4.9 TB/s; a kernel that
+// only reads as much takes 276); 4001 rows of one expert, gate and up 4096 x
+// 4096, 75 to 81 us (3.3 to 3.6 PFLOP/s; the instruction alone reaches 8).
 #include <algorithm>
 #include <type_traits>
 

@@ -13,8 +13,10 @@
 // sums and the outputs, so all of them are bound by memory for many tokens
 // and by the latency of load, sum, store for few.  Kernel times: post with the
 // next pre-norm, one fp32 row of 4096 3.4 us, 2048 bf16 rows with fp32 y 84 MB
-// in 14 us (6 TB/s); 2047 bf16 rows of 1792: post_grad 22 MB in 10.6 us,
-// pre_grad 29 MB in 9.6 us, each with 3.7 us for the sum over tokens.
+// in 14 us (6 TB/s); 2047 bf16 rows of 1792: post_grad 22 MB in 10.3 us,
+// pre_grad 29 MB in 9.1 us, each with 3.4 us for the sum over tokens.  Above
+// 8192 columns post_grad spills 51 to 65 registers a thread, on 4096 fp32
+// columns 3.
 #include <algorithm>
 
 #include "../trace.h"
