@@ -259,8 +259,8 @@ _I32, _BYTES = 100, 101
 _addresses = None
 
 
-def _checker():
-    """The native checker (csrc/binding/tensor_args.cpp)."""
+def _load_addresses():
+    """The native argument checks (csrc/binding/tensor_args.cpp)."""
     global _addresses
     if _addresses is None:
         try:
@@ -278,7 +278,7 @@ def _call(name: str, stream, *args) -> None:
     current stream's handle is taken without building the Stream object that
     torch.cuda.current_stream() returns (0.2 us against 2.8)."""
     dev = _current_gpu()
-    flat = (_addresses or _checker())(name, dev, args)
+    flat = (_addresses or _load_addresses())(name, dev, args)
     flat.append(_stream(stream) if stream is not None or dev < 0 else _raw_stream(dev))
     status = getattr(_lib or lib(), name)(*flat)
     if status != OK:
