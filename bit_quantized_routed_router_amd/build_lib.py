@@ -44,6 +44,10 @@ SOURCES = {
     "ops/mxprod.hip": [],
     "ops/mxgrad.hip": [],
     "ops/capi_ops.cpp": ["-x", "hip"],
+    "train/balance.hip": [],
+    "train/xent.hip": [],
+    "train/adamw.hip": [],
+    "train/capi_train.cpp": ["-x", "hip"],
 }
 
 

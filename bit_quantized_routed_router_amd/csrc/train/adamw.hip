@@ -1,0 +1,358 @@
+// AdamW over many tensors at once, and the norm of all their gradients:
+//
+//   g' = s g,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+//   p  = p - lr (wd p + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
+//   norm = sqrt(sum g^2),  s = min(1, max_norm / norm)
+//
+// States in fp32, or m and sqrt(v) as E4M3 codes with an fp32 scale (largest
+// magnitude / 448) per 256 values.  The root halves the exponents that v
+// spans, and what is positive of it is held as the lowest code at least: a v
+// that became 0 would make its value's next step as large as eps allows.  The
+// scale is no power of two, so that a block that only decays is still followed.
+//
+// A block takes a run of one tensor, 8 values to a thread: 32 lanes hold a
+// block of 256, so its largest value stays within half a wave.  Tensors come
+// by value with the launch, kTensors at a time, so that nothing has to be kept
+// or copied between calls; a block finds its tensor by bisection.
+#include <algorithm>
+#include <cmath>
+
+#include "../trace.h"
+#include "train.h"
+
+namespace ds4 {
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamRun = 4096;       // values of a block
+constexpr int kNormRun = 16384;      // ... of the norm
+constexpr int kTensors = 46;         // of a launch: 4 KB of arguments
+
+struct AdamBatch {
+  int n;
+  int start[kTensors + 1];  // first block of each
+  int64_t first[kTensors];  // the run that it starts with
+  ds4moe_param p[kTensors];
+};
+
+template <int RUN>
+static int64_t runs_of(int64_t n) {
+  return (n + RUN - 1) / RUN;
+}
+size_t adam_ws_bytes(const ds4moe_param* p, int n) {
+  int64_t runs = 0;
+  for (int i = 0; i < n; ++i) runs += runs_of<kNormRun>(p[i].n);
+  return std::max<size_t>(256, 8 * (size_t)runs);
+}
+
+// The tensor of this block, and its first value.
+__device__ inline int adam_tensor(const AdamBatch& b, int run, int64_t& at) {
+  int lo = 0, hi = b.n;
+  const int blk = blockIdx.x;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (b.start[mid] <= blk) lo = mid;
+    else hi = mid;
+  }
+  at = (b.first[lo] + blk - b.start[lo]) * run;
+  return lo;
+}
+
+// Eight values from i on, `left` of them there; zeros for the others.
+template <bool BF>
+__device__ inline void get8(const void* p, int64_t i, int left, bool whole, float (&v)[8]) {
+  if (whole) {
+    unpack8<BF>(ld8<BF>(p, i), v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = 0.f;
+    if (e < left) {
+      if constexpr (BF) v[e] = __builtin_bit_cast(float, (uint32_t)((const uint16_t*)p)[i + e] << 16);
+      else v[e] = ((const float*)p)[i + e];
+    }
+  }
+}
+template <bool BF>
+__device__ inline void put8(void* p, int64_t i, int left, bool whole, const float (&v)[8]) {
+  if (whole) {
+    st8<BF>(p, i, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < left) {
+      if constexpr (BF) ((uint16_t*)p)[i + e] = (uint16_t)bf16_pair(v[e], 0.f);
+      else ((float*)p)[i + e] = v[e];
+    }
+}
+
+// E4M3 codes times a scale, and back.
+__device__ inline void get8_codes(const void* p, int64_t i, int left, bool whole, float scale, float (&v)[8]) {
+  uint32_t w[2] = {0, 0};
+  if (whole) {
+    const u32x2_t x = *(const u32x2_t*)((const uint8_t*)p + i);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) w[e >> 2] |= (uint32_t)((const uint8_t*)p)[i + e] << (8 * (e & 3));
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[q], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[q], true);
+    v[4 * q] = a.x * scale;
+    v[4 * q + 1] = a.y * scale;
+    v[4 * q + 2] = b.x * scale;
+    v[4 * q + 3] = b.y * scale;
+  }
+}
+// The block of 256 that 32 lanes hold.  Its scale: largest / 448; 0 (and codes
+// of 0) where that is below fp32's normal numbers; NaN, and so the whole
+// block, where a value is not finite.
+template <bool ROOT>
+__device__ inline float put8_codes(void* p, int64_t i, int left, bool whole, const float (&v)[8]) {
+  float top = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    top = fmaxf(top, fabsf(v[e]));
+    bad |= !(fabsf(v[e]) <= 3.402823466e38f);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  const uint64_t half = 0xFFFFFFFFull << (threadIdx.x & 32);
+  bad = (__ballot(bad) & half) != 0;
+  float scale = top * (1.0f / 448.0f);
+  if (scale < 1.17549435e-38f) scale = 0.f;
+  const float r = scale > 0.f && !bad ? 1.0f / scale : 0.f;
+  uint32_t w[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[4 * q + e];
+      y[e] = bad ? 0.f : x * r;
+      if constexpr (ROOT) y[e] = y[e] > 0.f ? fmaxf(y[e], 0.001953125f) : 0.f;  // 2^-9, the lowest code
+    }
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
+  }
+  if (whole) {
+    *(u32x2_t*)((uint8_t*)p + i) = u32x2_t{w[0], w[1]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) ((uint8_t*)p)[i + e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+  }
+  return bad ? NAN : scale;
+}
+
+struct AdamScalars {
+  float b1, b1m, b2, b2m, eps;
+  double lr, c1, c2, log_b1, log_b2;  // lr; 1 - b1^t and 1 - b2^t; for a step on the device
+  const float *lr_dev, *grad_scale;
+  const int32_t* step_dev;
+};
+static_assert(sizeof(AdamBatch) + sizeof(AdamScalars) <= 4096, "arguments of a launch");
+
+template <bool PBF, bool GBF, bool FP8>
+__global__ __launch_bounds__(kAdamThreads) void k_adamw(AdamBatch b, AdamScalars s) {
+  int64_t at;
+  const int t = adam_tensor(b, kAdamRun, at);
+  const ds4moe_param q = b.p[t];
+  const float gs = s.grad_scale ? *s.grad_scale : 1.0f;
+  if (!(fabsf(gs) <= 3.402823466e38f)) return;  // a step without finite gradients changes nothing
+  const double lr = s.lr_dev ? (double)*s.lr_dev : s.lr;
+  double c1 = s.c1, c2 = s.c2;
+  if (s.step_dev) {
+    const double step = max(*s.step_dev, 1);
+    c1 = 1.0 - exp(step * s.log_b1);
+    c2 = 1.0 - exp(step * s.log_b2);
+  }
+  const float keep = (float)(1.0 - lr * q.weight_decay), up = (float)(lr / c1), root = (float)(1.0 / sqrt(c2));
+  const uintptr_t align = (uintptr_t)q.param | (uintptr_t)q.grad | (uintptr_t)q.master |
+                          (FP8 ? ((uintptr_t)q.m | (uintptr_t)q.v) << 1 : (uintptr_t)q.m | (uintptr_t)q.v);
+  const bool vec = (align & 15) == 0;
+  const int64_t end = min(at + kAdamRun, q.n);
+  // FP8: every lane of a block of 256 stays, so that its largest value is known
+  for (int64_t i0 = at; i0 < end; i0 += 8 * kAdamThreads) {
+    const int64_t i = i0 + 8 * threadIdx.x;
+    const int left = (int)max((int64_t)0, min((int64_t)8, end - i));
+    const bool whole = vec && left == 8;
+    if (!FP8 && left == 0) break;
+    float g[8], m[8], v[8], p[8];
+    float ms = 0.f, vs = 0.f;
+    if (FP8 && left > 0) {
+      ms = q.m_scale[i >> 8];
+      vs = q.v_scale[i >> 8];
+    }
+    get8<GBF>(q.grad, i, left, whole, g);
+    if (q.master) get8<false>(q.master, i, left, whole, p);
+    else get8<PBF>(q.param, i, left, whole, p);
+    if constexpr (FP8) {
+      get8_codes(q.m, i, left, whole, ms, m);
+      get8_codes(q.v, i, left, whole, vs, v);
+    } else {
+      get8<false>(q.m, i, left, whole, m);
+      get8<false>(q.v, i, left, whole, v);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = gs * g[e];
+      if (FP8) v[e] *= v[e];
+      m[e] = s.b1 * m[e] + s.b1m * d;
+      v[e] = s.b2 * v[e] + s.b2m * (d * d);
+      const float r = __builtin_amdgcn_sqrtf(v[e]);  // within a step of the root, as the reciprocal is
+      p[e] = keep * p[e] - up * m[e] * __builtin_amdgcn_rcpf(root * r + s.eps);
+      if (FP8) v[e] = r;
+    }
+    put8<PBF>(q.param, i, left, whole, p);
+    if (q.master) put8<false>(q.master, i, left, whole, p);
+    if constexpr (FP8) {
+      ms = put8_codes<false>(q.m, i, left, whole, m);
+      vs = put8_codes<true>(q.v, i, left, whole, v);
+      if ((threadIdx.x & 31) == 0 && left > 0) {
+        q.m_scale[i >> 8] = ms;
+        q.v_scale[i >> 8] = vs;
+      }
+    } else {
+      put8<false>(q.m, i, left, whole, m);
+      put8<false>(q.v, i, left, whole, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- norm
+// Sums of squares in fp64: fp32 squares overflow above 2^64, and the sum over
+// 10^9 values keeps its digits.
+__device__ inline double block_sum(double x, double* lds, int waves) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = 0.0;
+  for (int w = 0; w < waves; ++w) x += lds[w];
+  return x;
+}
+template <bool GBF>
+__global__ __launch_bounds__(kAdamThreads) void k_adamw_squares(AdamBatch b, double* __restrict__ part) {
+  __shared__ double lds[kAdamThreads / 64];
+  int64_t at;
+  const int t = adam_tensor(b, kNormRun, at);
+  const ds4moe_param q = b.p[t];
+  const bool vec = ((uintptr_t)q.grad & 15) == 0;
+  const int64_t end = min(at + kNormRun, q.n);
+  double sum = 0.0;
+#pragma unroll 4
+  for (int64_t i = at + 8 * threadIdx.x; i < end; i += 8 * kAdamThreads) {
+    const int left = (int)min((int64_t)8, end - i);
+    float g[8];
+    get8<GBF>(q.grad, i, left, vec && left == 8, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)g[e] * (double)g[e];
+  }
+  sum = block_sum(sum, lds, kAdamThreads / 64);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+__global__ __launch_bounds__(1024) void k_adamw_norm(const double* __restrict__ part, int64_t n, float max_norm,
+                                                     float* __restrict__ out) {
+  __shared__ double lds[16];
+  double sum = 0.0;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x; i < n; i += 1024) sum += part[i];
+  sum = block_sum(sum, lds, 16);
+  if (threadIdx.x != 0) return;
+  const float norm = (float)sqrt(sum);
+  out[0] = norm;
+  out[1] = !(norm <= 3.402823466e38f) ? NAN : norm > max_norm ? max_norm / norm : 1.0f;
+}
+
+// ---------------------------------------------------------------- launches
+// Tensors by batches of kTensors and of fewer than 2^23 blocks.
+template <int RUN, typename Launch>
+static hipError_t adam_batches(const ds4moe_param* p, int n, Launch launch) {
+  constexpr int64_t kMost = 1 << 23;
+  AdamBatch b;
+  b.n = 0;
+  b.start[0] = 0;
+  int64_t done = 0;  // runs of the batches before
+  auto flush = [&]() -> hipError_t {
+    if (b.n == 0) return hipSuccess;
+    const hipError_t e = launch(b, done);
+    done += b.start[b.n];
+    b.n = 0;
+    return e;
+  };
+  for (int i = 0; i < n; ++i) {
+    const int64_t runs = runs_of<RUN>(p[i].n);
+    for (int64_t r = 0; r < runs;) {
+      const int64_t take = std::min(runs - r, kMost - b.start[b.n]);
+      if (b.n == kTensors || take <= 0) {
+        const hipError_t e = flush();
+        if (e) return e;
+        continue;
+      }
+      b.p[b.n] = p[i];
+      b.first[b.n] = r;
+      b.start[b.n + 1] = b.start[b.n] + (int)take;
+      ++b.n;
+      r += take;
+    }
+  }
+  return flush();
+}
+
+template <bool PBF, bool GBF, bool FP8>
+static hipError_t adam_step(const AdamCall& c) {
+  AdamScalars s{};
+  const ds4moe_adamw& A = c.A;
+  s.b1 = (float)A.beta1;
+  s.b1m = (float)(1.0 - A.beta1);
+  s.b2 = (float)A.beta2;
+  s.b2m = (float)(1.0 - A.beta2);
+  s.eps = (float)A.eps;
+  s.lr = A.lr;
+  s.log_b1 = std::log(A.beta1);
+  s.log_b2 = std::log(A.beta2);
+  s.c1 = -std::expm1(c.step * s.log_b1);
+  s.c2 = -std::expm1(c.step * s.log_b2);
+  s.lr_dev = A.lr_dev;
+  s.step_dev = A.step_dev;
+  s.grad_scale = c.grad_scale;
+  return adam_batches<kAdamRun>(c.p, c.n, [&](const AdamBatch& b, int64_t) {
+    DS4_LAUNCH((k_adamw<PBF, GBF, FP8>), dim3((unsigned)b.start[b.n]), dim3(kAdamThreads), 0, c.st, b, s);
+    return hipGetLastError();
+  });
+}
+template <bool PBF, bool GBF>
+static hipError_t adam_step_state(const AdamCall& c) {
+  return c.A.state == DS4MOE_STATE_FP8 ? adam_step<PBF, GBF, true>(c) : adam_step<PBF, GBF, false>(c);
+}
+template <bool PBF>
+static hipError_t adam_step_grad(const AdamCall& c) {
+  return c.A.grad_dtype == DS4MOE_DT_BF16 ? adam_step_state<PBF, true>(c) : adam_step_state<PBF, false>(c);
+}
+hipError_t launch_adamw_step(const AdamCall& c) {
+  return c.A.param_dtype == DS4MOE_DT_BF16 ? adam_step_grad<true>(c) : adam_step_grad<false>(c);
+}
+
+template <bool GBF>
+static hipError_t adam_norm(const AdamCall& c) {
+  int64_t runs = 0;
+  const hipError_t e = adam_batches<kNormRun>(c.p, c.n, [&](const AdamBatch& b, int64_t done) {
+    DS4_LAUNCH((k_adamw_squares<GBF>), dim3((unsigned)b.start[b.n]), dim3(kAdamThreads), 0, c.st, b, c.ws + done);
+    runs = done + b.start[b.n];
+    return hipGetLastError();
+  });
+  if (e) return e;
+  DS4_LAUNCH(k_adamw_norm, dim3(1), dim3(1024), 0, c.st, (const double*)c.ws, runs, c.max_norm, c.out);
+  return hipGetLastError();
+}
+hipError_t launch_adamw_norm(const AdamCall& c) {
+  return c.A.grad_dtype == DS4MOE_DT_BF16 ? adam_norm<true>(c) : adam_norm<false>(c);
+}
+
+}  // namespace ds4

@@ -1,0 +1,568 @@
+// Softmax cross entropy of rows h [T][d] against a vocabulary w [V][d], in
+// pieces of the vocabulary and without keeping the logits:
+//
+//   z = scale h w^T,  lse = log sum_v e^z_v,  loss = lse - z_target
+//   ds = dloss scale (e^(z - lse) - [v = target]),  dh = ds w,  dw = ds^T h
+//
+// Forward: a tile of the product leaves, for each of its rows, the maximum and
+// the sum of e^(z - maximum) over its words, and a second kernel joins them.
+// Backward: for each piece, the product again with ds as its epilogue (bfloat16,
+// or three planes of it for fp32), then the two products with ds.  Rows without
+// a target take no part: those that do are copied together first, so a masked
+// prompt costs nothing and what its rows hold (NaN, too) reaches nothing.  ds is
+// held over the largest |dloss scale|, by which the products are multiplied in
+// fp32: 1 / rows, which most losses have there, would otherwise be rounded the
+// same way in every value (dh 0.0034 off, against 0.002).
+#include <algorithm>
+
+#include "../trace.h"
+#include "../ops/rowtile.h"
+#include "xgemm.h"
+
+namespace ds4 {
+
+// ---------------------------------------------------------------- workspace
+// What grows with rows and words is bounded by taking words a piece at a time
+// (ds, and the planes of an fp32 w) and, in the forward pass, rows (the partial
+// sums).
+constexpr int64_t kXentPiece = 128 << 20;   // bytes that either aims at
+constexpr int kXentSlabs = 4;               // parts of the sum over words in dh, at most
+
+template <typename T>
+static T round_up(T v, T m) {
+  return (v + m - 1) / m * m;
+}
+
+struct XentPlan {
+  int parts;          // bfloat16 planes of an operand
+  int64_t piece;      // words of a piece, a multiple of 256
+  int pieces;
+  int64_t rows;       // rows of a forward pass over the vocabulary
+  int slabs;
+  // offsets into the workspace
+  size_t hc, wp, n, live, y, lse, g, ds, slab, zt, part, bytes;
+};
+
+static bool xent_small(int64_t T) { return T <= 64; }  // tiles of 32 rows, 32 words a wave
+
+static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
+  XentPlan p{};
+  p.parts = dt == DS4MOE_DT_F32 ? 3 : 1;
+  // bytes per word of what a piece keeps: ds, and the planes of an fp32 w
+  const int64_t per = 2 * p.parts * std::max<int64_t>(grad ? T : 0, p.parts == 3 ? d : 0);
+  const int64_t all = round_up<int64_t>(V, 256);
+  int64_t most = per ? std::max<int64_t>(2048, kXentPiece / per / 256 * 256) : all;
+  p.pieces = (int)((all + most - 1) / most);
+  p.piece = round_up<int64_t>((all + p.pieces - 1) / p.pieces, 256);
+  p.pieces = (int)((all + p.piece - 1) / p.piece);
+  p.slabs = 1;
+  if (grad) {
+    const int64_t tiles = (T + 127) / 128 * ((d + 127) / 128);
+    while (p.slabs < kXentSlabs && tiles * p.slabs < 512 && p.piece / p.slabs >= 2048) p.slabs *= 2;
+  }
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round_up<size_t>(bytes, 256);
+    return here;
+  };
+  if (p.parts == 3 || grad) p.hc = take((size_t)2 * p.parts * T * d);
+  if (p.parts == 3) p.wp = take((size_t)6 * p.piece * d);
+  if (grad) {
+    p.n = take(8);
+    p.live = take(4 * T);
+    p.y = take(4 * T);
+    p.lse = take(4 * T);
+    p.g = take(4 * T);
+    p.ds = take((size_t)2 * p.parts * T * p.piece);
+    p.slab = take((size_t)4 * p.slabs * T * d);
+  } else {
+    const int64_t parts = all / (xent_small(T) ? 32 : 64);
+    p.rows = std::min(T, std::max<int64_t>(1024, kXentPiece / (8 * parts) / 256 * 256));
+    p.zt = take(4 * p.rows);
+    p.part = take((size_t)8 * p.rows * parts);
+  }
+  p.bytes = at;
+  return p;
+}
+size_t xent_ws_bytes(int dt, int64_t T, int64_t V, int d, bool grad) { return xent_plan(dt, T, V, d, grad).bytes; }
+
+// ---------------------------------------------------------------- rows that have a target
+// live: the rows with a target in order, then the others from the end; n: how
+// many; y, lse, g: theirs; top: the largest |g|, or 1.  One block: rows are
+// few beside the products.
+__global__ __launch_bounds__(1024) void k_xent_live(const int32_t* __restrict__ target, int T, int V, float scale,
+                                                    const float* __restrict__ lse, const float* __restrict__ dloss,
+                                                    int32_t* __restrict__ n, int32_t* __restrict__ live,
+                                                    int32_t* __restrict__ y, float* __restrict__ lse_c,
+                                                    float* __restrict__ g_c) {
+  __shared__ int sums[2][16];
+  __shared__ float tops[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  float top = 0.f;
+  for (int t0 = 0, b = 0; t0 < T; t0 += 1024, b ^= 1) {
+    const int t = t0 + tid;
+    const int v = t < T ? target[t] : -1;
+    const bool on = v >= 0 && v < V;
+    const uint64_t m = __ballot(on);
+    if (lane == 0) sums[b][wave] = __popcll(m);
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? sums[b][w] : 0;
+      total += sums[b][w];
+    }
+    const int at = base + before + __popcll(m & ((1ull << lane) - 1));
+    if (on) {
+      const float g = scale * (dloss ? dloss[t] : 1.0f);
+      live[at] = t;
+      y[at] = v;
+      lse_c[at] = lse[t];
+      g_c[at] = g;
+      top = fmaxf(top, fabsf(g));
+    } else if (t < T) {
+      live[T - 1 - (t - at)] = t;  // t - at rows without a target lie before it
+    }
+    base += total;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  if (tid != 0) return;
+  for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w]);
+  n[0] = base;
+  // a range that its reciprocal stays within, too
+  ((float*)n)[1] = top >= 1.17549435e-38f && top <= 8.507059e37f ? top : 1.0f;
+}
+
+// x as three bfloat16 values whose sum it is (8 + 8 + 8 bits, by truncation;
+// what lies under 2^-133 is lost).  An infinity or a NaN is its first part.
+__device__ inline void xsplit8(const float (&x)[8], u32x4_t (&o)[3]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float a = __builtin_canonicalizef(x[2 * p]), b = __builtin_canonicalizef(x[2 * p + 1]);
+    const bool fa = fabsf(a) <= 3.402823466e38f, fb = fabsf(b) <= 3.402823466e38f;
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
+      o[s][p] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+      a -= __builtin_bit_cast(float, ua & 0xFFFF0000u);
+      b -= __builtin_bit_cast(float, ub & 0xFFFF0000u);
+      if (s == 0) {
+        a = fa ? a : 0.f;
+        b = fb ? b : 0.f;
+      }
+    }
+  }
+}
+
+// Rows of src (live[r], or r itself) side by side, as planes; dh of a row
+// without a target is zero.  A block takes a row.
+template <bool BF>
+__global__ __launch_bounds__(256) void k_xent_rows(const void* __restrict__ src, const int32_t* __restrict__ n,
+                                                   const int32_t* __restrict__ live, int64_t rows, int d,
+                                                   uint8_t* __restrict__ dst, int64_t plane, void* __restrict__ dh) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int64_t from = live ? live[r] : r;
+    const bool on = !n || r < *n;
+    for (int i = 8 * threadIdx.x; i < d; i += 2048) {
+      if (on) {
+        const Raw8<BF> v = ld8<BF>(src, from * d + i);
+        if constexpr (BF) {
+          *(u32x4_t*)(dst + (r * d + i) * 2) = v.a;
+        } else {
+          float x[8];
+          u32x4_t o[3];
+          unpack8<BF>(v, x);
+          xsplit8(x, o);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + (r * d + i) * 2) = o[s];
+        }
+      } else if (dh) {
+        const float zero[8] = {};
+        st8<BF>(dh, from * d + i, zero);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+struct XArgs {
+  XOperand a, b;
+  int64_t a_rows, b_rows;  // how many a's and b's there are (b's: at most)
+  int64_t K;
+  const int32_t* n;  // live rows, backward: b's, or the k of dw
+  int splits;        // of k
+  // epilogues
+  float scale;
+  int V;             // words of the piece
+  const int32_t* y;
+  int v0;            // the piece's first word
+  int rows;          // partial sums: rows of one
+  float2* part;
+  float* zt;
+  const float *lse, *g, *top;
+  uint8_t* out;
+  int64_t out_pitch, out_plane;  // bytes
+  bool add;
+};
+enum { XE_SUM = 0, XE_DS = 1, XE_ROWS = 2, XE_SLAB = 3 };
+
+// Tile of this block: (split, a tile, b tile).  Each XCD takes a contiguous run
+// of them (block_item), in which four a tiles meet all b tiles before the next
+// four: the 32 blocks that an XCD runs at once read 4 + 8 tiles' operands.
+__device__ inline bool xtile(int ta, int tb, int splits, int& a, int& b, int& s) {
+  int64_t item;
+  if (!block_item((int64_t)ta * tb * splits, item)) return false;
+  const int per = ta * tb;
+  s = (int)(item / per);
+  const int left = (int)(item - (int64_t)s * per);
+  const int g = left / (4 * tb), in = left - g * 4 * tb;
+  const int wide = min(4, ta - 4 * g);
+  b = in / wide;
+  a = 4 * g + in - b * wide;
+  return true;
+}
+
+template <class S, int EPI, int PARTS, bool OBF>
+__global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(XArgs x) {
+  constexpr bool ACOL = EPI == XE_ROWS || EPI == XE_SLAB, BCOL = EPI == XE_ROWS;
+  extern __shared__ uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int64_t b_rows = x.b_rows, K = x.K;
+  if (x.n) {
+    const int64_t n = ld_uniform(x.n);
+    if constexpr (BCOL) K = n;
+    else b_rows = n;
+  }
+  if (b_rows <= 0) return;
+  int ta, tb, s;
+  if (!xtile((int)((x.a_rows + S::BM - 1) / S::BM), (int)((b_rows + S::BN - 1) / S::BN), x.splits, ta, tb, s)) return;
+  const int64_t a0 = (int64_t)ta * S::BM, b0 = (int64_t)tb * S::BN;
+  XSide<S::BM, ACOL> A;
+  XSide<S::BN, BCOL> B;
+  A.init(x.a, a0, x.a_rows, tid);
+  B.init(x.b, b0, b_rows, tid);
+  const int nk = (int)((K + 63) / 64);
+  const int kc0 = (int)((int64_t)nk * s / x.splits), kc1 = (int)((int64_t)nk * (s + 1) / x.splits);
+  float16_t acc[S::FM][S::FN] = {};
+  xgemm<S, ACOL, BCOL, PARTS>(A, B, K, kc0, kc1, smem, acc, wave, lane);
+
+  const int am = (wave % S::WM) * 32 * S::FM, bn = (wave / S::WM) * 32 * S::FN;
+  if constexpr (EPI == XE_SUM) {
+    const int a1 = (int)a0 + am;  // the wave's first word of the piece
+    const int left = x.V - a1;    // and how many there are from it on
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i) {
+      const int64_t t = b0 + bn + 32 * i + c;
+      const bool on = t < b_rows;
+      float m = -INFINITY;
+#pragma unroll
+      for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int w = 32 * f + 8 * (v >> 2) + 4 * h + (v & 3);
+          float z = x.scale * acc[f][i][v];
+          z = w < left ? z : -INFINITY;
+          acc[f][i][v] = z;
+          m = fmaxf(m, z);
+        }
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float mm = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+#pragma unroll
+      for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) sum += __expf(acc[f][i][v] - mm);
+      sum += __shfl_xor(sum, 32);
+      if (on && left > 0 && h == 0) x.part[(int64_t)((x.v0 + a1) / (32 * S::FM)) * x.rows + t] = float2{m, sum};
+      const int y = on ? x.y[t] - x.v0 - a1 : -1;  // the target among the wave's words
+      const bool mine = y >= 0 && y < 32 * S::FM && y < left && ((y >> 2) & 1) == h;
+      if (__ballot(mine)) {
+        float z = 0.f;
+#pragma unroll
+        for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) z = y == 32 * f + 8 * (v >> 2) + 4 * h + (v & 3) ? acc[f][i][v] : z;
+        if (mine) x.zt[t] = z;
+      }
+    }
+  } else if constexpr (EPI == XE_DS) {
+    // words past the vocabulary's end are zeros: the products with ds run over whole pieces
+    uint8_t* const turn = smem + wave * 32 * xturn_pitch<S::FM, 2>();
+    const int left = x.V - (int)a0 - am;
+    const float by = 1.0f / *x.top;
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i) {
+      const int64_t t = b0 + bn + 32 * i + c;
+      const bool on = t < b_rows;
+      const float lse = on ? x.lse[t] : 0.f, g = on ? x.g[t] * by : 0.f;
+      const int y = on ? x.y[t] - x.v0 - (int)a0 - am : -1;
+#pragma unroll
+      for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int w = 32 * f + 8 * (v >> 2) + 4 * h + (v & 3);
+          const float p = __expf(x.scale * acc[f][i][v] - lse) - (w == y ? 1.f : 0.f);
+          acc[f][i][v] = w < left ? g * p : 0.f;
+        }
+      // by planes: what the bfloat16 before leaves
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        xturn<S::FM, 2>(
+            turn, lane, [&](int f, int v) { return acc[f][i][v]; },
+            [&](int row, int ch, u32x4_t v) {
+              const int64_t r = b0 + bn + 32 * i + row;
+              if (r < b_rows) *(u32x4_t*)(x.out + q * x.out_plane + r * x.out_pitch + (a0 + am) * 2 + ch * 16) = v;
+            });
+        if (q + 1 < PARTS) {
+#pragma unroll
+          for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+            for (int v = 0; v < 16; v += 2) {
+              const uint32_t b = bf16_pair(acc[f][i][v], acc[f][i][v + 1]);
+              acc[f][i][v] -= __builtin_bit_cast(float, b << 16);
+              acc[f][i][v + 1] -= __builtin_bit_cast(float, b & 0xFFFF0000u);
+            }
+        }
+      }
+    }
+  } else {
+    constexpr int ES = EPI == XE_ROWS && OBF ? 2 : 4;
+    uint8_t* const turn = smem + wave * 32 * xturn_pitch<S::FM, ES>();
+    uint8_t* const out = x.out + s * x.out_plane;
+    const float by = EPI == XE_ROWS ? *x.top : 1.f;
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i)
+      xturn<S::FM, ES>(
+          turn, lane, [&](int f, int v) { return EPI == XE_ROWS ? by * acc[f][i][v] : acc[f][i][v]; },
+          [&](int row, int ch, u32x4_t v) {
+            const int64_t r = b0 + bn + 32 * i + row;
+            if (r >= b_rows) return;
+            u32x4_t* at = (u32x4_t*)(out + r * x.out_pitch + (a0 + am) * ES + ch * 16);
+            if (EPI == XE_SLAB && x.add)
+              *(float4_t*)at = *(const float4_t*)at + __builtin_bit_cast(float4_t, v);
+            else
+              *at = v;
+          });
+  }
+}
+
+// ---------------------------------------------------------------- joins
+// loss and lse of the rows from their partial sums: 32 rows by 32 shares of
+// the parts to a block.
+__device__ inline void xent_add(float& m, float& sum, bool& nan, float2 v) {
+  const float top = fmaxf(m, v.x), mm = top == -INFINITY ? 0.f : top;
+  sum = sum * __expf(m - mm) + v.y * __expf(v.x - mm);
+  nan |= v.y != v.y;
+  m = top;
+}
+__global__ __launch_bounds__(1024) void k_xent_join(const float2* __restrict__ part, int parts, int64_t rows,
+                                                    const int32_t* __restrict__ target, int V,
+                                                    const float* __restrict__ zt, float* __restrict__ loss,
+                                                    float* __restrict__ lse) {
+  __shared__ float2 lds[32][33];
+  const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
+  const int64_t r = (int64_t)blockIdx.x * 32 + c;
+  const bool on = r < rows;
+  float m = -INFINITY, sum = 0.f;
+  bool nan = false;
+  if (on) {
+#pragma unroll 8
+    for (int p = s; p < parts; p += 32) xent_add(m, sum, nan, part[(int64_t)p * rows + r]);
+  }
+  lds[s][c] = float2{m, nan ? NAN : sum};
+  __syncthreads();
+  if (s != 0 || !on) return;
+  for (int i = 1; i < 32; ++i) xent_add(m, sum, nan, lds[i][c]);
+  const float l = nan ? NAN : m + logf(sum);
+  lse[r] = l;
+  const int y = target[r];
+  loss[r] = y >= 0 && y < V ? l - zt[r] : 0.f;
+}
+
+// dh of the live rows from the slabs.
+template <bool BF>
+__global__ __launch_bounds__(256) void k_xent_dh(const float* __restrict__ slab, int slabs, int64_t stride,
+                                                 const int32_t* __restrict__ n, const int32_t* __restrict__ live,
+                                                 int d, const float* __restrict__ top, void* __restrict__ dh) {
+  const int rows = *n;
+  const float by = *top;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int64_t t = live[r];
+    for (int i = 8 * threadIdx.x; i < d; i += 2048) {
+      float v[8];
+      unpack8<false>(ld8<false>(slab, r * d + i), v);
+      for (int s = 1; s < slabs; ++s) {
+        float u[8];
+        unpack8<false>(ld8<false>(slab + s * stride, r * d + i), u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += u[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= by;
+      st8<BF>(dh, t * d + i, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- launches
+using XBig = XShape<2, 2, 4, 4, 2>;    // 256 x 256
+using XMid = XShape<2, 2, 2, 2, 2>;    // 128 x 128, two blocks to a CU
+using XFew = XShape<4, 1, 1, 1, 3>;    // 128 a's x 32 b's, two blocks to a CU
+
+template <class S, int EPI, int PARTS, bool OBF>
+static hipError_t xent_launch(const XArgs& x, hipStream_t st) {
+  const int64_t blocks = (x.a_rows + S::BM - 1) / S::BM * ((x.b_rows + S::BN - 1) / S::BN) * x.splits;
+  DS4_LAUNCH((k_xent_gemm<S, EPI, PARTS, OBF>), dim3((unsigned)blocks), dim3(256), S::lds, st, x);
+  return hipGetLastError();
+}
+template <int EPI, int PARTS, bool OBF>
+static hipError_t xent_gemm(const XArgs& x, hipStream_t st) {
+  const int64_t big = (x.a_rows + 255) / 256 * ((x.b_rows + 255) / 256) * x.splits;
+  if (big >= 192) return xent_launch<XBig, EPI, PARTS, OBF>(x, st);
+  return xent_launch<XMid, EPI, PARTS, OBF>(x, st);
+}
+static unsigned xent_row_blocks(int64_t rows) { return (unsigned)std::min<int64_t>(rows, 8192); }
+
+// all rows of an fp32 matrix as planes
+static void xent_copy(const void* src, int64_t rows, int d, uint8_t* dst, int64_t plane, hipStream_t st) {
+  DS4_LAUNCH(k_xent_rows<false>, dim3(xent_row_blocks(rows)), dim3(256), 0, st, src, (const int32_t*)nullptr,
+             (const int32_t*)nullptr, rows, d, dst, plane, (void*)nullptr);
+}
+
+template <int PARTS>
+static hipError_t xent_forward(const XentCall& c) {
+  const XentPlan p = xent_plan(c.dt, c.T, c.V, c.d, false);
+  uint8_t* w = c.ws;
+  const bool few = xent_small(c.T);
+  const int per = few ? 32 : 64;  // words of a partial sum
+  const int64_t pitch = 2 * (int64_t)c.d;
+  const uint8_t* h = (const uint8_t*)c.h;
+  if (PARTS == 3) {
+    xent_copy(c.h, c.T, c.d, w + p.hc, c.T * pitch, c.st);
+    h = w + p.hc;
+  }
+  for (int64_t r0 = 0; r0 < c.T; r0 += p.rows) {
+    const int64_t rows = std::min(c.T - r0, p.rows);
+    for (int i = 0; i < p.pieces; ++i) {
+      const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
+      const uint8_t* src = (const uint8_t*)c.w + v0 * pitch * (PARTS == 3 ? 2 : 1);
+      XArgs x{};
+      x.a = {src, 0, pitch};
+      if (PARTS == 3) {
+        xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
+        x.a = {w + p.wp, p.piece * pitch, pitch};
+      }
+      x.b = {h + r0 * pitch, c.T * pitch, pitch};
+      x.a_rows = words;
+      x.b_rows = rows;
+      x.K = c.d;
+      x.splits = 1;
+      x.scale = c.scale;
+      x.V = (int)words;
+      x.y = c.target + r0;
+      x.v0 = (int)v0;
+      x.rows = (int)rows;
+      x.part = (float2*)(w + p.part);
+      x.zt = (float*)(w + p.zt);
+      const hipError_t e = few ? xent_launch<XFew, XE_SUM, PARTS, false>(x, c.st) : xent_launch<XMid, XE_SUM, PARTS, false>(x, c.st);
+      if (e) return e;
+    }
+    DS4_LAUNCH(k_xent_join, dim3((unsigned)((rows + 31) / 32)), dim3(1024), 0, c.st, (const float2*)(w + p.part),
+               (int)((c.V + per - 1) / per), rows, c.target + r0, (int)c.V, (const float*)(w + p.zt), c.loss + r0,
+               c.lse + r0);
+  }
+  return hipGetLastError();
+}
+
+template <int PARTS>
+static hipError_t xent_backward(const XentCall& c) {
+  constexpr bool BF = PARTS == 1;
+  const XentPlan p = xent_plan(c.dt, c.T, c.V, c.d, true);
+  uint8_t* w = c.ws;
+  const int64_t pitch = 2 * (int64_t)c.d;
+  int32_t* const n = (int32_t*)(w + p.n);
+  int32_t* const live = (int32_t*)(w + p.live);
+  hipError_t e;
+  DS4_LAUNCH(k_xent_live, dim3(1), dim3(1024), 0, c.st, c.target, (int)c.T, (int)c.V, c.scale, c.lse_in, c.dloss, n, live,
+             (int32_t*)(w + p.y), (float*)(w + p.lse), (float*)(w + p.g));
+  DS4_LAUNCH((k_xent_rows<PARTS == 1>), dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, c.h, (const int32_t*)n,
+             (const int32_t*)live, c.T, c.d, w + p.hc, c.T * pitch, c.dh);
+  for (int i = 0; i < p.pieces; ++i) {
+    const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
+    const uint8_t* src = (const uint8_t*)c.w + v0 * pitch * (PARTS == 3 ? 2 : 1);
+    XOperand wop = {src, 0, pitch};
+    if (PARTS == 3) {
+      xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
+      wop = {w + p.wp, p.piece * pitch, pitch};
+    }
+    const XOperand hop = {w + p.hc, c.T * pitch, pitch}, dsop = {w + p.ds, 2 * c.T * p.piece, 2 * p.piece};
+    XArgs x{};
+    x.a = wop;
+    x.b = hop;
+    x.a_rows = words;
+    x.b_rows = c.T;
+    x.K = c.d;
+    x.n = n;
+    x.splits = 1;
+    x.scale = c.scale;
+    x.V = (int)words;
+    x.y = (const int32_t*)(w + p.y);
+    x.v0 = (int)v0;
+    x.lse = (const float*)(w + p.lse);
+    x.g = (const float*)(w + p.g);
+    x.top = (const float*)n + 1;
+    x.out = w + p.ds;
+    x.out_pitch = 2 * p.piece;
+    x.out_plane = 2 * c.T * p.piece;
+    // the last tile's words past the end are written too: as zeros
+    if ((e = xent_gemm<XE_DS, PARTS, false>(x, c.st))) return e;
+    if (c.dh) {
+      XArgs u{};
+      u.a = wop;
+      u.b = dsop;
+      u.a_rows = c.d;
+      u.b_rows = c.T;
+      u.K = words;
+      u.n = n;
+      u.splits = p.slabs;
+      u.out = w + p.slab;
+      u.out_pitch = 4 * (int64_t)c.d;
+      u.out_plane = 4 * c.T * c.d;
+      u.add = i > 0;
+      if ((e = xent_gemm<XE_SLAB, PARTS, false>(u, c.st))) return e;
+    }
+    if (c.dw) {
+      XArgs u{};
+      u.a = hop;
+      u.b = dsop;
+      u.a_rows = c.d;
+      u.b_rows = words;
+      u.K = c.T;
+      u.n = n;
+      u.top = (const float*)n + 1;
+      u.splits = 1;
+      u.out = (uint8_t*)c.dw + v0 * c.d * (BF ? 2 : 4);
+      u.out_pitch = c.d * (int64_t)(BF ? 2 : 4);
+      if ((e = xent_gemm<XE_ROWS, PARTS, BF>(u, c.st))) return e;
+    }
+  }
+  if (c.dh)
+    DS4_LAUNCH(k_xent_dh<BF>, dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, (const float*)(w + p.slab), p.slabs,
+               c.T * (int64_t)c.d, (const int32_t*)n, (const int32_t*)live, c.d, (const float*)n + 1, c.dh);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent(const XentCall& c) {
+  return c.dt == DS4MOE_DT_F32 ? xent_forward<3>(c) : xent_forward<1>(c);
+}
+hipError_t launch_xent_grad(const XentCall& c) {
+  return c.dt == DS4MOE_DT_F32 ? xent_backward<3>(c) : xent_backward<1>(c);
+}
+
+}  // namespace ds4

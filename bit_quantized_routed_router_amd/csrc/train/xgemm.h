@@ -1,0 +1,203 @@
+// The products of the cross entropy on v_mfma_f32_32x32x16_bf16:
+//
+//   acc[a][b] = sum_k A[a][k] B[b][k]
+//
+// over tiles of BM a's by BN b's, four waves, both operands through LDS a
+// chunk of 64 k at a time with R chunks in the ring.  An operand lies in
+// memory either by rows (k contiguous: 128 bytes of a row per chunk) or by
+// columns (its own index contiguous: 64 rows of the tile's width per chunk,
+// turned by the transposing LDS read).  fp32 operands come as three bfloat16
+// planes whose sum they are, and a chunk is multiplied six times: hi hi, hi
+// mid, mid hi, mid mid, hi lo, lo hi.  What is left out is below 2^-24 of the
+// product, fp32's own rounding.
+//
+// LDS: 16-byte pieces, swizzled on their way in by choosing which piece a
+// lane copies.  By rows piece p of row r lies at p ^ (r / 2 & 7), so that the
+// 16 rows that a quarter of a wave reads lie in different banks; by columns
+// piece p of row k lies at p ^ 2 (k & 7), since a quarter reads two
+// neighbouring pieces of four rows.
+#pragma once
+
+#include "../ring.h"
+#include "train.h"
+
+namespace ds4 {
+
+typedef float float16_t __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+__device__ inline float16_t mfma32(u32x4_t a, u32x4_t b, float16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
+}
+
+// waves along a and b, 32x32 fragments of a wave along both, chunks in the ring
+template <int WM_, int WN_, int FM_, int FN_, int R_>
+struct XShape {
+  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, R = R_;
+  static constexpr int BM = 32 * WM * FM, BN = 32 * WN * FN;
+  static constexpr int slot = (BM + BN) * 128, lds = R * slot;
+  static constexpr int copies = (BM + BN) / 32;  // a thread's copies per chunk
+  static_assert(WM * WN == 4 && lds <= 160 * 1024 && (R - 2) * copies < 64, "four waves, LDS, copies in flight");
+};
+
+struct XOperand {
+  const uint8_t* p;
+  int64_t plane;  // bytes from one bfloat16 plane to the next
+  int64_t pitch;  // bytes of a row (a k of an operand by columns); 256 of them below 2^31
+};
+
+// One operand's side of a tile of B indices, from index i0 on.
+template <int B, bool COL>
+struct XSide {
+  static constexpr int NF = B / 32;
+  const uint8_t* base;
+  int64_t plane, pitch;
+  uint32_t records;  // by rows: bytes that the tile has; by columns: what a row's end leaves out
+  uint32_t vo;       // the lane's piece
+  __device__ inline void init(const XOperand& o, int64_t i0, int64_t rows, int tid) {
+    plane = o.plane;
+    pitch = o.pitch;
+    if constexpr (!COL) {
+      base = o.p + i0 * pitch;
+      records = (uint32_t)((rows - i0 < B ? rows - i0 : B) * pitch);
+      const int r = tid >> 3;
+      vo = (uint32_t)(r * pitch) + ((tid ^ (r >> 1)) & 7) * 16;
+    } else {
+      constexpr int P = B / 8;  // pieces of a row
+      base = o.p + i0 * 2;
+      records = (uint32_t)i0 * 2;
+      const int k = tid / P, p = tid % P;
+      vo = (uint32_t)(k * pitch) + ((p ^ (2 * (k & 7))) & (P - 1)) * 16;
+    }
+  }
+  // chunk kc of plane q into LDS at dst; K: how many k there are
+  __device__ __attribute__((always_inline)) inline void issue(int kc, int q, int64_t K, bool on, uint8_t* dst,
+                                                              int wave) const {
+    const uint8_t* src = base + q * plane;
+    uint32_t n = records;
+    if constexpr (COL) {
+      src += (int64_t)kc * 64 * pitch;
+      const int64_t left = K - (int64_t)kc * 64;
+      n = left > 0 ? (uint32_t)((left < 64 ? left : 64) * pitch) - records : 0;
+    }
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(src, n);
+    constexpr int step = COL ? 2048 / B : 32;  // rows from one copy to the next
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (__attribute__((address_space(3))) void*)(dst + i * 4096 + wave * 1024), 16, on ? (int)vo : (int)kOob,
+          (int)(i * step * pitch) + (COL ? 0 : kc * 128), 0, 0);
+  }
+  // Fragment f (32 indices from first on) of step j (16 k): lane l gets index
+  // l & 31 and k 8 (l >> 5) .. + 7.
+  static __device__ __attribute__((always_inline)) inline u32x4_t read(const uint8_t* at, int first, int f, int j,
+                                                                       int lane) {
+    if constexpr (!COL) {
+      const int c = lane & 31, h = lane >> 5;
+      return *(const u32x4_t*)(at + (first + 32 * f + c) * 128 + (((2 * j + h) ^ (c >> 1)) & 7) * 16);
+    } else {
+      // Of a quarter's 16 lanes, four hold 16 neighbouring indices of one k,
+      // four k in all; the read hands lane i index i of the four.
+      constexpr int RB = B * 2, P = B / 8;
+      const int i = lane & 15, s = (lane >> 4) & 1, h = lane >> 5;
+      u32x4_t v;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int k = 4 * r + (i >> 2);  // its last three bits
+        const int piece = (first / 8 + 4 * f + 2 * s + ((i & 3) >> 1)) ^ ((2 * k) & (P - 1));
+        const u32x2_t x = __builtin_bit_cast(
+            u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(
+                         at + (16 * j + 8 * h + k) * RB + piece * 16 + 8 * (i & 1))));
+        v[2 * r] = x.x;
+        v[2 * r + 1] = x.y;
+      }
+      return v;
+    }
+  }
+};
+
+// Planes of a chunk's q-th product.
+__device__ inline int plane_a(int q) { return (0x200110 >> (4 * (5 - q))) & 3; }
+__device__ inline int plane_b(int q) { return (0x021010 >> (4 * (5 - q))) & 3; }
+
+// Chunks kc0 .. kc1 - 1 of the tile into acc[FM][FN] of this wave.
+template <class S, bool ACOL, bool BCOL, int PARTS>
+__device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, ACOL>& A, const XSide<S::BN, BCOL>& B,
+                                                            int64_t K, int kc0, int kc1, uint8_t* smem,
+                                                            float16_t (&acc)[S::FM][S::FN], int wave, int lane) {
+  constexpr int Q = PARTS == 3 ? 6 : 1;
+  const int n = (kc1 - kc0) * Q;
+  const int am = (wave % S::WM) * 32 * S::FM, bn = (wave / S::WM) * 32 * S::FN;
+  auto issue = [&](int ch, int u) __attribute__((always_inline)) {
+    const int kc = kc0 + ch / Q, q = ch % Q;
+    const int qa = PARTS == 3 ? plane_a(q) : 0, qb = PARTS == 3 ? plane_b(q) : 0;
+    uint8_t* dst = smem + u * S::slot;
+    A.issue(kc, qa, K, ch < n, dst, wave);
+    B.issue(kc, qb, K, ch < n, dst + S::BM * 128, wave);
+  };
+#pragma unroll
+  for (int u = 0; u < S::R - 1; ++u) issue(u, u);
+  int u = 0;
+#pragma unroll 1
+  for (int ch = 0; ch < n; ++ch) {
+    pin();
+    vm_wait<(S::R - 2) * S::copies>();  // this wave's copies of the chunk
+    ring_barrier();                      // everyone's, and everyone is done with the chunk before
+    pin();
+    issue(ch + S::R - 1, u == 0 ? S::R - 1 : u - 1);
+    pin();
+    const uint8_t* slot = smem + u * S::slot;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4_t fa[S::FM], fb[S::FN];
+#pragma unroll
+      for (int f = 0; f < S::FM; ++f) fa[f] = XSide<S::BM, ACOL>::read(slot, am, f, j, lane);
+#pragma unroll
+      for (int f = 0; f < S::FN; ++f) fb[f] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, f, j, lane);
+#pragma unroll
+      for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+        for (int f = 0; f < S::FM; ++f) acc[f][i] = mfma32(fa[f], fb[i], acc[f][i]);
+    }
+    u = u + 1 == S::R ? 0 : u + 1;
+  }
+  vm_wait<0>();
+  ring_barrier();
+}
+
+// A wave's 32 b's by 32 FM a's (fragment i of its b's) through its share of
+// LDS, so that runs of a are stored whole: put(f, g, four values) fills, and
+// store(row, piece, sixteen bytes) gets every piece of a row.
+template <int FM, int ES>
+constexpr int xturn_pitch() {
+  return 32 * FM * ES + 16;
+}
+template <int FM, int ES, typename Value, typename Store>
+__device__ __attribute__((always_inline)) inline void xturn(uint8_t* turn, int lane, Value value, Store store) {
+  constexpr int PITCH = xturn_pitch<FM, ES>(), LPR = 32 * FM * ES / 16;
+  const int c = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int f = 0; f < FM; ++f)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float4_t o;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) o[v] = value(f, 4 * g + v);
+      uint8_t* at = turn + c * PITCH + (32 * f + 8 * g + 4 * h) * ES;
+      if constexpr (ES == 2)
+        *(u32x2_t*)at = u32x2_t{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+      else
+        *(float4_t*)at = o;
+    }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int x = 0; x < 32 * LPR / 64; ++x) {
+    const int row = x * (64 / LPR) + lane / LPR, ch = lane % LPR;
+    store(row, ch, *(const u32x4_t*)(turn + row * PITCH + ch * 16));
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+}  // namespace ds4

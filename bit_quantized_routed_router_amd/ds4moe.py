@@ -21,6 +21,7 @@ DT_F32, DT_BF16 = 0, 1
 MODE_DECODE, MODE_PREFILL, MODE_ROUTE = 0, 1, 2
 DECODE_MAX_T = 64
 GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
+STATE_F32, STATE_FP8 = 0, 1
 
 
 class Ds4moeError(RuntimeError):
@@ -56,6 +57,24 @@ class NormDesc(ctypes.Structure):
     _fields_ = [
         ("d_model", ctypes.c_int32), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float), ("gate", ctypes.c_int32),
         ("w_pre", ctypes.c_void_p), ("w_post", ctypes.c_void_p), ("w_next", ctypes.c_void_p),
+    ]
+
+
+class ParamDesc(ctypes.Structure):
+    """Mirror of ds4moe_param."""
+    _fields_ = [
+        ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+        ("weight_decay", ctypes.c_double),
+    ]
+
+
+class AdamWDesc(ctypes.Structure):
+    """Mirror of ds4moe_adamw."""
+    _fields_ = [
+        ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
     ]
 
 
@@ -101,6 +120,11 @@ def lib() -> ctypes.CDLL:
         L.ds4moe_norm_workspace_bytes.argtypes = [NP, I64]
         L.ds4moe_group_workspace_bytes.restype = SZ
         L.ds4moe_group_workspace_bytes.argtypes = [I64, N32, N32]
+        AP, PP, F32 = ctypes.POINTER(AdamWDesc), ctypes.POINTER(ParamDesc), ctypes.c_float
+        for name, args in {"balance": [I64, N32, N32], "xent": [I32, I64, I64, N32, I32], "adamw": [PP, N32]}.items():
+            fn = getattr(L, f"ds4moe_{name}_workspace_bytes")
+            fn.restype = SZ
+            fn.argtypes = args
         for name, args in {
             "norm_pre": [NP, P, I32, I64, P, I32, P],
             "norm_post": [NP, P, I32, P, I32, P, I64, P, P, I32, P],
@@ -114,6 +138,12 @@ def lib() -> ctypes.CDLL:
             "mx_dequantize": [P, I64, N32, P, I32, P],
             "mx_product": [P, I64, N32, P, P, N32, N32, P, P, I32, P],
             "mx_product_grad": [P, I32, I64, N32, P, N32, N32, P, P, I32, P],
+            "balance": [P, I32, I64, N32, P, N32, P, N32, P, P, P, P, SZ, P],
+            "balance_grad": [P, I32, I64, N32, P, N32, P, N32, P, P, P, P, P, P],
+            "xent": [P, P, I32, I64, I64, N32, F32, P, P, P, P, SZ, P],
+            "xent_grad": [P, P, I32, I64, I64, N32, F32, P, P, P, P, P, P, SZ, P],
+            "adamw_step": [AP, PP, N32, I64, P, P],
+            "adamw_norm": [AP, PP, N32, F32, P, P, SZ, P],
         }.items():
             fn = getattr(L, "ds4moe_" + name)
             fn.restype = I32
@@ -138,7 +168,9 @@ EXPORTS = ["ds4moe_packed_bytes", "ds4moe_quantize", "ds4moe_dequantize", "ds4mo
            "ds4moe_norm_workspace_bytes", "ds4moe_norm_pre", "ds4moe_norm_post", "ds4moe_norm_pre_grad",
            "ds4moe_norm_post_grad", "ds4moe_group_workspace_bytes", "ds4moe_group", "ds4moe_dispatch",
            "ds4moe_combine", "ds4moe_combine_grad", "ds4moe_mx_quantize", "ds4moe_mx_dequantize",
-           "ds4moe_mx_product", "ds4moe_mx_product_grad"]
+           "ds4moe_mx_product", "ds4moe_mx_product_grad", "ds4moe_balance_workspace_bytes", "ds4moe_balance",
+           "ds4moe_balance_grad", "ds4moe_xent_workspace_bytes", "ds4moe_xent", "ds4moe_xent_grad",
+           "ds4moe_adamw_workspace_bytes", "ds4moe_adamw_step", "ds4moe_adamw_norm"]
 
 
 def strerror(status: int) -> str:
@@ -411,6 +443,135 @@ def mx_product_grad(dy, dy_dtype, n_rows, rows, w, cols, n_experts, offsets, da,
     _call("ds4moe_mx_product_grad", stream, (dy, n_rows * rows, dy_dtype), dy_dtype, n_rows, rows,
           (w, n_experts * _mx_bytes(rows, cols), _BYTES), cols, n_experts, (offsets, n_experts + 1, _I32),
           (da, n_rows * cols, da_dtype), da_dtype)
+
+
+# ---------------------------------------------------------------- a training step
+# The router's balance loss, the cross entropy against a vocabulary and AdamW:
+# thin calls as above.
+
+def balance_workspace_bytes(T: int, n_experts: int, n_seqs: int) -> int:
+    return int(lib().ds4moe_balance_workspace_bytes(T, n_experts, n_seqs))
+
+
+def balance(logits, l_dtype, T, n_experts, topk_idx, k, seq_offsets, n_seqs, counts, tokens, loss, ws, ws_bytes,
+            stream=None) -> None:
+    _call("ds4moe_balance", stream, (logits, T * n_experts, l_dtype), l_dtype, T, n_experts, (topk_idx, T * k, _I32), k,
+          (seq_offsets, n_seqs + 1, _I32), n_seqs, (counts, n_seqs * n_experts, _I32), (tokens, n_seqs, _I32),
+          (loss, n_seqs, DT_F32), (ws, ws_bytes, _BYTES), ws_bytes)
+
+
+def balance_grad(logits, l_dtype, T, n_experts, topk_idx, k, seq_offsets, n_seqs, counts, tokens, dloss, dslots, dlogits,
+                 stream=None) -> None:
+    n = T * n_experts
+    _call("ds4moe_balance_grad", stream, (logits, n, l_dtype), l_dtype, T, n_experts, (topk_idx, T * k, _I32), k,
+          (seq_offsets, n_seqs + 1, _I32), n_seqs, (counts, n_seqs * n_experts, _I32), (tokens, n_seqs, _I32),
+          (dloss, n_seqs, DT_F32), (dslots, T * k, DT_F32), (dlogits, n, l_dtype))
+
+
+def xent_workspace_bytes(dtype: int, T: int, vocab: int, d: int, with_grad: bool) -> int:
+    return int(lib().ds4moe_xent_workspace_bytes(dtype, T, vocab, d, int(with_grad)))
+
+
+def xent(h, w, dtype, T, vocab, d, scale, target, loss, lse, ws, ws_bytes, stream=None) -> None:
+    _call("ds4moe_xent", stream, (h, T * d, dtype), (w, vocab * d, dtype), dtype, T, vocab, d, scale, (target, T, _I32),
+          (loss, T, DT_F32), (lse, T, DT_F32), (ws, ws_bytes, _BYTES), ws_bytes)
+
+
+def xent_grad(h, w, dtype, T, vocab, d, scale, target, lse, dloss, dh, dw, ws, ws_bytes, stream=None) -> None:
+    _call("ds4moe_xent_grad", stream, (h, T * d, dtype), (w, vocab * d, dtype), dtype, T, vocab, d, scale,
+          (target, T, _I32), (lse, T, DT_F32), (dloss, T, DT_F32), (dh, T * d, dtype), (dw, vocab * d, dtype),
+          (ws, ws_bytes, _BYTES), ws_bytes)
+
+
+class AdamW:
+    """Tensors that AdamW updates (lists of equal length, CUDA tensors on one
+    GPU) plus the ds4moe_adamw descriptor and its ds4moe_param table.
+
+    params, grads: float32 or bfloat16, one type each; master: float32, or None
+    (for all, or in a tensor's place); m, v: float32, or torch.float8_e4m3fn (or
+    uint8) codes with m_scale and v_scale, float32 with one value for each 256.
+    weight_decay: one value, or one a tensor.  lr_dev float32 [1] and step_dev
+    int32 [1] on the GPU take lr's and the step's place (for captured graphs).
+    A step that gets its gradients in other tensors calls set_grads first."""
+
+    _TYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None, lr=1e-3, beta1=0.9, beta2=0.999,
+                 eps=1e-8, weight_decay=0.0, lr_dev=None, step_dev=None):
+        self.n = len(params)
+        self.gpu = None
+        fp8 = m_scale is not None or v_scale is not None
+        none = [None] * self.n
+        decay = [weight_decay] * self.n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        sizes = [p.numel() for p in params]
+        blocks = [(n + 255) // 256 for n in sizes]
+        state = (torch.float8_e4m3fn, torch.uint8) if fp8 else (torch.float32,)
+        f32 = (torch.float32,)
+        self.sizes = sizes
+        self.tensors = dict(
+            param=self._take("params", params, sizes, tuple(self._TYPES)),
+            grad=self._take("grads", grads, sizes, tuple(self._TYPES)),
+            master=self._take("master", none if master is None else master, sizes, f32, optional=True),
+            m=self._take("m", m, sizes, state), v=self._take("v", v, sizes, state),
+            m_scale=self._take("m_scale", m_scale, blocks, f32) if fp8 else none,
+            v_scale=self._take("v_scale", v_scale, blocks, f32) if fp8 else none)
+        if len(decay) != self.n:
+            raise ValueError("weight_decay: expected one value, or one a tensor")
+        for name, t, dtype in (("lr_dev", lr_dev, torch.float32), ("step_dev", step_dev, torch.int32)):
+            if t is not None:
+                self._take(name, [t], [1], (dtype,))
+        self.devices = (lr_dev, step_dev)
+        one = lambda ts: self._TYPES[ts[0].dtype] if ts else DT_F32  # noqa: E731
+        self.desc = AdamWDesc(one(params), one(grads), STATE_FP8 if fp8 else STATE_F32, lr, beta1, beta2, eps, _ptr(lr_dev),
+                              _ptr(step_dev))
+        self.table = (ParamDesc * max(self.n, 1))()
+        for i in range(self.n):
+            q = self.table[i]
+            for name, ts in self.tensors.items():
+                setattr(q, name, _ptr(ts[i]))
+            q.n, q.weight_decay = sizes[i], decay[i]
+
+    def _take(self, name, tensors, sizes, types, optional=False):
+        """The tensors as a list, if they are what a call takes."""
+        if tensors is None or len(tensors) != len(sizes):
+            raise ValueError(f"{name}: expected {len(sizes)} tensors")
+        tensors = list(tensors)
+        for t, n in zip(tensors, sizes):
+            if optional and t is None:
+                continue
+            if t.dtype not in types or t.dtype != tensors[0].dtype and not optional:
+                raise ValueError(f"{name}: a tensor of dtype {t.dtype}")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name}: expected {n} contiguous values, got {tuple(t.shape)}")
+            if not t.is_cuda or self.gpu not in (None, t.get_device()):
+                raise ValueError(f"{name}: expected all tensors on one GPU")
+            self.gpu = t.get_device()
+        return tensors
+
+    def set_grads(self, grads) -> None:
+        self.tensors["grad"] = self._take("grads", grads, self.sizes, tuple(self._TYPES))
+        if grads:
+            self.desc.grad_dtype = self._TYPES[grads[0].dtype]
+        for i, g in enumerate(self.tensors["grad"]):
+            self.table[i].grad = _ptr(g)
+
+    def workspace_bytes(self) -> int:
+        return int(lib().ds4moe_adamw_workspace_bytes(self.table, self.n))
+
+
+def _adamw_on_gpu(opt):
+    if opt.gpu is not None and opt.gpu != _current_gpu():
+        raise ValueError("the optimizer's tensors are not on the current GPU")
+    return opt.desc
+
+
+def adamw_step(opt: AdamW, step, grad_scale=None, stream=None) -> None:
+    _call("ds4moe_adamw_step", stream, _adamw_on_gpu(opt), opt.table, opt.n, step, (grad_scale, 1, DT_F32))
+
+
+def adamw_norm(opt: AdamW, max_norm, out, ws, ws_bytes, stream=None) -> None:
+    _call("ds4moe_adamw_norm", stream, _adamw_on_gpu(opt), opt.table, opt.n, max_norm, (out, 2, DT_F32),
+          (ws, ws_bytes, _BYTES), ws_bytes)
 
 
 def trace_enable(on: bool) -> None:

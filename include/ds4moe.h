@@ -466,6 +466,119 @@ int ds4moe_mx_product(const void *a, int64_t n, int32_t cols, const void *w, con
 int ds4moe_mx_product_grad(const void *dy, int dy_dtype, int64_t n, int32_t rows, const void *w, int32_t cols,
                            int32_t n_experts, const int32_t *offsets, void *da, int da_dtype, void *stream);
 
+/* ----------------------------------------------------------------------
+ * A training step's losses and update, next to the gradients above: the
+ * router's balance loss, the cross entropy of the rows that leave the model
+ * against a vocabulary, and AdamW.
+ * ---------------------------------------------------------------------- */
+
+/* Balance loss of the router.  With the tokens of sequence b, [seq_offsets[b],
+ * seq_offsets[b+1]):
+ *   p_te   = softmax of token t's routing logits (a row of -inf: zeros)
+ *   c_be   = slots of b's tokens on expert e
+ *   n_b    = tokens of b with a slot on any expert: one without (padding, all
+ *            slots dropped) takes no part, and neither does one in no sequence
+ *   loss_b = n_experts / (k n_b^2) sum_e c_be sum_t p_te;  0 where n_b = 0
+ * which is 1 where loads and probabilities are even.  A slot whose expert lies
+ * outside [0, n_experts) is not counted; one that names an expert again is.
+ *   logits [T][n_experts]   fp32 or bf16, contiguous, aligned as its type
+ *   topk_idx [T][k]         as ds4moe_group takes it
+ *   seq_offsets [n_seqs+1]  device, ascending, taken as held to [0, T]; NULL with
+ *                           n_seqs = 1: all tokens
+ *   counts [n_seqs][n_experts], tokens [n_seqs] (n_b): int32 out
+ *   loss [n_seqs]           fp32 out
+ * 1 <= T <= 1048576, T n_experts < 2^31, 1 <= k <= 16, 1 <= n_experts <= 1024,
+ * 1 <= n_seqs <= 16384.  Sums have a fixed order.  A non-finite logit makes
+ * its sequence's loss non-finite, and its own row's gradient. */
+size_t ds4moe_balance_workspace_bytes(int64_t T, int32_t n_experts, int32_t n_seqs);
+int ds4moe_balance(const void *logits, int l_dtype, int64_t T, int32_t n_experts, const int32_t *topk_idx, int32_t k,
+                   const int32_t *seq_offsets, int32_t n_seqs, int32_t *counts, int32_t *tokens, float *loss, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* Gradient to the logits, with that of the slots' weights added:
+ *   dlogits_te = dloss_b n_experts / (k n_b^2) p_te (c_be - sum_j p_tj c_bj)
+ *                + sum of dslots_tj over the token's slots on e
+ * counts and tokens as ds4moe_balance wrote them.  dloss fp32 [n_seqs], or NULL
+ * for ones: the loss's weight goes in here.  dslots fp32 [T][k]: dlogits of
+ * ds4moe_combine_grad, or NULL for none.  dlogits [T][n_experts] in the
+ * logits' type, every row written (zeros and its slots' part for a token that
+ * takes no part); it may equal logits. */
+int ds4moe_balance_grad(const void *logits, int l_dtype, int64_t T, int32_t n_experts, const int32_t *topk_idx,
+                        int32_t k, const int32_t *seq_offsets, int32_t n_seqs, const int32_t *counts,
+                        const int32_t *tokens, const float *dloss, const float *dslots, void *dlogits, void *stream);
+
+/* Softmax cross entropy of T rows h [T][d] against a vocabulary w [vocab][d],
+ * both fp32 or both bf16, without keeping the logits:
+ *   z = scale h w^T,  lse_t = log sum_v e^z_tv,  loss_t = lse_t - z_t,target
+ * target int32 [T]; a row whose target lies outside [0, vocab) has the loss 0
+ * (and its lse) and takes no part in the gradients.  loss and lse fp32 [T].
+ * 1 <= T <= 1048576, 1 <= vocab <= 1048576, d a multiple of 256, <= 16384; scale
+ * finite.  Products of bf16 are exact and summed in fp32; fp32 operands are
+ * multiplied as three bf16 parts each, to fp32 rounding (what lies under
+ * 2^-133 is lost).  ws need not be cleared. */
+size_t ds4moe_xent_workspace_bytes(int dtype, int64_t T, int64_t vocab, int32_t d, int with_grad);
+int ds4moe_xent(const void *h, const void *w, int dtype, int64_t T, int64_t vocab, int32_t d, float scale,
+                const int32_t *target, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients, the logits formed again a piece of the vocabulary at a time:
+ *   ds_tv = dloss_t scale (e^(z_tv - lse_t) - [v = target_t])
+ *   dh = ds w,  dw = ds^T h          [T][d], [vocab][d], in dtype
+ * lse as ds4moe_xent wrote it; dloss fp32 [T], or NULL for ones.  dh of a row
+ * without a target is zero.  dh or dw may be NULL, not both.  ds is held in
+ * bf16 for bf16 operands, in three bf16 parts for fp32; sums are fp32.  One
+ * workspace of the size with_grad = 1 gives serves both calls. */
+int ds4moe_xent_grad(const void *h, const void *w, int dtype, int64_t T, int64_t vocab, int32_t d, float scale,
+                     const int32_t *target, const float *lse, const float *dloss, void *dh, void *dw, void *ws,
+                     size_t ws_bytes, void *stream);
+
+/* AdamW over many tensors at once:
+ *   g' = s g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p  = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
+ * in fp32.  States: fp32 m and v; or DS4MOE_STATE_FP8: m and sqrt(v) as OCP
+ * E4M3 codes (torch.float8_e4m3fn) to the nearest of scale times code, with an fp32
+ * scale, largest magnitude / 448, for each 256 consecutive values (the last
+ * block of a tensor may be shorter).  A positive sqrt(v) is held as the lowest
+ * positive code at least; a scale below 2^-126 is 0, and so is its block;
+ * a block with a value that is not finite gets the scale NaN and reads back
+ * as NaN.  The update takes the new m and v as they are before they are
+ * rounded to codes.  States start as zeros. */
+enum { DS4MOE_STATE_F32 = 0, DS4MOE_STATE_FP8 = 1 };
+
+/* One tensor.  Plain data: read during the call, not retained.  Pointers are
+ * aligned as their type; 16 bytes (8 for codes) is faster. */
+typedef struct {
+  void *param;          /* [n] fp32 or bf16, updated */
+  const void *grad;     /* [n] fp32 or bf16 */
+  float *master;        /* [n] fp32: updated in param's place, which gets it rounded; or NULL */
+  void *m, *v;          /* [n] states: fp32, or codes */
+  float *m_scale, *v_scale; /* [(n + 255) / 256] with DS4MOE_STATE_FP8, else not read */
+  int64_t n;            /* 0 <= n <= 2^40 */
+  double weight_decay;  /* finite */
+} ds4moe_param;
+
+typedef struct {
+  int32_t param_dtype, grad_dtype; /* DS4MOE_DT_*, of all tensors of a call */
+  int32_t state;                   /* DS4MOE_STATE_* */
+  double lr, beta1, beta2, eps;    /* finite; 0 <= beta < 1; eps > 0 as an fp32 */
+  const float *lr_dev;             /* device: the learning rate in lr's place, or NULL */
+  const int32_t *step_dev;         /* device: the step in the argument's place, or NULL */
+} ds4moe_adamw;
+
+/* One step over params[0 .. n_params) (host array; 0 <= n_params <= 2^20, no two
+ * overlap).  step counts from 1 (below 1 on the device: 1).  grad_scale: device,
+ * s, or NULL for 1; where it is not finite nothing changes, which is how
+ * a step without finite gradients is left out. */
+int ds4moe_adamw_step(const ds4moe_adamw *A, const ds4moe_param *params, int32_t n_params, int64_t step,
+                      const float *grad_scale, void *stream);
+
+/* out[0] = sqrt(sum of the squares of all gradients), summed in fp64 in a fixed
+ * order; out[1] = min(1, max_norm / out[0]), NaN where out[0] is not finite:
+ * the grad_scale of a clipped step.  fp32 [2], device.  Of params only grad and
+ * n are read.  max_norm > 0.  ws, 256-byte aligned, need not be cleared. */
+size_t ds4moe_adamw_workspace_bytes(const ds4moe_param *params, int32_t n_params);
+int ds4moe_adamw_norm(const ds4moe_adamw *A, const ds4moe_param *params, int32_t n_params, float max_norm, float *out,
+                      void *ws, size_t ws_bytes, void *stream);
+
 /* Opt-in per-kernel timing (profiling aid).  While enabled, every kernel
  * the library launches is bracketed by two HIP events on its stream, which
  * adds a little launch overhead.  Thread-safe. */

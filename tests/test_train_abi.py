@@ -1,0 +1,202 @@
+"""Host-side checks of a training step's operators (no device work): sizes of
+workspaces, and calls that are refused before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+from bit_quantized_routed_router_amd import ds4moe as D
+
+A = 0x10000  # stand-in device address: aligned, never dereferenced
+BIG = 1 << 60
+NAN, INF = float("nan"), float("inf")
+
+
+def status(name, *args):
+    return getattr(D.lib(), "ds4moe_" + name)(*args)
+
+
+# ---------------------------------------------------------------- balance
+def balance(z=A, dt=0, T=8, E=16, idx=A, k=2, off=None, B=1, counts=A, tokens=A, loss=A, ws=A, nb=BIG):
+    return status("balance", z, dt, T, E, idx, k, off, B, counts, tokens, loss, ws, nb, None)
+
+
+def balance_grad(z=A, dt=0, T=8, E=16, idx=A, k=2, off=None, B=1, counts=A, tokens=A, dloss=None, ds=None, dz=A):
+    return status("balance_grad", z, dt, T, E, idx, k, off, B, counts, tokens, dloss, ds, dz, None)
+
+
+def test_balance_errors():
+    for call in (balance, balance_grad):
+        for kw in (dict(T=0), dict(T=-1), dict(T=(1 << 20) + 1), dict(E=0), dict(E=1025), dict(k=0), dict(k=17), dict(B=0),
+                   dict(B=16385), dict(T=1 << 20, E=1024, B=1 << 15)):
+            assert call(**kw) == D.ESHAPE, kw
+        for kw in (dict(z=None), dict(idx=None), dict(counts=None), dict(tokens=None), dict(dt=2), dict(dt=-1), dict(B=2)):
+            assert call(**kw) == D.EINVAL, kw
+        for kw in (dict(z=A + 2), dict(z=A + 1, dt=1), dict(idx=A + 2), dict(off=A + 1), dict(counts=A + 2),
+                   dict(tokens=A + 2)):
+            assert call(**kw) == D.EALIGN, kw
+    assert balance(loss=None) == D.EINVAL and balance(ws=None) == D.EINVAL and balance_grad(dz=None) == D.EINVAL
+    for kw in (dict(loss=A + 2), dict(ws=A + 128)):
+        assert balance(**kw) == D.EALIGN
+    for kw in (dict(dz=A + 2), dict(dloss=A + 2), dict(ds=A + 2)):
+        assert balance_grad(**kw) == D.EALIGN
+    need = D.balance_workspace_bytes(1000, 16, 3)
+    assert need > 0 and balance(T=1000, off=A, B=3, nb=need - 1) == D.EWORKSPACE
+    for bad in ((0, 16, 1), (8, 0, 1), (8, 16, 0), (8, 2000, 1), (1 << 21, 4, 1), (8, 16, 1 << 15)):
+        assert D.balance_workspace_bytes(*bad) == 0
+
+
+# ---------------------------------------------------------------- cross entropy
+def xent(h=A, w=A, dt=1, T=8, V=100, d=256, scale=1.0, y=A, loss=A, lse=A, ws=A, nb=BIG):
+    return status("xent", h, w, dt, T, V, d, scale, y, loss, lse, ws, nb, None)
+
+
+def xent_grad(h=A, w=A, dt=1, T=8, V=100, d=256, scale=1.0, y=A, lse=A, dloss=None, dh=A, dw=A, ws=A, nb=BIG):
+    return status("xent_grad", h, w, dt, T, V, d, scale, y, lse, dloss, dh, dw, ws, nb, None)
+
+
+def test_xent_errors():
+    for call in (xent, xent_grad):
+        for kw in (dict(T=0), dict(T=(1 << 20) + 1), dict(V=0), dict(V=(1 << 20) + 1), dict(d=0), dict(d=300),
+                   dict(d=16640)):
+            assert call(**kw) == D.ESHAPE, kw
+        for kw in (dict(h=None), dict(w=None), dict(y=None), dict(lse=None), dict(ws=None), dict(dt=2), dict(scale=NAN),
+                   dict(scale=INF)):
+            assert call(**kw) == D.EINVAL, kw
+        for kw in (dict(h=A + 8), dict(w=A + 8), dict(y=A + 2), dict(lse=A + 2), dict(ws=A + 128)):
+            assert call(**kw) == D.EALIGN, kw
+    assert xent(loss=None) == D.EINVAL and xent(loss=A + 2) == D.EALIGN
+    assert xent_grad(dh=None, dw=None) == D.EINVAL
+    for kw in (dict(dh=A + 8), dict(dw=A + 4), dict(dloss=A + 1)):
+        assert xent_grad(**kw) == D.EALIGN
+    for dt in (0, 1):
+        need, more = D.xent_workspace_bytes(dt, 100, 5000, 512, False), D.xent_workspace_bytes(dt, 100, 5000, 512, True)
+        assert 0 < need <= more
+        assert xent(dt=dt, T=100, V=5000, d=512, nb=need - 1) == D.EWORKSPACE
+    assert xent_grad(T=100, V=5000, d=512, nb=1024) == D.EWORKSPACE
+    for bad in ((2, 8, 100, 256), (1, 0, 100, 256), (1, 8, 0, 256), (1, 8, 100, 100), (1, 1 << 21, 100, 256)):
+        assert D.xent_workspace_bytes(*bad, True) == 0
+
+
+def test_xent_workspace_does_not_hold_the_logits():
+    """Past a piece's size it does not grow with the vocabulary."""
+    for dt in (0, 1):
+        small, large = (D.xent_workspace_bytes(dt, 8192, V, 1024, True) for V in (1 << 17, 1 << 20))
+        assert large < 1.2 * small and large < 8192 * (1 << 20)
+
+
+# ---------------------------------------------------------------- AdamW
+def param(**kw):
+    v = dict(param=A, grad=A, master=None, m=A, v=A, m_scale=A, v_scale=A, n=100, weight_decay=0.1)
+    v.update(kw)
+    return D.ParamDesc(*(v[f[0]] for f in D.ParamDesc._fields_))
+
+
+def opts(**kw):
+    v = dict(param_dtype=0, grad_dtype=0, state=0, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, lr_dev=None, step_dev=None)
+    v.update(kw)
+    return D.AdamWDesc(*(v[f[0]] for f in D.AdamWDesc._fields_))
+
+
+def step(o=None, p=None, n=1, at=1, scale=None):
+    o = opts() if o is None else o
+    table = (D.ParamDesc * 2)(param() if p is None else p, param(n=0, param=None, grad=None, m=None, v=None))
+    return status("adamw_step", ctypes.byref(o) if o else None, table, n, at, scale, None)
+
+
+def norm(o=None, p=None, n=1, most=1.0, out=A, ws=A, nb=BIG):
+    table = (D.ParamDesc * 2)(param() if p is None else p, param(n=0))
+    return status("adamw_norm", ctypes.byref(opts() if o is None else o), table, n, most, out, ws, nb, None)
+
+
+def test_adamw_errors():
+    for kw in (dict(param_dtype=2), dict(grad_dtype=-1), dict(state=2), dict(lr=NAN), dict(lr=INF), dict(beta1=1.0),
+               dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=NAN), dict(eps=0.0), dict(eps=NAN), dict(eps=INF),
+               dict(eps=1e-60)):
+        assert step(o=opts(**kw)) == D.EINVAL, kw
+    assert step(o=opts(lr_dev=A + 2)) == D.EALIGN and step(o=opts(step_dev=A + 2)) == D.EALIGN
+    assert step(at=0) == D.EINVAL and step(at=-3) == D.EINVAL and step(scale=A + 2) == D.EALIGN
+    assert step(n=-1) == D.ESHAPE
+    for kw in (dict(param=None), dict(grad=None), dict(m=None), dict(v=None), dict(weight_decay=NAN)):
+        assert step(p=param(**kw)) == D.EINVAL, kw
+    for kw in (dict(n=-1), dict(n=(1 << 40) + 1)):
+        assert step(p=param(**kw)) == D.ESHAPE and norm(p=param(**kw)) == D.ESHAPE
+    for kw in (dict(param=A + 2), dict(grad=A + 2), dict(m=A + 2), dict(v=A + 1), dict(master=A + 2)):
+        assert step(p=param(**kw)) == D.EALIGN, kw
+    assert step(o=opts(param_dtype=1), p=param(param=A + 1)) == D.EALIGN
+    fp8 = opts(state=D.STATE_FP8)
+    for kw in (dict(m_scale=None), dict(v_scale=None)):
+        assert step(o=fp8, p=param(**kw)) == D.EINVAL
+    assert step(o=fp8, p=param(m_scale=A + 2, m=A + 1)) == D.EALIGN
+    assert status("adamw_step", None, None, 0, 1, None, None) == D.EINVAL
+    assert status("adamw_step", ctypes.byref(opts()), None, 1, 1, None, None) == D.EINVAL
+    # nothing to do launches nothing
+    assert status("adamw_step", ctypes.byref(opts()), None, 0, 1, None, None) == D.OK
+
+
+def test_norm_errors():
+    for kw in (dict(most=0.0), dict(most=-1.0), dict(most=NAN), dict(out=None), dict(ws=None), dict(p=param(grad=None)),
+               dict(o=opts(grad_dtype=3))):
+        assert norm(**kw) == D.EINVAL, kw
+    for kw in (dict(out=A + 2), dict(ws=A + 64), dict(p=param(grad=A + 2))):
+        assert norm(**kw) == D.EALIGN, kw
+    need = D.lib().ds4moe_adamw_workspace_bytes((D.ParamDesc * 1)(param(n=1 << 30)), 1)
+    assert need > 0 and norm(p=param(n=1 << 30), nb=need - 1) == D.EWORKSPACE
+    assert D.lib().ds4moe_adamw_workspace_bytes(None, 1) == 0
+    assert D.lib().ds4moe_adamw_workspace_bytes((D.ParamDesc * 1)(param(n=-1)), 1) == 0
+
+
+def test_struct_sizes():
+    """The structures as the header lays them out on a 64-bit host."""
+    assert ctypes.sizeof(D.ParamDesc) == 72 and ctypes.sizeof(D.AdamWDesc) == 64
+
+
+# ---------------------------------------------------------------- binding
+F32, BF16, I32, U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+
+
+def calls(dt, code):
+    T, E, K, B, V, d = 4, 8, 2, 3, 10, 256
+    return {
+        "balance": (D.balance, [(T * E, dt), code, T, E, (T * K, I32), K, (B + 1, I32), B, (B * E, I32), (B, I32), (B, F32),
+                                (512, U8), 512]),
+        "balance_grad": (D.balance_grad, [(T * E, dt), code, T, E, (T * K, I32), K, (B + 1, I32), B, (B * E, I32), (B, I32),
+                                          (B, F32), (T * K, F32), (T * E, dt)]),
+        "xent": (D.xent, [(T * d, dt), (V * d, dt), code, T, V, d, 1.0, (T, I32), (T, F32), (T, F32), (512, U8), 512]),
+        "xent_grad": (D.xent_grad, [(T * d, dt), (V * d, dt), code, T, V, d, 1.0, (T, I32), (T, F32), (T, F32), (T * d, dt),
+                                    (V * d, dt), (512, U8), 512]),
+    }
+
+
+@pytest.mark.parametrize("dt,code", [(F32, 0), (BF16, 1)])
+@pytest.mark.parametrize("name", ["balance", "balance_grad", "xent", "xent_grad"])
+def test_refused_tensors(name, dt, code):
+    f, args = calls(dt, code)[name]
+    for i, a in enumerate(args):
+        if not isinstance(a, tuple):
+            continue
+        for n, t, match in ((a[0], a[1], "current GPU"), (a[0] - 1, a[1], "bytes where" if a[1] == U8 else "values where"),
+                            (2 * a[0], torch.float64, "bytes|dtype|current GPU" if a[1] == U8 else "dtype")):
+            given = [torch.zeros(n, dtype=t) if j == i else A if isinstance(b, tuple) else b for j, b in enumerate(args)]
+            with pytest.raises(ValueError, match=match):
+                f(*given)
+
+
+def test_optimizer_refuses_host_tensors_and_lists_that_do_not_match():
+    t = [torch.zeros(4)]
+    with pytest.raises(ValueError, match="one GPU"):
+        D.AdamW(t, t, t, t)
+    with pytest.raises(ValueError, match="expected 0 tensors"):
+        D.AdamW([], t, [], [])
+    with pytest.raises(ValueError, match="dtype"):
+        D.AdamW([torch.zeros(4, dtype=torch.float16)], t, t, t)
+    with pytest.raises(ValueError, match="contiguous"):
+        D.AdamW([torch.zeros(8)[::2]], t, t, t)
+    assert D.AdamW([], [], [], []).n == 0
+
+
+def test_optimizer_of_another_device_is_refused():
+    opt = D.AdamW([], [], [], [])
+    opt.gpu = 63
+    with pytest.raises(ValueError, match="optimizer's tensors are not"):
+        D.adamw_step(opt, 1)
