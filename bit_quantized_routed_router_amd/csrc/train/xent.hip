@@ -38,6 +38,7 @@ struct XentPlan {
   int64_t piece;      // words of a piece, a multiple of 256
   int pieces;
   int64_t rows;       // rows of a forward pass over the vocabulary
+  int64_t hp, dsp;    // bytes from row to row of h's copy and of ds
   int slabs;
   // offsets into the workspace
   size_t hc, wp, n, live, y, lse, g, ds, slab, zt, part, bytes;
@@ -66,7 +67,10 @@ static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
     at += round_up<size_t>(bytes, 256);
     return here;
   };
-  if (p.parts == 3 || grad) p.hc = take((size_t)2 * p.parts * T * d);
+  // rows at a large power of two from each other meet in few of the L2's channels
+  p.hp = 2 * (int64_t)d + 256;
+  p.dsp = 2 * p.piece + 256;
+  if (p.parts == 3 || grad) p.hc = take((size_t)p.parts * T * p.hp);
   if (p.parts == 3) p.wp = take((size_t)6 * p.piece * d);
   if (grad) {
     p.n = take(8);
@@ -74,7 +78,7 @@ static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
     p.y = take(4 * T);
     p.lse = take(4 * T);
     p.g = take(4 * T);
-    p.ds = take((size_t)2 * p.parts * T * p.piece);
+    p.ds = take((size_t)p.parts * T * p.dsp);
     p.slab = take((size_t)4 * p.slabs * T * d);
   } else {
     const int64_t parts = all / (xent_small(T) ? 32 : 64);
@@ -164,7 +168,8 @@ __device__ inline void xsplit8(const float (&x)[8], u32x4_t (&o)[3]) {
 template <bool BF>
 __global__ __launch_bounds__(256) void k_xent_rows(const void* __restrict__ src, const int32_t* __restrict__ n,
                                                    const int32_t* __restrict__ live, int64_t rows, int d,
-                                                   uint8_t* __restrict__ dst, int64_t plane, void* __restrict__ dh) {
+                                                   uint8_t* __restrict__ dst, int64_t pitch, int64_t plane,
+                                                   void* __restrict__ dh) {
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const int64_t from = live ? live[r] : r;
     const bool on = !n || r < *n;
@@ -172,14 +177,14 @@ __global__ __launch_bounds__(256) void k_xent_rows(const void* __restrict__ src,
       if (on) {
         const Raw8<BF> v = ld8<BF>(src, from * d + i);
         if constexpr (BF) {
-          *(u32x4_t*)(dst + (r * d + i) * 2) = v.a;
+          *(u32x4_t*)(dst + r * pitch + i * 2) = v.a;
         } else {
           float x[8];
           u32x4_t o[3];
           unpack8<BF>(v, x);
           xsplit8(x, o);
 #pragma unroll
-          for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + (r * d + i) * 2) = o[s];
+          for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + r * pitch + i * 2) = o[s];
         }
       } else if (dh) {
         const float zero[8] = {};
@@ -249,10 +254,26 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
   B.init(x.b, b0, b_rows, tid);
   const int nk = (int)((K + 63) / 64);
   const int kc0 = (int)((int64_t)nk * s / x.splits), kc1 = (int)((int64_t)nk * (s + 1) / x.splits);
+  const int am = (wave % S::WM) * 32 * S::FM, bn = (wave / S::WM) * 32 * S::FN;
   float16_t acc[S::FM][S::FN] = {};
+  if (EPI == XE_SLAB && x.add) {  // on top of the pieces before
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i) {
+      const int64_t r = b0 + bn + 32 * i + c;
+      if (r >= b_rows) continue;
+      const float* at = (const float*)(x.out + s * x.out_plane + r * x.out_pitch) + a0 + am + 4 * h;
+#pragma unroll
+      for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4_t u = *(const float4_t*)(at + 32 * f + 8 * g);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[f][i][4 * g + v] = u[v];
+        }
+    }
+  }
   xgemm<S, ACOL, BCOL, PARTS>(A, B, K, kc0, kc1, smem, acc, wave, lane);
 
-  const int am = (wave % S::WM) * 32 * S::FM, bn = (wave / S::WM) * 32 * S::FN;
   if constexpr (EPI == XE_SUM) {
     const int a1 = (int)a0 + am;  // the wave's first word of the piece
     const int left = x.V - a1;    // and how many there are from it on
@@ -343,11 +364,7 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
           [&](int row, int ch, u32x4_t v) {
             const int64_t r = b0 + bn + 32 * i + row;
             if (r >= b_rows) return;
-            u32x4_t* at = (u32x4_t*)(out + r * x.out_pitch + (a0 + am) * ES + ch * 16);
-            if (EPI == XE_SLAB && x.add)
-              *(float4_t*)at = *(const float4_t*)at + __builtin_bit_cast(float4_t, v);
-            else
-              *at = v;
+            *(u32x4_t*)(out + r * x.out_pitch + (a0 + am) * ES + ch * 16) = v;
           });
   }
 }
@@ -430,9 +447,9 @@ static hipError_t xent_gemm(const XArgs& x, hipStream_t st) {
 static unsigned xent_row_blocks(int64_t rows) { return (unsigned)std::min<int64_t>(rows, 8192); }
 
 // all rows of an fp32 matrix as planes
-static void xent_copy(const void* src, int64_t rows, int d, uint8_t* dst, int64_t plane, hipStream_t st) {
+static void xent_copy(const void* src, int64_t rows, int d, uint8_t* dst, int64_t pitch, int64_t plane, hipStream_t st) {
   DS4_LAUNCH(k_xent_rows<false>, dim3(xent_row_blocks(rows)), dim3(256), 0, st, src, (const int32_t*)nullptr,
-             (const int32_t*)nullptr, rows, d, dst, plane, (void*)nullptr);
+             (const int32_t*)nullptr, rows, d, dst, pitch, plane, (void*)nullptr);
 }
 
 template <int PARTS>
@@ -440,12 +457,12 @@ static hipError_t xent_forward(const XentCall& c) {
   const XentPlan p = xent_plan(c.dt, c.T, c.V, c.d, false);
   uint8_t* w = c.ws;
   const bool few = xent_small(c.T);
-  const int per = few ? 32 : 64;  // words of a partial sum
+  const int per = few ? 32 : 128;  // words of a partial sum
   const int64_t pitch = 2 * (int64_t)c.d;
-  const uint8_t* h = (const uint8_t*)c.h;
+  XOperand h = {(const uint8_t*)c.h, 0, pitch};
   if (PARTS == 3) {
-    xent_copy(c.h, c.T, c.d, w + p.hc, c.T * pitch, c.st);
-    h = w + p.hc;
+    h = {w + p.hc, c.T * p.hp, p.hp};
+    xent_copy(c.h, c.T, c.d, w + p.hc, h.pitch, h.plane, c.st);
   }
   for (int64_t r0 = 0; r0 < c.T; r0 += p.rows) {
     const int64_t rows = std::min(c.T - r0, p.rows);
@@ -455,10 +472,10 @@ static hipError_t xent_forward(const XentCall& c) {
       XArgs x{};
       x.a = {src, 0, pitch};
       if (PARTS == 3) {
-        xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
+        xent_copy(src, words, c.d, w + p.wp, pitch, p.piece * pitch, c.st);
         x.a = {w + p.wp, p.piece * pitch, pitch};
       }
-      x.b = {h + r0 * pitch, c.T * pitch, pitch};
+      x.b = {h.p + r0 * h.pitch, h.plane, h.pitch};
       x.a_rows = words;
       x.b_rows = rows;
       x.K = c.d;
@@ -470,7 +487,7 @@ static hipError_t xent_forward(const XentCall& c) {
       x.rows = (int)rows;
       x.part = (float2*)(w + p.part);
       x.zt = (float*)(w + p.zt);
-      const hipError_t e = few ? xent_launch<XFew, XE_SUM, PARTS, false>(x, c.st) : xent_launch<XMid, XE_SUM, PARTS, false>(x, c.st);
+      const hipError_t e = few ? xent_launch<XFew, XE_SUM, PARTS, false>(x, c.st) : xent_launch<XBig, XE_SUM, PARTS, false>(x, c.st);
       if (e) return e;
     }
     DS4_LAUNCH(k_xent_join, dim3((unsigned)((rows + 31) / 32)), dim3(1024), 0, c.st, (const float2*)(w + p.part),
@@ -492,16 +509,16 @@ static hipError_t xent_backward(const XentCall& c) {
   DS4_LAUNCH(k_xent_live, dim3(1), dim3(1024), 0, c.st, c.target, (int)c.T, (int)c.V, c.scale, c.lse_in, c.dloss, n, live,
              (int32_t*)(w + p.y), (float*)(w + p.lse), (float*)(w + p.g));
   DS4_LAUNCH((k_xent_rows<PARTS == 1>), dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, c.h, (const int32_t*)n,
-             (const int32_t*)live, c.T, c.d, w + p.hc, c.T * pitch, c.dh);
+             (const int32_t*)live, c.T, c.d, w + p.hc, p.hp, c.T * p.hp, c.dh);
   for (int i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
     const uint8_t* src = (const uint8_t*)c.w + v0 * pitch * (PARTS == 3 ? 2 : 1);
     XOperand wop = {src, 0, pitch};
     if (PARTS == 3) {
-      xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
+      xent_copy(src, words, c.d, w + p.wp, pitch, p.piece * pitch, c.st);
       wop = {w + p.wp, p.piece * pitch, pitch};
     }
-    const XOperand hop = {w + p.hc, c.T * pitch, pitch}, dsop = {w + p.ds, 2 * c.T * p.piece, 2 * p.piece};
+    const XOperand hop = {w + p.hc, c.T * p.hp, p.hp}, dsop = {w + p.ds, c.T * p.dsp, p.dsp};
     XArgs x{};
     x.a = wop;
     x.b = hop;
@@ -518,8 +535,8 @@ static hipError_t xent_backward(const XentCall& c) {
     x.g = (const float*)(w + p.g);
     x.top = (const float*)n + 1;
     x.out = w + p.ds;
-    x.out_pitch = 2 * p.piece;
-    x.out_plane = 2 * c.T * p.piece;
+    x.out_pitch = dsop.pitch;
+    x.out_plane = dsop.plane;
     // the last tile's words past the end are written too: as zeros
     if ((e = xent_gemm<XE_DS, PARTS, false>(x, c.st))) return e;
     if (c.dh) {

@@ -14,7 +14,7 @@
 // LDS: 16-byte pieces, swizzled on their way in by choosing which piece a
 // lane copies.  By rows piece p of row r lies at p ^ (r / 2 & 7), so that the
 // 16 rows that a quarter of a wave reads lie in different banks; by columns
-// piece p of row k lies at p ^ 2 (k & 7), since a quarter reads two
+// piece p of row k lies at p ^ 4 (k & 3), since half a wave reads four
 // neighbouring pieces of four rows.
 #pragma once
 
@@ -30,6 +30,13 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 __device__ inline float16_t mfma32(u32x4_t a, u32x4_t b, float16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);
+}
+
+// The transposing read.  The argument's __restrict__ is what the compiler knows
+// about the read: without it, it would wait for every copy under way before.
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+__device__ __attribute__((always_inline)) inline u32x2_t read_turned(lds_s16x4_t* __restrict__ p) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
 }
 
 // waves along a and b, 32x32 fragments of a wave along both, chunks in the ring
@@ -51,7 +58,7 @@ struct XOperand {
 // One operand's side of a tile of B indices, from index i0 on.
 template <int B, bool COL>
 struct XSide {
-  static constexpr int NF = B / 32;
+  static_assert(!COL || B >= 128, "sixteen pieces of a row, at least");
   const uint8_t* base;
   int64_t plane, pitch;
   uint32_t records;  // by rows: bytes that the tile has; by columns: what a row's end leaves out
@@ -69,26 +76,25 @@ struct XSide {
       base = o.p + i0 * 2;
       records = (uint32_t)i0 * 2;
       const int k = tid / P, p = tid % P;
-      vo = (uint32_t)(k * pitch) + ((p ^ (2 * (k & 7))) & (P - 1)) * 16;
+      vo = (uint32_t)(k * pitch) + (p ^ (4 * (k & 3))) * 16;
     }
   }
-  // chunk kc of plane q into LDS at dst; K: how many k there are
-  __device__ __attribute__((always_inline)) inline void issue(int kc, int q, int64_t K, bool on, uint8_t* dst,
-                                                              int wave) const {
+  static constexpr int kStep = COL ? 2048 / B : 32;  // rows from one copy to the next
+  // chunk kc of plane q; K: how many k there are
+  __device__ __attribute__((always_inline)) inline __amdgpu_buffer_rsrc_t chunk(int kc, int q, int64_t K) const {
     const uint8_t* src = base + q * plane;
-    uint32_t n = records;
-    if constexpr (COL) {
-      src += (int64_t)kc * 64 * pitch;
+    if constexpr (!COL) {
+      return buf_rsrc(src + (int64_t)kc * 128, kc * 128 < (int)records ? records - kc * 128 : 0);
+    } else {
       const int64_t left = K - (int64_t)kc * 64;
-      n = left > 0 ? (uint32_t)((left < 64 ? left : 64) * pitch) - records : 0;
+      return buf_rsrc(src + (int64_t)kc * 64 * pitch, left > 0 ? (uint32_t)((left < 64 ? left : 64) * pitch) - records : 0);
     }
-    const __amdgpu_buffer_rsrc_t r = buf_rsrc(src, n);
-    constexpr int step = COL ? 2048 / B : 32;  // rows from one copy to the next
-#pragma unroll
-    for (int i = 0; i < NF; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (__attribute__((address_space(3))) void*)(dst + i * 4096 + wave * 1024), 16, on ? (int)vo : (int)kOob,
-          (int)(i * step * pitch) + (COL ? 0 : kc * 128), 0, 0);
+  }
+  // copy i of the thread (B / 32 in all), of a chunk that lies at dst
+  __device__ __attribute__((always_inline)) inline void copy(__amdgpu_buffer_rsrc_t r, bool on, int i, uint8_t* dst,
+                                                             int wave) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(dst + i * 4096 + wave * 1024),
+                                             16, on ? (int)vo : (int)kOob, (int)(i * kStep * pitch), 0, 0);
   }
   // Fragment f (32 indices from first on) of step j (16 k): lane l gets index
   // l & 31 and k 8 (l >> 5) .. + 7.
@@ -100,16 +106,14 @@ struct XSide {
     } else {
       // Of a quarter's 16 lanes, four hold 16 neighbouring indices of one k,
       // four k in all; the read hands lane i index i of the four.
-      constexpr int RB = B * 2, P = B / 8;
+      constexpr int RB = B * 2;
       const int i = lane & 15, s = (lane >> 4) & 1, h = lane >> 5;
       u32x4_t v;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int k = 4 * r + (i >> 2);  // its last three bits
-        const int piece = (first / 8 + 4 * f + 2 * s + ((i & 3) >> 1)) ^ ((2 * k) & (P - 1));
-        const u32x2_t x = __builtin_bit_cast(
-            u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(
-                         at + (16 * j + 8 * h + k) * RB + piece * 16 + 8 * (i & 1))));
+        const int piece = (first / 8 + 4 * f + 2 * s + ((i & 3) >> 1)) ^ (4 * (k & 3));
+        const u32x2_t x = read_turned((lds_s16x4_t*)(at + (16 * j + 8 * h + k) * RB + piece * 16 + 8 * (i & 1)));
         v[2 * r] = x.x;
         v[2 * r + 1] = x.y;
       }
@@ -123,6 +127,12 @@ __device__ inline int plane_a(int q) { return (0x200110 >> (4 * (5 - q))) & 3; }
 __device__ inline int plane_b(int q) { return (0x021010 >> (4 * (5 - q))) & 3; }
 
 // Chunks kc0 .. kc1 - 1 of the tile into acc[FM][FN] of this wave.
+//
+// One chunk after another, with R - 1 of them under way.  256 x 256 tiles are
+// written out further: with one wave to a SIMD nothing else hides a wait, so a
+// step's fragments are read while the products of the step before run, across
+// the chunk's border too, and the copies are dealt out between products, which
+// would otherwise wait behind a run of them.
 template <class S, bool ACOL, bool BCOL, int PARTS>
 __device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, ACOL>& A, const XSide<S::BN, BCOL>& B,
                                                             int64_t K, int kc0, int kc1, uint8_t* smem,
@@ -130,38 +140,98 @@ __device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, A
   constexpr int Q = PARTS == 3 ? 6 : 1;
   const int n = (kc1 - kc0) * Q;
   const int am = (wave % S::WM) * 32 * S::FM, bn = (wave / S::WM) * 32 * S::FN;
-  auto issue = [&](int ch, int u) __attribute__((always_inline)) {
-    const int kc = kc0 + ch / Q, q = ch % Q;
-    const int qa = PARTS == 3 ? plane_a(q) : 0, qb = PARTS == 3 ? plane_b(q) : 0;
-    uint8_t* dst = smem + u * S::slot;
-    A.issue(kc, qa, K, ch < n, dst, wave);
-    B.issue(kc, qb, K, ch < n, dst + S::BM * 128, wave);
+  struct Chunk {
+    __amdgpu_buffer_rsrc_t a, b;
+    bool on;  // a chunk past the last copies nothing
   };
+  auto chunk = [&](int ch) __attribute__((always_inline)) {
+    const int kc = kc0 + ch / Q, q = ch % Q;
+    return Chunk{A.chunk(kc, PARTS == 3 ? plane_a(q) : 0, K), B.chunk(kc, PARTS == 3 ? plane_b(q) : 0, K), ch < n};
+  };
+  auto copy = [&](const Chunk& x, int i, uint8_t* dst) __attribute__((always_inline)) {
+    if (i < S::BM / 32) A.copy(x.a, x.on, i, dst, wave);
+    else B.copy(x.b, x.on, i - S::BM / 32, dst + S::BM * 128, wave);
+  };
+  struct Frags {
+    u32x4_t a[S::FM], b[S::FN];
+  };
+  auto read = [&](Frags& F, const uint8_t* slot, int j) __attribute__((always_inline)) {
 #pragma unroll
-  for (int u = 0; u < S::R - 1; ++u) issue(u, u);
-  int u = 0;
+    for (int f = 0; f < S::FM; ++f) F.a[f] = XSide<S::BM, ACOL>::read(slot, am, f, j, lane);
+#pragma unroll
+    for (int f = 0; f < S::FN; ++f) F.b[f] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, f, j, lane);
+  };
+  if constexpr (S::FM * S::FN == 16) {
+    static_assert(S::R == 2 && S::copies == 16, "two chunks in turn");
+    // A step's 16 products; between them the reads of the next step's
+    // fragments (step j of the chunk at slot) and eight copies of chunk x.
+    auto step = [&](const Frags& F, Frags& N, const uint8_t* slot, int j, const Chunk& x, int first, uint8_t* dst)
+                    __attribute__((always_inline)) {
+#pragma unroll
+      for (int p = 0; p < 16; ++p) {
+        acc[p % 4][p / 4] = mfma32(F.a[p % 4], F.b[p / 4], acc[p % 4][p / 4]);
+        pin();
+        if (p < 4) N.a[p] = XSide<S::BM, ACOL>::read(slot, am, p, j, lane);
+        else if (p < 8) N.b[p - 4] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, p - 4, j, lane);
+        if (first >= 0 && p >= 8) copy(x, first + p - 8, dst);
+        pin();
+      }
+    };
+    Frags F0, F1;
+    Chunk x = chunk(0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) copy(x, i, smem);
+    vm_wait<0>();
+    ring_barrier();
+    read(F0, smem, 0);
+    x = chunk(1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy(x, i, smem + S::slot);
 #pragma unroll 1
-  for (int ch = 0; ch < n; ++ch) {
-    pin();
-    vm_wait<(S::R - 2) * S::copies>();  // this wave's copies of the chunk
-    ring_barrier();                      // everyone's, and everyone is done with the chunk before
-    pin();
-    issue(ch + S::R - 1, u == 0 ? S::R - 1 : u - 1);
-    pin();
-    const uint8_t* slot = smem + u * S::slot;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4_t fa[S::FM], fb[S::FN];
-#pragma unroll
-      for (int f = 0; f < S::FM; ++f) fa[f] = XSide<S::BM, ACOL>::read(slot, am, f, j, lane);
-#pragma unroll
-      for (int f = 0; f < S::FN; ++f) fb[f] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, f, j, lane);
-#pragma unroll
-      for (int i = 0; i < S::FN; ++i)
-#pragma unroll
-        for (int f = 0; f < S::FM; ++f) acc[f][i] = mfma32(fa[f], fb[i], acc[f][i]);
+    for (int ch = 0; ch < n; ++ch) {
+      uint8_t* const slot = smem + (ch & 1) * S::slot;
+      uint8_t* const next = smem + (~ch & 1) * S::slot;
+      pin();
+      step(F0, F1, slot, 1, x, 8, next);
+      step(F1, F0, slot, 2, x, -1, next);
+      step(F0, F1, slot, 3, x, -1, next);
+      vm_wait<0>();    // this wave's copies of the next chunk
+      ring_barrier();  // everyone's, and everyone has read this one
+      x = chunk(ch + 2);
+      pin();
+      step(F1, F0, next, 0, x, 0, slot);  // (what it reads is not used after the last)
     }
-    u = u + 1 == S::R ? 0 : u + 1;
+  } else {
+#pragma unroll
+    for (int u = 0; u < S::R - 1; ++u) {
+      const Chunk x = chunk(u);
+#pragma unroll
+      for (int i = 0; i < S::copies; ++i) copy(x, i, smem + u * S::slot);
+    }
+    int u = 0;
+#pragma unroll 1
+    for (int ch = 0; ch < n; ++ch) {
+      pin();
+      vm_wait<(S::R - 2) * S::copies>();  // this wave's copies of the chunk
+      ring_barrier();                      // everyone's, and everyone is done with the chunk before
+      pin();
+      const Chunk x = chunk(ch + S::R - 1);
+      uint8_t* const dst = smem + (u == 0 ? S::R - 1 : u - 1) * S::slot;
+#pragma unroll
+      for (int i = 0; i < S::copies; ++i) copy(x, i, dst);
+      pin();
+      const uint8_t* slot = smem + u * S::slot;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Frags F;
+        read(F, slot, j);
+#pragma unroll
+        for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+          for (int f = 0; f < S::FM; ++f) acc[f][i] = mfma32(F.a[f], F.b[i], acc[f][i]);
+      }
+      u = u + 1 == S::R ? 0 : u + 1;
+    }
   }
   vm_wait<0>();
   ring_barrier();
