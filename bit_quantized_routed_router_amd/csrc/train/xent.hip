@@ -14,6 +14,7 @@
 // fp32: 1 / rows, which most losses have there, would otherwise be rounded the
 // same way in every value (dh 0.0034 off, against 0.002).
 #include <algorithm>
+#include <type_traits>
 
 #include "../trace.h"
 #include "../ops/rowtile.h"
@@ -67,9 +68,8 @@ static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
     at += round_up<size_t>(bytes, 256);
     return here;
   };
-  // rows at a large power of two from each other meet in few of the L2's channels
-  p.hp = 2 * (int64_t)d + 256;
-  p.dsp = 2 * p.piece + 256;
+  p.hp = 2 * (int64_t)d;
+  p.dsp = 2 * p.piece;
   if (p.parts == 3 || grad) p.hc = take((size_t)p.parts * T * p.hp);
   if (p.parts == 3) p.wp = take((size_t)6 * p.piece * d);
   if (grad) {
@@ -256,51 +256,67 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
   const int kc0 = (int)((int64_t)nk * s / x.splits), kc1 = (int)((int64_t)nk * (s + 1) / x.splits);
   const int am = (wave % S::WM) * 32 * S::FM, bn = (wave / S::WM) * 32 * S::FN;
   float16_t acc[S::FM][S::FN] = {};
-  if (EPI == XE_SLAB && x.add) {  // on top of the pieces before
+  if constexpr (EPI == XE_SLAB) {  // on top of the pieces before; zeros without any
+    const int64_t rows = min((int64_t)S::BN, b_rows - b0);
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(x.out + s * x.out_plane + b0 * x.out_pitch, (uint32_t)(rows * x.out_pitch));
 #pragma unroll
     for (int i = 0; i < S::FN; ++i) {
-      const int64_t r = b0 + bn + 32 * i + c;
-      if (r >= b_rows) continue;
-      const float* at = (const float*)(x.out + s * x.out_plane + r * x.out_pitch) + a0 + am + 4 * h;
+      const uint32_t at = x.add ? (uint32_t)((bn + 32 * i + c) * x.out_pitch + (a0 + am + 4 * h) * 4) : kOob;
 #pragma unroll
       for (int f = 0; f < S::FM; ++f)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float4_t u = *(const float4_t*)(at + 32 * f + 8 * g);
+          const float4_t u = __builtin_bit_cast(float4_t, buf_ld128(r, at, 128 * f + 32 * g));
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[f][i][4 * g + v] = u[v];
         }
+      pin();
     }
   }
   xgemm<S, ACOL, BCOL, PARTS>(A, B, K, kc0, kc1, smem, acc, wave, lane);
 
+  // Exponentials to base 2, the scale in the same multiply-add.  Words past the
+  // vocabulary's end are only in its last tile, a row's target in few.
+  const float k2 = x.scale * 1.44269504f;
+  const int left = x.V - (int)a0 - am;  // words from the wave's first on
+  auto word = [&](int f, int v) { return 32 * f + 8 * (v >> 2) + 4 * h + (v & 3); };
   if constexpr (EPI == XE_SUM) {
-    const int a1 = (int)a0 + am;  // the wave's first word of the piece
-    const int left = x.V - a1;    // and how many there are from it on
+    const int a1 = (int)a0 + am;
+    const bool whole = left >= 32 * S::FM, falling = k2 < 0.f;
 #pragma unroll
     for (int i = 0; i < S::FN; ++i) {
       const int64_t t = b0 + bn + 32 * i + c;
       const bool on = t < b_rows;
-      float m = -INFINITY;
-#pragma unroll
-      for (int f = 0; f < S::FM; ++f)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int w = 32 * f + 8 * (v >> 2) + 4 * h + (v & 3);
-          float z = x.scale * acc[f][i][v];
-          z = w < left ? z : -INFINITY;
-          acc[f][i][v] = z;
-          m = fmaxf(m, z);
-        }
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float mm = m == -INFINITY ? 0.f : m;
+      float m = -INFINITY;  // the largest product, or that of their negatives where the scale turns them
       float sum = 0.f;
+      auto top = [&](auto all, float sign) __attribute__((always_inline)) {
 #pragma unroll
-      for (int f = 0; f < S::FM; ++f)
+        for (int f = 0; f < S::FM; ++f)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) sum += __expf(acc[f][i][v] - mm);
+          for (int v = 0; v < 16; ++v)
+            if (decltype(all)::value) m = fmaxf(m, sign * acc[f][i][v]);
+            else m = fmaxf(m, word(f, v) < left ? sign * acc[f][i][v] : -INFINITY);
+        m = fmaxf(m, __shfl_xor(m, 32));
+      };
+      if (!whole) top(std::false_type{}, falling ? -1.f : 1.f);
+      else if (falling) top(std::true_type{}, -1.f);
+      else top(std::true_type{}, 1.f);
+      const float z = fabsf(k2) * m, mm = m == -INFINITY ? 0.f : z;
+      auto add = [&](auto all) __attribute__((always_inline)) {
+#pragma unroll
+        for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(k2, acc[f][i][v], -mm));
+            sum += decltype(all)::value || word(f, v) < left ? e : 0.f;
+          }
+      };
+      if (whole) add(std::true_type{});
+      else add(std::false_type{});
+      pin();
       sum += __shfl_xor(sum, 32);
-      if (on && left > 0 && h == 0) x.part[(int64_t)((x.v0 + a1) / (32 * S::FM)) * x.rows + t] = float2{m, sum};
+      if (on && left > 0 && h == 0)
+        x.part[(int64_t)((x.v0 + a1) / (32 * S::FM)) * x.rows + t] = float2{m == -INFINITY ? m : fabsf(x.scale) * m, sum};
       const int y = on ? x.y[t] - x.v0 - a1 : -1;  // the target among the wave's words
       const bool mine = y >= 0 && y < 32 * S::FM && y < left && ((y >> 2) & 1) == h;
       if (__ballot(mine)) {
@@ -308,14 +324,13 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
 #pragma unroll
         for (int f = 0; f < S::FM; ++f)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) z = y == 32 * f + 8 * (v >> 2) + 4 * h + (v & 3) ? acc[f][i][v] : z;
-        if (mine) x.zt[t] = z;
+          for (int v = 0; v < 16; ++v) z = y == word(f, v) ? acc[f][i][v] : z;
+        if (mine) x.zt[t] = x.scale * z;
       }
     }
   } else if constexpr (EPI == XE_DS) {
     // words past the vocabulary's end are zeros: the products with ds run over whole pieces
     uint8_t* const turn = smem + wave * 32 * xturn_pitch<S::FM, 2>();
-    const int left = x.V - (int)a0 - am;
     const float by = 1.0f / *x.top;
 #pragma unroll
     for (int i = 0; i < S::FN; ++i) {
@@ -323,14 +338,32 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
       const bool on = t < b_rows;
       const float lse = on ? x.lse[t] : 0.f, g = on ? x.g[t] * by : 0.f;
       const int y = on ? x.y[t] - x.v0 - (int)a0 - am : -1;
+      // lse to base 2 in two parts where the values are held to fp32
+      const float l = 1.44269504f * lse, ll = PARTS == 3 ? fmaf(1.44269504f, lse, -l) + 1.92596299e-8f * lse : 0.f;
 #pragma unroll
       for (int f = 0; f < S::FM; ++f)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const int w = 32 * f + 8 * (v >> 2) + 4 * h + (v & 3);
-          const float p = __expf(x.scale * acc[f][i][v] - lse) - (w == y ? 1.f : 0.f);
-          acc[f][i][v] = w < left ? g * p : 0.f;
+          float e = fmaf(k2, acc[f][i][v], -l);
+          if (PARTS == 3) e -= ll;
+          acc[f][i][v] = __builtin_amdgcn_exp2f(e);
         }
+      if (__ballot(y >= 0 && y < 32 * S::FM)) {
+#pragma unroll
+        for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[f][i][v] -= word(f, v) == y ? 1.f : 0.f;
+      }
+      if (left < 32 * S::FM) {
+#pragma unroll
+        for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[f][i][v] = word(f, v) < left ? acc[f][i][v] : 0.f;
+      }
+#pragma unroll
+      for (int f = 0; f < S::FM; ++f)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[f][i][v] *= g;
       // by planes: what the bfloat16 before leaves
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {

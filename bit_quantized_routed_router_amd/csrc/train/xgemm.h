@@ -44,7 +44,7 @@ template <int WM_, int WN_, int FM_, int FN_, int R_>
 struct XShape {
   static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, R = R_;
   static constexpr int BM = 32 * WM * FM, BN = 32 * WN * FN;
-  static constexpr int slot = (BM + BN) * 128, lds = R * slot;
+  static constexpr int slot = (BM + BN) * 128, lds = FM * FN == 16 ? 160 * 1024 : R * slot;
   static constexpr int copies = (BM + BN) / 32;  // a thread's copies per chunk
   static_assert(WM * WN == 4 && lds <= 160 * 1024 && (R - 2) * copies < 64, "four waves, LDS, copies in flight");
 };
@@ -148,60 +148,83 @@ __device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, A
     const int kc = kc0 + ch / Q, q = ch % Q;
     return Chunk{A.chunk(kc, PARTS == 3 ? plane_a(q) : 0, K), B.chunk(kc, PARTS == 3 ? plane_b(q) : 0, K), ch < n};
   };
-  auto copy = [&](const Chunk& x, int i, uint8_t* dst) __attribute__((always_inline)) {
-    if (i < S::BM / 32) A.copy(x.a, x.on, i, dst, wave);
-    else B.copy(x.b, x.on, i - S::BM / 32, dst + S::BM * 128, wave);
-  };
   struct Frags {
     u32x4_t a[S::FM], b[S::FN];
   };
-  auto read = [&](Frags& F, const uint8_t* slot, int j) __attribute__((always_inline)) {
-#pragma unroll
-    for (int f = 0; f < S::FM; ++f) F.a[f] = XSide<S::BM, ACOL>::read(slot, am, f, j, lane);
-#pragma unroll
-    for (int f = 0; f < S::FN; ++f) F.b[f] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, f, j, lane);
-  };
   if constexpr (S::FM * S::FN == 16) {
-    static_assert(S::R == 2 && S::copies == 16, "two chunks in turn");
+    // LDS: two chunks of A in turn, and three of B.  Once everyone has read a
+    // chunk, the A after next takes its place; the B after next has had a place
+    // since the chunk before, so its copies go out while nothing else does.
+    static_assert(S::R == 2 && S::copies == 16, "eight copies of either");
+    constexpr int kSide = S::BM * 128;
+    auto copy_a = [&](const Chunk& x, int i, uint8_t* dst) __attribute__((always_inline)) { A.copy(x.a, x.on, i, dst, wave); };
+    auto copy_b = [&](const Chunk& x, int i, uint8_t* dst) __attribute__((always_inline)) { B.copy(x.b, x.on, i, dst, wave); };
+    auto read1 = [&](Frags& N, int p, const uint8_t* sa, const uint8_t* sb, int j) __attribute__((always_inline)) {
+      if (p < 4) N.a[p] = XSide<S::BM, ACOL>::read(sa, am, p, j, lane);
+      else if (p < 8) N.b[p - 4] = XSide<S::BN, BCOL>::read(sb, bn, p - 4, j, lane);
+    };
     // A step's 16 products; between them the reads of the next step's
-    // fragments (step j of the chunk at slot) and eight copies of chunk x.
-    auto step = [&](const Frags& F, Frags& N, const uint8_t* slot, int j, const Chunk& x, int first, uint8_t* dst)
+    // fragments (step j of the chunk at sa and sb), and copies.
+    auto step = [&](const Frags& F, Frags& N, const uint8_t* sa, const uint8_t* sb, int j, auto copies)
                     __attribute__((always_inline)) {
 #pragma unroll
       for (int p = 0; p < 16; ++p) {
         acc[p % 4][p / 4] = mfma32(F.a[p % 4], F.b[p / 4], acc[p % 4][p / 4]);
         pin();
-        if (p < 4) N.a[p] = XSide<S::BM, ACOL>::read(slot, am, p, j, lane);
-        else if (p < 8) N.b[p - 4] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, p - 4, j, lane);
-        if (first >= 0 && p >= 8) copy(x, first + p - 8, dst);
+        read1(N, p, sa, sb, j);
+        copies(p);
         pin();
       }
     };
     Frags F0, F1;
+    uint8_t *a0 = smem, *a1 = smem + kSide;  // chunk ch's, the next one's
+    uint8_t *b0 = smem + 2 * kSide, *b1 = b0 + kSide, *b2 = b1 + kSide;
     Chunk x = chunk(0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) copy(x, i, smem);
-    vm_wait<0>();
-    ring_barrier();
-    read(F0, smem, 0);
+    for (int i = 0; i < 8; ++i) copy_a(x, i, a0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy_b(x, i, b0);
     x = chunk(1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) copy(x, i, smem + S::slot);
+    for (int i = 0; i < 8; ++i) copy_b(x, i, b1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy_a(x, i, a1);
+    vm_wait<16>();
+    ring_barrier();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) read1(F0, p, a0, b0, 0);
+    x = chunk(2);
 #pragma unroll 1
     for (int ch = 0; ch < n; ++ch) {
-      uint8_t* const slot = smem + (ch & 1) * S::slot;
-      uint8_t* const next = smem + (~ch & 1) * S::slot;
       pin();
-      step(F0, F1, slot, 1, x, 8, next);
-      step(F1, F0, slot, 2, x, -1, next);
-      step(F0, F1, slot, 3, x, -1, next);
-      vm_wait<0>();    // this wave's copies of the next chunk
+      step(F0, F1, a0, b0, 1, [&](int p) __attribute__((always_inline)) { if (p % 4 == 3) copy_b(x, p / 4, b2); });
+      step(F1, F0, a0, b0, 2, [&](int p) __attribute__((always_inline)) { if (p % 4 == 3) copy_b(x, 4 + p / 4, b2); });
+      step(F0, F1, a0, b0, 3, [](int) {});
+      vm_wait<8>();    // this wave's copies of the next chunk; those of the B after it may be under way
       ring_barrier();  // everyone's, and everyone has read this one
-      x = chunk(ch + 2);
       pin();
-      step(F1, F0, next, 0, x, 0, slot);  // (what it reads is not used after the last)
+      // (what it reads is not used after the last chunk)
+      step(F1, F0, a1, b1, 0, [&](int p) __attribute__((always_inline)) { if (p % 2) copy_a(x, p / 2, a0); });
+      uint8_t* const u = a0;
+      a0 = a1;
+      a1 = u;
+      uint8_t* const v = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = v;
+      x = chunk(ch + 3);
     }
   } else {
+    auto copy = [&](const Chunk& x, int i, uint8_t* dst) __attribute__((always_inline)) {
+      if (i < S::BM / 32) A.copy(x.a, x.on, i, dst, wave);
+      else B.copy(x.b, x.on, i - S::BM / 32, dst + S::BM * 128, wave);
+    };
+    auto read = [&](Frags& F, const uint8_t* slot, int j) __attribute__((always_inline)) {
+  #pragma unroll
+      for (int f = 0; f < S::FM; ++f) F.a[f] = XSide<S::BM, ACOL>::read(slot, am, f, j, lane);
+  #pragma unroll
+      for (int f = 0; f < S::FN; ++f) F.b[f] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, f, j, lane);
+    };
 #pragma unroll
     for (int u = 0; u < S::R - 1; ++u) {
       const Chunk x = chunk(u);
