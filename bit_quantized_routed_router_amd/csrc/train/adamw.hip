@@ -11,9 +11,10 @@
 // scale is no power of two, so that a block that only decays is still followed.
 //
 // A block takes a run of one tensor, 8 values to a thread: 32 lanes hold a
-// block of 256, so its largest value stays within half a wave.  Tensors come
-// by value with the launch, kTensors at a time, so that nothing has to be kept
-// or copied between calls; a block finds its tensor by bisection.
+// block of 256, so its largest value stays within half a wave.  Which run is
+// read from a table on the device that the program lays out once: passed with
+// the launch instead, 46 tensors fit, and finding one among arguments in host
+// memory took 8 us a launch (512 tensors of 32768: 236 us in 25 launches).
 #include <algorithm>
 #include <cmath>
 
@@ -23,39 +24,45 @@
 namespace ds4 {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamRun = 4096;       // values of a block
-constexpr int kNormRun = 16384;      // ... of the norm
-constexpr int kTensors = 46;         // of a launch: 4 KB of arguments
+constexpr int64_t kAdamRun = 4096;           // values of a block, or a power of two more:
+constexpr int64_t kAdamBlocks = 1 << 17;     // that many blocks are enough
+constexpr int64_t kAdamParts = 1 << 13;      // and that many sums of squares
 
-struct AdamBatch {
-  int n;
-  int start[kTensors + 1];  // first block of each
-  int64_t first[kTensors];  // the run that it starts with
-  ds4moe_param p[kTensors];
+// The table: ds4moe_param [n], then for each block (tensor, run).
+struct AdamRun {
+  int32_t tensor, run;
 };
-
-template <int RUN>
-static int64_t runs_of(int64_t n) {
-  return (n + RUN - 1) / RUN;
+static size_t adam_map_at(int64_t n) { return (size_t)(n * sizeof(ds4moe_param) + 15) / 16 * 16; }
+static int64_t adam_blocks(const ds4moe_param* p, int n, int64_t run) {
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) blocks += (p[i].n + run - 1) / run;
+  return blocks;
 }
-size_t adam_ws_bytes(const ds4moe_param* p, int n) {
-  int64_t runs = 0;
-  for (int i = 0; i < n; ++i) runs += runs_of<kNormRun>(p[i].n);
-  return std::max<size_t>(256, 8 * (size_t)runs);
+static int64_t adam_run(const ds4moe_param* p, int n) {
+  int64_t run = kAdamRun;
+  // (a tensor has a block at least, however long the runs)
+  while (adam_blocks(p, n, run) > kAdamBlocks + n) run *= 2;
+  return run;
 }
-
-// The tensor of this block, and its first value.
-__device__ inline int adam_tensor(const AdamBatch& b, int run, int64_t& at) {
-  int lo = 0, hi = b.n;
-  const int blk = blockIdx.x;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (b.start[mid] <= blk) lo = mid;
-    else hi = mid;
-  }
-  at = (b.first[lo] + blk - b.start[lo]) * run;
-  return lo;
+size_t adam_table_bytes(const ds4moe_param* p, int n) {
+  return adam_map_at(n) + std::max<size_t>(16, sizeof(AdamRun) * (size_t)adam_blocks(p, n, adam_run(p, n)));
 }
+void adam_table(ds4moe_adamw* A, const ds4moe_param* p, int n, void* table) {
+  A->n_params = n;
+  A->run = adam_run(p, n);
+  A->blocks = 0;
+  std::copy(p, p + n, (ds4moe_param*)table);
+  AdamRun* map = (AdamRun*)((uint8_t*)table + adam_map_at(n));
+  for (int i = 0; i < n; ++i)
+    for (int64_t r = 0; r * A->run < p[i].n; ++r) map[A->blocks++] = {i, (int32_t)r};
+}
+// blocks whose squares are summed together, and how many such groups there are
+static int adam_group(const ds4moe_adamw& A) { return (int)((A.blocks + kAdamParts - 1) / kAdamParts); }
+static int64_t adam_groups(const ds4moe_adamw& A) {
+  const int g = adam_group(A);
+  return g ? (A.blocks + g - 1) / g : 0;
+}
+size_t adam_ws_bytes(const ds4moe_adamw& A) { return std::max<size_t>(256, 8 * (size_t)adam_groups(A)); }
 
 // Eight values from i on, `left` of them there; zeros for the others.
 template <bool BF>
@@ -156,14 +163,14 @@ struct AdamScalars {
   const float *lr_dev, *grad_scale;
   const int32_t* step_dev;
 };
-static_assert(sizeof(AdamBatch) + sizeof(AdamScalars) <= 4096, "arguments of a launch");
 
 template <bool PBF, bool GBF, bool FP8>
-__global__ __launch_bounds__(kAdamThreads) void k_adamw(AdamBatch b, AdamScalars s) {
-  int64_t at;
-  const int t = adam_tensor(b, kAdamRun, at);
-  const ds4moe_param q = b.p[t];
+__global__ __launch_bounds__(kAdamThreads) void k_adamw(const ds4moe_param* __restrict__ params,
+                                                        const AdamRun* __restrict__ map, int64_t run, AdamScalars s) {
   const float gs = s.grad_scale ? *s.grad_scale : 1.0f;
+  const AdamRun r = map[blockIdx.x];
+  const ds4moe_param q = params[r.tensor];
+  const int64_t at = r.run * run;
   if (!(fabsf(gs) <= 3.402823466e38f)) return;  // a step without finite gradients changes nothing
   const double lr = s.lr_dev ? (double)*s.lr_dev : s.lr;
   double c1 = s.c1, c2 = s.c2;
@@ -176,7 +183,7 @@ __global__ __launch_bounds__(kAdamThreads) void k_adamw(AdamBatch b, AdamScalars
   const uintptr_t align = (uintptr_t)q.param | (uintptr_t)q.grad | (uintptr_t)q.master |
                           (FP8 ? ((uintptr_t)q.m | (uintptr_t)q.v) << 1 : (uintptr_t)q.m | (uintptr_t)q.v);
   const bool vec = (align & 15) == 0;
-  const int64_t end = min(at + kAdamRun, q.n);
+  const int64_t end = min(at + run, q.n);
   // FP8: every lane of a block of 256 stays, so that its largest value is known
   for (int64_t i0 = at; i0 < end; i0 += 8 * kAdamThreads) {
     const int64_t i = i0 + 8 * threadIdx.x;
@@ -238,21 +245,25 @@ __device__ inline double block_sum(double x, double* lds, int waves) {
   return x;
 }
 template <bool GBF>
-__global__ __launch_bounds__(kAdamThreads) void k_adamw_squares(AdamBatch b, double* __restrict__ part) {
+__global__ __launch_bounds__(kAdamThreads) void k_adamw_squares(const ds4moe_param* __restrict__ params,
+                                                                const AdamRun* __restrict__ map, int64_t blocks,
+                                                                int group, int64_t run, double* __restrict__ part) {
   __shared__ double lds[kAdamThreads / 64];
-  int64_t at;
-  const int t = adam_tensor(b, kNormRun, at);
-  const ds4moe_param q = b.p[t];
-  const bool vec = ((uintptr_t)q.grad & 15) == 0;
-  const int64_t end = min(at + kNormRun, q.n);
   double sum = 0.0;
-#pragma unroll 4
-  for (int64_t i = at + 8 * threadIdx.x; i < end; i += 8 * kAdamThreads) {
-    const int left = (int)min((int64_t)8, end - i);
-    float g[8];
-    get8<GBF>(q.grad, i, left, vec && left == 8, g);
+  const int64_t last = min(blocks, ((int64_t)blockIdx.x + 1) * group);
+  for (int64_t b = (int64_t)blockIdx.x * group; b < last; ++b) {
+    const AdamRun r = map[b];
+    const void* grad = params[r.tensor].grad;
+    const int64_t at = r.run * run, end = min(at + run, params[r.tensor].n);
+    const bool vec = ((uintptr_t)grad & 15) == 0;
+#pragma unroll 2
+    for (int64_t i = at + 8 * threadIdx.x; i < end; i += 8 * kAdamThreads) {
+      const int left = (int)min((int64_t)8, end - i);
+      float g[8];
+      get8<GBF>(grad, i, left, vec && left == 8, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += (double)g[e] * (double)g[e];
+      for (int e = 0; e < 8; ++e) sum += (double)g[e] * (double)g[e];
+    }
   }
   sum = block_sum(sum, lds, kAdamThreads / 64);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
@@ -271,40 +282,10 @@ __global__ __launch_bounds__(1024) void k_adamw_norm(const double* __restrict__ 
 }
 
 // ---------------------------------------------------------------- launches
-// Tensors by batches of kTensors and of fewer than 2^23 blocks.
-template <int RUN, typename Launch>
-static hipError_t adam_batches(const ds4moe_param* p, int n, Launch launch) {
-  constexpr int64_t kMost = 1 << 23;
-  AdamBatch b;
-  b.n = 0;
-  b.start[0] = 0;
-  int64_t done = 0;  // runs of the batches before
-  auto flush = [&]() -> hipError_t {
-    if (b.n == 0) return hipSuccess;
-    const hipError_t e = launch(b, done);
-    done += b.start[b.n];
-    b.n = 0;
-    return e;
-  };
-  for (int i = 0; i < n; ++i) {
-    const int64_t runs = runs_of<RUN>(p[i].n);
-    for (int64_t r = 0; r < runs;) {
-      const int64_t take = std::min(runs - r, kMost - b.start[b.n]);
-      if (b.n == kTensors || take <= 0) {
-        const hipError_t e = flush();
-        if (e) return e;
-        continue;
-      }
-      b.p[b.n] = p[i];
-      b.first[b.n] = r;
-      b.start[b.n + 1] = b.start[b.n] + (int)take;
-      ++b.n;
-      r += take;
-    }
-  }
-  return flush();
+static const ds4moe_param* adam_params(const AdamCall& c) { return (const ds4moe_param*)c.table; }
+static const AdamRun* adam_map(const AdamCall& c) {
+  return (const AdamRun*)((const uint8_t*)c.table + adam_map_at(c.A.n_params));
 }
-
 template <bool PBF, bool GBF, bool FP8>
 static hipError_t adam_step(const AdamCall& c) {
   AdamScalars s{};
@@ -322,10 +303,10 @@ static hipError_t adam_step(const AdamCall& c) {
   s.lr_dev = A.lr_dev;
   s.step_dev = A.step_dev;
   s.grad_scale = c.grad_scale;
-  return adam_batches<kAdamRun>(c.p, c.n, [&](const AdamBatch& b, int64_t) {
-    DS4_LAUNCH((k_adamw<PBF, GBF, FP8>), dim3((unsigned)b.start[b.n]), dim3(kAdamThreads), 0, c.st, b, s);
-    return hipGetLastError();
-  });
+  if (A.blocks == 0) return hipSuccess;
+  DS4_LAUNCH((k_adamw<PBF, GBF, FP8>), dim3((unsigned)A.blocks), dim3(kAdamThreads), 0, c.st, adam_params(c), adam_map(c),
+             A.run, s);
+  return hipGetLastError();
 }
 template <bool PBF, bool GBF>
 static hipError_t adam_step_state(const AdamCall& c) {
@@ -341,14 +322,11 @@ hipError_t launch_adamw_step(const AdamCall& c) {
 
 template <bool GBF>
 static hipError_t adam_norm(const AdamCall& c) {
-  int64_t runs = 0;
-  const hipError_t e = adam_batches<kNormRun>(c.p, c.n, [&](const AdamBatch& b, int64_t done) {
-    DS4_LAUNCH((k_adamw_squares<GBF>), dim3((unsigned)b.start[b.n]), dim3(kAdamThreads), 0, c.st, b, c.ws + done);
-    runs = done + b.start[b.n];
-    return hipGetLastError();
-  });
-  if (e) return e;
-  DS4_LAUNCH(k_adamw_norm, dim3(1), dim3(1024), 0, c.st, (const double*)c.ws, runs, c.max_norm, c.out);
+  const int64_t groups = adam_groups(c.A);
+  if (groups > 0)
+    DS4_LAUNCH((k_adamw_squares<GBF>), dim3((unsigned)groups), dim3(kAdamThreads), 0, c.st, adam_params(c), adam_map(c),
+               c.A.blocks, adam_group(c.A), c.A.run, c.ws);
+  DS4_LAUNCH(k_adamw_norm, dim3(1), dim3(1024), 0, c.st, (const double*)c.ws, groups, c.max_norm, c.out);
   return hipGetLastError();
 }
 hipError_t launch_adamw_norm(const AdamCall& c) {

@@ -45,33 +45,42 @@ static int check_xent_args(const XentCall& c, bool grad, size_t ws_bytes) {
 
 static bool params_ok(const ds4moe_param* p, int32_t n) {
   if (n < 0 || n > kAdamMaxTensors) return false;
-  for (int32_t i = 0; i < n; ++i)
+  int64_t all = 0;
+  for (int32_t i = 0; i < n; ++i) {
     if (p[i].n < 0 || p[i].n > kAdamMaxN) return false;
-  return true;
-}
-static int check_adamw(const ds4moe_adamw* A, const ds4moe_param* p, int32_t n, bool step) {
-  if (!A || (!p && n != 0) || !dt_ok(A->grad_dtype)) return DS4MOE_EINVAL;
-  if (!params_ok(p, n)) return DS4MOE_ESHAPE;
-  if (step) {
-    if (!dt_ok(A->param_dtype) || (A->state != DS4MOE_STATE_F32 && A->state != DS4MOE_STATE_FP8)) return DS4MOE_EINVAL;
-    if (!std::isfinite(A->lr) || !std::isfinite(A->eps) || !((float)A->eps > 0.0f)) return DS4MOE_EINVAL;
-    if (!(A->beta1 >= 0.0 && A->beta1 < 1.0) || !(A->beta2 >= 0.0 && A->beta2 < 1.0)) return DS4MOE_EINVAL;
-    if (!al(A->lr_dev, 4) || !al(A->step_dev, 4)) return DS4MOE_EALIGN;
+    all += p[i].n;
   }
+  return all <= kAdamMaxN;
+}
+static int check_options(const ds4moe_adamw* A) {
+  if (!A || !dt_ok(A->grad_dtype) || !dt_ok(A->param_dtype)) return DS4MOE_EINVAL;
+  if (A->state != DS4MOE_STATE_F32 && A->state != DS4MOE_STATE_FP8) return DS4MOE_EINVAL;
+  if (!std::isfinite(A->lr) || !std::isfinite(A->eps) || !((float)A->eps > 0.0f)) return DS4MOE_EINVAL;
+  if (!(A->beta1 >= 0.0 && A->beta1 < 1.0) || !(A->beta2 >= 0.0 && A->beta2 < 1.0)) return DS4MOE_EINVAL;
+  return al(A->lr_dev, 4) && al(A->step_dev, 4) ? DS4MOE_OK : DS4MOE_EALIGN;
+}
+static int check_params(const ds4moe_adamw* A, const ds4moe_param* p, int32_t n) {
   const bool fp8 = A->state == DS4MOE_STATE_FP8;
   for (int32_t i = 0; i < n; ++i) {
     const ds4moe_param& q = p[i];
+    if (!std::isfinite(q.weight_decay)) return DS4MOE_EINVAL;
     if (q.n == 0) continue;
-    if (!q.grad) return DS4MOE_EINVAL;
-    if (!al(q.grad, dt_size(A->grad_dtype))) return DS4MOE_EALIGN;
-    if (!step) continue;
-    if (!q.param || !q.m || !q.v || (fp8 && (!q.m_scale || !q.v_scale)) || !std::isfinite(q.weight_decay))
-      return DS4MOE_EINVAL;
-    if (!al(q.param, dt_size(A->param_dtype)) || !al(q.master, 4) || !al(q.m, fp8 ? 1 : 4) || !al(q.v, fp8 ? 1 : 4))
+    if (!q.param || !q.grad || !q.m || !q.v || (fp8 && (!q.m_scale || !q.v_scale))) return DS4MOE_EINVAL;
+    if (!al(q.param, dt_size(A->param_dtype)) || !al(q.grad, dt_size(A->grad_dtype)) || !al(q.master, 4) ||
+        !al(q.m, fp8 ? 1 : 4) || !al(q.v, fp8 ? 1 : 4) || (fp8 && (!al(q.m_scale, 4) || !al(q.v_scale, 4))))
       return DS4MOE_EALIGN;
-    if (fp8 && (!al(q.m_scale, 4) || !al(q.v_scale, 4))) return DS4MOE_EALIGN;
   }
   return DS4MOE_OK;
+}
+// a descriptor that ds4moe_adamw_table has filled in, and its table
+static int check_table(const ds4moe_adamw* A, const void* table) {
+  const int rc = check_options(A);
+  if (rc) return rc;
+  if (A->n_params < 0 || A->n_params > kAdamMaxTensors || A->blocks < 0 || A->blocks > kAdamMaxBlocks || A->run < 256 ||
+      A->run % 256)
+    return DS4MOE_ESHAPE;
+  if (!table) return DS4MOE_EINVAL;
+  return al(table, 16) ? DS4MOE_OK : DS4MOE_EALIGN;
 }
 
 }  // namespace ds4
@@ -190,38 +199,52 @@ int ds4moe_xent_grad(const void* h, const void* w, int dtype, int64_t T, int64_t
 }
 
 // ---------------------------------------------------------------- AdamW
-int ds4moe_adamw_step(const ds4moe_adamw* A, const ds4moe_param* params, int32_t n_params, int64_t step,
-                      const float* grad_scale, void* stream) {
-  const int rc = check_adamw(A, params, n_params, true);
+size_t ds4moe_adamw_table_bytes(const ds4moe_param* params, int32_t n_params) {
+  if ((!params && n_params != 0) || !params_ok(params, n_params)) return 0;
+  return adam_table_bytes(params, n_params);
+}
+
+int ds4moe_adamw_table(ds4moe_adamw* A, const ds4moe_param* params, int32_t n_params, void* table, size_t table_bytes) {
+  int rc = check_options(A);
+  if (rc) return rc;
+  if (!table || (!params && n_params != 0)) return DS4MOE_EINVAL;
+  if (!params_ok(params, n_params)) return DS4MOE_ESHAPE;
+  if ((rc = check_params(A, params, n_params))) return rc;
+  if (!al(table, 8)) return DS4MOE_EALIGN;
+  if (table_bytes < adam_table_bytes(params, n_params)) return DS4MOE_EWORKSPACE;
+  adam_table(A, params, n_params, table);
+  return DS4MOE_OK;
+}
+
+int ds4moe_adamw_step(const ds4moe_adamw* A, const void* table, int64_t step, const float* grad_scale, void* stream) {
+  const int rc = check_table(A, table);
   if (rc) return rc;
   if (step < 1 && !A->step_dev) return DS4MOE_EINVAL;
   if (!al(grad_scale, 4)) return DS4MOE_EALIGN;
   AdamCall c{};
   c.A = *A;
-  c.p = params;
-  c.n = n_params;
+  c.table = table;
   c.step = step;
   c.grad_scale = grad_scale;
   c.st = (hipStream_t)stream;
   return status(launch_adamw_step(c));
 }
 
-size_t ds4moe_adamw_workspace_bytes(const ds4moe_param* params, int32_t n_params) {
-  if ((!params && n_params != 0) || !params_ok(params, n_params)) return 0;
-  return adam_ws_bytes(params, n_params);
+size_t ds4moe_adamw_workspace_bytes(const ds4moe_adamw* A) {
+  if (!A || A->blocks < 0 || A->blocks > kAdamMaxBlocks) return 0;
+  return adam_ws_bytes(*A);
 }
 
-int ds4moe_adamw_norm(const ds4moe_adamw* A, const ds4moe_param* params, int32_t n_params, float max_norm, float* out,
-                      void* ws, size_t ws_bytes, void* stream) {
-  const int rc = check_adamw(A, params, n_params, false);
+int ds4moe_adamw_norm(const ds4moe_adamw* A, const void* table, float max_norm, float* out, void* ws, size_t ws_bytes,
+                      void* stream) {
+  const int rc = check_table(A, table);
   if (rc) return rc;
   if (!(max_norm > 0.0f) || !out || !ws) return DS4MOE_EINVAL;
   if (!al(out, 4) || !al(ws, 256)) return DS4MOE_EALIGN;
-  if (ws_bytes < adam_ws_bytes(params, n_params)) return DS4MOE_EWORKSPACE;
+  if (ws_bytes < adam_ws_bytes(*A)) return DS4MOE_EWORKSPACE;
   AdamCall c{};
   c.A = *A;
-  c.p = params;
-  c.n = n_params;
+  c.table = table;
   c.max_norm = max_norm;
   c.out = out;
   c.ws = (double*)ws;

@@ -10,8 +10,9 @@ namespace ds4 {
 // ---------------------------------------------------------------- limits
 constexpr int kBalMaxSeqs = 16384;         // sequences of a balance call
 constexpr int64_t kXentMaxV = 1 << 20;     // words of a vocabulary
-constexpr int64_t kAdamMaxN = 1ll << 40;   // values of one tensor
+constexpr int64_t kAdamMaxN = 1ll << 40;   // values of all tensors
 constexpr int kAdamMaxTensors = 1 << 20;
+constexpr int64_t kAdamMaxBlocks = (1 << 17) + 2 * kAdamMaxTensors;
 
 // ---------------------------------------------------------------- balance
 struct BalanceCall {
@@ -52,8 +53,7 @@ hipError_t launch_xent_grad(const XentCall& c);
 // ---------------------------------------------------------------- AdamW
 struct AdamCall {
   ds4moe_adamw A;
-  const ds4moe_param* p;
-  int n;
+  const void* table;
   int64_t step;
   const float* grad_scale;
   float max_norm;
@@ -61,7 +61,9 @@ struct AdamCall {
   double* ws;
   hipStream_t st;
 };
-size_t adam_ws_bytes(const ds4moe_param* p, int n);
+size_t adam_table_bytes(const ds4moe_param* p, int n);
+void adam_table(ds4moe_adamw* A, const ds4moe_param* p, int n, void* table);
+size_t adam_ws_bytes(const ds4moe_adamw& A);
 hipError_t launch_adamw_step(const AdamCall& c);
 hipError_t launch_adamw_norm(const AdamCall& c);
 

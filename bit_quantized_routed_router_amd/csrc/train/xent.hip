@@ -14,6 +14,7 @@
 // fp32: 1 / rows, which most losses have there, would otherwise be rounded the
 // same way in every value (dh 0.0034 off, against 0.002).
 #include <algorithm>
+#include <numeric>
 #include <type_traits>
 
 #include "../trace.h"
@@ -27,11 +28,41 @@ namespace ds4 {
 // (ds, and the planes of an fp32 w) and, in the forward pass, rows (the partial
 // sums).
 constexpr int64_t kXentPiece = 128 << 20;   // bytes that either aims at
-constexpr int kXentSlabs = 4;               // parts of the sum over words in dh, at most
+constexpr int kXentSlabs = 8;               // parts of the sum over words in dh, at most
 
 template <typename T>
 static T round_up(T v, T m) {
   return (v + m - 1) / m * m;
+}
+
+// Shapes of a product's tiles (a's by b's), and the words that a wave of one
+// has, which a partial sum covers.
+enum { kFew, kSmall, kMid, kBig };  // 128 x 32, 64 x 64, 128 x 128, 256 x 256
+constexpr int kXentPart[] = {32, 32, 64, 128};
+
+// Which: 256 x 256 (one block to a CU) where it has blocks for more than half
+// of the chip's CUs, else 128 x 128 (two to a CU) on the same condition, else 64 x 64.
+static int xent_shape(int64_t a, int64_t b, int64_t splits) {
+  auto blocks = [&](int64_t m) { return (a + m - 1) / m * ((b + m - 1) / m) * splits; };
+  return blocks(256) > 128 ? kBig : blocks(128) > 128 ? kMid : kSmall;
+}
+
+// A product over `words` words by `rows` rows (or columns) as one launch, or
+// as two: full rounds of 256 blocks, and what a last round would leave more than
+// half of the chip idle for in smaller tiles.
+struct XentLaunch {
+  int shape;
+  int64_t w0, words;
+};
+static int xent_launches(int64_t words, int64_t rows, XentLaunch (&l)[2]) {
+  l[0] = {xent_shape(words, rows, 1), 0, words};
+  if (l[0].shape != kBig) return 1;
+  const int64_t per = (rows + 255) / 256, blocks = (words + 255) / 256 * per, rest = blocks % 256;
+  const int64_t first = blocks / 256 * 256 / per * 256;
+  if (rest == 0 || rest > 128 || first == 0 || first >= words) return 1;
+  l[0].words = first;
+  l[1] = {xent_shape(words - first, rows, 1), first, words - first};
+  return 2;
 }
 
 struct XentPlan {
@@ -39,38 +70,41 @@ struct XentPlan {
   int64_t piece;      // words of a piece, a multiple of 256
   int pieces;
   int64_t rows;       // rows of a forward pass over the vocabulary
-  int64_t hp, dsp;    // bytes from row to row of h's copy and of ds
   int slabs;
   // offsets into the workspace
   size_t hc, wp, n, live, y, lse, g, ds, slab, zt, part, bytes;
 };
 
-static bool xent_small(int64_t T) { return T <= 64; }  // tiles of 32 rows, 32 words a wave
+static bool xent_few(int64_t T) { return T <= 32; }
 
 static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
   XentPlan p{};
   p.parts = dt == DS4MOE_DT_F32 ? 3 : 1;
   // bytes per word of what a piece keeps: ds, and the planes of an fp32 w
   const int64_t per = 2 * p.parts * std::max<int64_t>(grad ? T : 0, p.parts == 3 ? d : 0);
-  const int64_t all = round_up<int64_t>(V, 256);
-  int64_t most = per ? std::max<int64_t>(2048, kXentPiece / per / 256 * 256) : all;
-  p.pieces = (int)((all + most - 1) / most);
-  p.piece = round_up<int64_t>((all + p.pieces - 1) / p.pieces, 256);
+  const int64_t all = round_up<int64_t>(V, 256), tr = (T + 255) / 256, td = d / 256;
+  const int64_t most = per ? std::max<int64_t>(2048, kXentPiece / per / 256 * 256) : all;
+  // words of a piece whose products are full rounds of blocks
+  const int64_t unit = 256 * std::max(256 / std::gcd<int64_t>(256, tr), 256 / std::gcd<int64_t>(256, td));
+  if (most >= all) p.piece = all;
+  else if (most >= unit) p.piece = most / unit * unit;
+  else p.piece = round_up<int64_t>((all + (all + most - 1) / most - 1) / ((all + most - 1) / most), 256);
   p.pieces = (int)((all + p.piece - 1) / p.piece);
+  // parts of dh's sum, as long as they fill the chip better
   p.slabs = 1;
-  if (grad) {
-    const int64_t tiles = (T + 127) / 128 * ((d + 127) / 128);
-    while (p.slabs < kXentSlabs && tiles * p.slabs < 512 && p.piece / p.slabs >= 2048) p.slabs *= 2;
-  }
+  auto full = [&](int s) {
+    const int64_t n = tr * td * s;
+    return (double)n / (double)((n + 255) / 256 * 256);
+  };
+  for (int s = 2; s <= kXentSlabs && p.piece / s >= 256; s *= 2)
+    if (full(s) > full(p.slabs)) p.slabs = s;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += round_up<size_t>(bytes, 256);
     return here;
   };
-  p.hp = 2 * (int64_t)d;
-  p.dsp = 2 * p.piece;
-  if (p.parts == 3 || grad) p.hc = take((size_t)p.parts * T * p.hp);
+  if (p.parts == 3 || grad) p.hc = take((size_t)2 * p.parts * T * d);
   if (p.parts == 3) p.wp = take((size_t)6 * p.piece * d);
   if (grad) {
     p.n = take(8);
@@ -78,13 +112,25 @@ static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
     p.y = take(4 * T);
     p.lse = take(4 * T);
     p.g = take(4 * T);
-    p.ds = take((size_t)p.parts * T * p.dsp);
+    p.ds = take((size_t)2 * p.parts * T * p.piece);
     p.slab = take((size_t)4 * p.slabs * T * d);
   } else {
-    const int64_t parts = all / (xent_small(T) ? 32 : 64);
+    const int64_t parts = all / (xent_few(T) ? 32 : 128);
     p.rows = std::min(T, std::max<int64_t>(1024, kXentPiece / (8 * parts) / 256 * 256));
     p.zt = take(4 * p.rows);
-    p.part = take((size_t)8 * p.rows * parts);
+    auto sums = [&](int64_t rows) {  // partial sums of that many rows
+      int64_t n = 0;
+      for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+        XentLaunch l[2];
+        const int m = xent_launches(std::min(p.piece, V - v0), rows, l);
+        for (int i = 0; i < m; ++i) {
+          const int per = kXentPart[xent_few(T) ? kFew : l[i].shape];
+          n += (l[i].words + per - 1) / per;
+        }
+      }
+      return n * rows;
+    };
+    p.part = take((size_t)8 * std::max(sums(p.rows), T % p.rows ? sums(T % p.rows) : 0));
   }
   p.bytes = at;
   return p;
@@ -168,8 +214,7 @@ __device__ inline void xsplit8(const float (&x)[8], u32x4_t (&o)[3]) {
 template <bool BF>
 __global__ __launch_bounds__(256) void k_xent_rows(const void* __restrict__ src, const int32_t* __restrict__ n,
                                                    const int32_t* __restrict__ live, int64_t rows, int d,
-                                                   uint8_t* __restrict__ dst, int64_t pitch, int64_t plane,
-                                                   void* __restrict__ dh) {
+                                                   uint8_t* __restrict__ dst, int64_t plane, void* __restrict__ dh) {
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const int64_t from = live ? live[r] : r;
     const bool on = !n || r < *n;
@@ -177,14 +222,14 @@ __global__ __launch_bounds__(256) void k_xent_rows(const void* __restrict__ src,
       if (on) {
         const Raw8<BF> v = ld8<BF>(src, from * d + i);
         if constexpr (BF) {
-          *(u32x4_t*)(dst + r * pitch + i * 2) = v.a;
+          *(u32x4_t*)(dst + (r * d + i) * 2) = v.a;
         } else {
           float x[8];
           u32x4_t o[3];
           unpack8<BF>(v, x);
           xsplit8(x, o);
 #pragma unroll
-          for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + r * pitch + i * 2) = o[s];
+          for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + (r * d + i) * 2) = o[s];
         }
       } else if (dh) {
         const float zero[8] = {};
@@ -203,10 +248,10 @@ struct XArgs {
   int splits;        // of k
   // epilogues
   float scale;
-  int V;             // words of the piece
+  int V;             // words of the launch
   const int32_t* y;
-  int v0;            // the piece's first word
-  int rows;          // partial sums: rows of one
+  int v0;            // its first word
+  int rows, part0;   // partial sums: rows of one, and the first of this launch
   float2* part;
   float* zt;
   const float *lse, *g, *top;
@@ -316,7 +361,7 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
       pin();
       sum += __shfl_xor(sum, 32);
       if (on && left > 0 && h == 0)
-        x.part[(int64_t)((x.v0 + a1) / (32 * S::FM)) * x.rows + t] = float2{m == -INFINITY ? m : fabsf(x.scale) * m, sum};
+        x.part[(int64_t)(x.part0 + a1 / (32 * S::FM)) * x.rows + t] = float2{m == -INFINITY ? m : fabsf(x.scale) * m, sum};
       const int y = on ? x.y[t] - x.v0 - a1 : -1;  // the target among the wave's words
       const bool mine = y >= 0 && y < 32 * S::FM && y < left && ((y >> 2) & 1) == h;
       if (__ballot(mine)) {
@@ -403,33 +448,38 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
 }
 
 // ---------------------------------------------------------------- joins
-// loss and lse of the rows from their partial sums: 32 rows by 32 shares of
-// the parts to a block.
-__device__ inline void xent_add(float& m, float& sum, bool& nan, float2 v) {
-  const float top = fmaxf(m, v.x), mm = top == -INFINITY ? 0.f : top;
-  sum = sum * __expf(m - mm) + v.y * __expf(v.x - mm);
-  nan |= v.y != v.y;
-  m = top;
+// loss and lse of the rows from their partial sums: R rows by 1024 / R shares
+// of the parts to a block (R = 4 where few rows have many parts: 16 rows of
+// 2048 parts 13 -> 5 us).
+__device__ inline void xent_add(float2& a, float2 b) {
+  const float top = fmaxf(a.x, b.x), mm = top == -INFINITY ? 0.f : top;
+  // (a sum that is no number stays one, whatever it is multiplied by)
+  a = float2{top, a.y * __expf(a.x - mm) + b.y * __expf(b.x - mm)};
 }
+template <int R>
 __global__ __launch_bounds__(1024) void k_xent_join(const float2* __restrict__ part, int parts, int64_t rows,
                                                     const int32_t* __restrict__ target, int V,
                                                     const float* __restrict__ zt, float* __restrict__ loss,
                                                     float* __restrict__ lse) {
-  __shared__ float2 lds[32][33];
-  const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
-  const int64_t r = (int64_t)blockIdx.x * 32 + c;
+  constexpr int S = 1024 / R;
+  __shared__ float2 lds[1024];
+  const int tid = threadIdx.x, c = tid % R, s = tid / R;
+  const int64_t r = (int64_t)blockIdx.x * R + c;
   const bool on = r < rows;
-  float m = -INFINITY, sum = 0.f;
-  bool nan = false;
+  float2 a = {-INFINITY, 0.f};
   if (on) {
 #pragma unroll 8
-    for (int p = s; p < parts; p += 32) xent_add(m, sum, nan, part[(int64_t)p * rows + r]);
+    for (int p = s; p < parts; p += S) xent_add(a, part[(int64_t)p * rows + r]);
   }
-  lds[s][c] = float2{m, nan ? NAN : sum};
+  lds[tid] = a;
   __syncthreads();
+#pragma unroll 1
+  for (int o = 512; o >= R; o >>= 1) {
+    if (tid < o) xent_add(lds[tid], lds[tid + o]);
+    __syncthreads();
+  }
   if (s != 0 || !on) return;
-  for (int i = 1; i < 32; ++i) xent_add(m, sum, nan, lds[i][c]);
-  const float l = nan ? NAN : m + logf(sum);
+  const float l = lds[tid].x + logf(lds[tid].y);
   lse[r] = l;
   const int y = target[r];
   loss[r] = y >= 0 && y < V ? l - zt[r] : 0.f;
@@ -461,9 +511,10 @@ __global__ __launch_bounds__(256) void k_xent_dh(const float* __restrict__ slab,
 }
 
 // ---------------------------------------------------------------- launches
-using XBig = XShape<2, 2, 4, 4, 2>;    // 256 x 256
-using XMid = XShape<2, 2, 2, 2, 2>;    // 128 x 128, two blocks to a CU
-using XFew = XShape<4, 1, 1, 1, 3>;    // 128 a's x 32 b's, two blocks to a CU
+using XFew = XShape<4, 1, 1, 1, 3>;    // two blocks to a CU, as the next two have
+using XSmall = XShape<2, 2, 1, 1, 4>;
+using XMid = XShape<2, 2, 2, 2, 2>;
+using XBig = XShape<2, 2, 4, 4, 2>;
 
 template <class S, int EPI, int PARTS, bool OBF>
 static hipError_t xent_launch(const XArgs& x, hipStream_t st) {
@@ -472,40 +523,71 @@ static hipError_t xent_launch(const XArgs& x, hipStream_t st) {
   return hipGetLastError();
 }
 template <int EPI, int PARTS, bool OBF>
-static hipError_t xent_gemm(const XArgs& x, hipStream_t st) {
-  const int64_t big = (x.a_rows + 255) / 256 * ((x.b_rows + 255) / 256) * x.splits;
-  if (big >= 192) return xent_launch<XBig, EPI, PARTS, OBF>(x, st);
-  return xent_launch<XMid, EPI, PARTS, OBF>(x, st);
+static hipError_t xent_shaped(int shape, const XArgs& x, hipStream_t st) {
+  if constexpr (EPI == XE_SUM) {
+    if (shape == kFew) return xent_launch<XFew, EPI, PARTS, OBF>(x, st);
+  }
+  if (shape == kSmall) return xent_launch<XSmall, EPI, PARTS, OBF>(x, st);
+  if (shape == kMid) return xent_launch<XMid, EPI, PARTS, OBF>(x, st);
+  return xent_launch<XBig, EPI, PARTS, OBF>(x, st);
+}
+// The product of a piece: its words are a's, or b's (dw); the sum over words
+// of dh is one launch.
+template <int EPI, int PARTS, bool OBF>
+static hipError_t xent_gemm(XArgs& x, bool few, hipStream_t st) {
+  if (EPI == XE_SLAB) return xent_shaped<EPI, PARTS, OBF>(xent_shape(x.a_rows, x.b_rows, x.splits), x, st);
+  constexpr bool of_b = EPI == XE_ROWS;
+  XentLaunch l[2];
+  const int n = xent_launches(of_b ? x.b_rows : x.a_rows, of_b ? x.a_rows : x.b_rows, l);
+  for (int i = 0; i < n; ++i) {
+    XArgs y = x;
+    const int shape = few ? kFew : l[i].shape;
+    if (of_b) {
+      y.b.p += 2 * l[i].w0;
+      y.b_rows = l[i].words;
+      y.out += l[i].w0 * y.out_pitch;
+    } else {
+      y.a.p += l[i].w0 * y.a.pitch;
+      y.a_rows = l[i].words;
+      y.V = (int)l[i].words;
+      y.v0 += (int)l[i].w0;
+      y.out += 2 * l[i].w0;
+      x.part0 += (int)((l[i].words + kXentPart[shape] - 1) / kXentPart[shape]);
+    }
+    const hipError_t e = xent_shaped<EPI, PARTS, OBF>(shape, y, st);
+    if (e) return e;
+  }
+  return hipSuccess;
 }
 static unsigned xent_row_blocks(int64_t rows) { return (unsigned)std::min<int64_t>(rows, 8192); }
 
 // all rows of an fp32 matrix as planes
-static void xent_copy(const void* src, int64_t rows, int d, uint8_t* dst, int64_t pitch, int64_t plane, hipStream_t st) {
+static void xent_copy(const void* src, int64_t rows, int d, uint8_t* dst, int64_t plane, hipStream_t st) {
   DS4_LAUNCH(k_xent_rows<false>, dim3(xent_row_blocks(rows)), dim3(256), 0, st, src, (const int32_t*)nullptr,
-             (const int32_t*)nullptr, rows, d, dst, pitch, plane, (void*)nullptr);
+             (const int32_t*)nullptr, rows, d, dst, plane, (void*)nullptr);
 }
 
 template <int PARTS>
 static hipError_t xent_forward(const XentCall& c) {
   const XentPlan p = xent_plan(c.dt, c.T, c.V, c.d, false);
   uint8_t* w = c.ws;
-  const bool few = xent_small(c.T);
-  const int per = few ? 32 : 128;  // words of a partial sum
+  const bool few = xent_few(c.T);
   const int64_t pitch = 2 * (int64_t)c.d;
   XOperand h = {(const uint8_t*)c.h, 0, pitch};
   if (PARTS == 3) {
-    h = {w + p.hc, c.T * p.hp, p.hp};
-    xent_copy(c.h, c.T, c.d, w + p.hc, h.pitch, h.plane, c.st);
+    h = {w + p.hc, c.T * pitch, pitch};
+    xent_copy(c.h, c.T, c.d, w + p.hc, h.plane, c.st);
   }
   for (int64_t r0 = 0; r0 < c.T; r0 += p.rows) {
     const int64_t rows = std::min(c.T - r0, p.rows);
+    int parts = 0;
     for (int i = 0; i < p.pieces; ++i) {
       const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
       const uint8_t* src = (const uint8_t*)c.w + v0 * pitch * (PARTS == 3 ? 2 : 1);
       XArgs x{};
       x.a = {src, 0, pitch};
       if (PARTS == 3) {
-        xent_copy(src, words, c.d, w + p.wp, pitch, p.piece * pitch, c.st);
+        xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
         x.a = {w + p.wp, p.piece * pitch, pitch};
       }
       x.b = {h.p + r0 * h.pitch, h.plane, h.pitch};
@@ -519,13 +601,18 @@ static hipError_t xent_forward(const XentCall& c) {
       x.v0 = (int)v0;
       x.rows = (int)rows;
       x.part = (float2*)(w + p.part);
+      x.part0 = parts;
       x.zt = (float*)(w + p.zt);
-      const hipError_t e = few ? xent_launch<XFew, XE_SUM, PARTS, false>(x, c.st) : xent_launch<XBig, XE_SUM, PARTS, false>(x, c.st);
+      const hipError_t e = xent_gemm<XE_SUM, PARTS, false>(x, few, c.st);
       if (e) return e;
+      parts = x.part0;
     }
-    DS4_LAUNCH(k_xent_join, dim3((unsigned)((rows + 31) / 32)), dim3(1024), 0, c.st, (const float2*)(w + p.part),
-               (int)((c.V + per - 1) / per), rows, c.target + r0, (int)c.V, (const float*)(w + p.zt), c.loss + r0,
-               c.lse + r0);
+#define DS4_JOIN(R)                                                                                                 \
+  DS4_LAUNCH(k_xent_join<R>, dim3((unsigned)((rows + R - 1) / R)), dim3(1024), 0, c.st, (const float2*)(w + p.part), \
+             parts, rows, c.target + r0, (int)c.V, (const float*)(w + p.zt), c.loss + r0, c.lse + r0)
+    if (rows <= 256 && parts > 64) DS4_JOIN(4);
+    else DS4_JOIN(32);
+#undef DS4_JOIN
   }
   return hipGetLastError();
 }
@@ -542,16 +629,16 @@ static hipError_t xent_backward(const XentCall& c) {
   DS4_LAUNCH(k_xent_live, dim3(1), dim3(1024), 0, c.st, c.target, (int)c.T, (int)c.V, c.scale, c.lse_in, c.dloss, n, live,
              (int32_t*)(w + p.y), (float*)(w + p.lse), (float*)(w + p.g));
   DS4_LAUNCH((k_xent_rows<PARTS == 1>), dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, c.h, (const int32_t*)n,
-             (const int32_t*)live, c.T, c.d, w + p.hc, p.hp, c.T * p.hp, c.dh);
+             (const int32_t*)live, c.T, c.d, w + p.hc, c.T * pitch, c.dh);
   for (int i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
     const uint8_t* src = (const uint8_t*)c.w + v0 * pitch * (PARTS == 3 ? 2 : 1);
     XOperand wop = {src, 0, pitch};
     if (PARTS == 3) {
-      xent_copy(src, words, c.d, w + p.wp, pitch, p.piece * pitch, c.st);
+      xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
       wop = {w + p.wp, p.piece * pitch, pitch};
     }
-    const XOperand hop = {w + p.hc, c.T * p.hp, p.hp}, dsop = {w + p.ds, c.T * p.dsp, p.dsp};
+    const XOperand hop = {w + p.hc, c.T * pitch, pitch}, dsop = {w + p.ds, 2 * c.T * p.piece, 2 * p.piece};
     XArgs x{};
     x.a = wop;
     x.b = hop;
@@ -571,7 +658,7 @@ static hipError_t xent_backward(const XentCall& c) {
     x.out_pitch = dsop.pitch;
     x.out_plane = dsop.plane;
     // the last tile's words past the end are written too: as zeros
-    if ((e = xent_gemm<XE_DS, PARTS, false>(x, c.st))) return e;
+    if ((e = xent_gemm<XE_DS, PARTS, false>(x, false, c.st))) return e;
     if (c.dh) {
       XArgs u{};
       u.a = wop;
@@ -585,7 +672,7 @@ static hipError_t xent_backward(const XentCall& c) {
       u.out_pitch = 4 * (int64_t)c.d;
       u.out_plane = 4 * c.T * c.d;
       u.add = i > 0;
-      if ((e = xent_gemm<XE_SLAB, PARTS, false>(u, c.st))) return e;
+      if ((e = xent_gemm<XE_SLAB, PARTS, false>(u, false, c.st))) return e;
     }
     if (c.dw) {
       XArgs u{};
@@ -599,7 +686,7 @@ static hipError_t xent_backward(const XentCall& c) {
       u.splits = 1;
       u.out = (uint8_t*)c.dw + v0 * c.d * (BF ? 2 : 4);
       u.out_pitch = c.d * (int64_t)(BF ? 2 : 4);
-      if ((e = xent_gemm<XE_ROWS, PARTS, BF>(u, c.st))) return e;
+      if ((e = xent_gemm<XE_ROWS, PARTS, BF>(u, false, c.st))) return e;
     }
   }
   if (c.dh)

@@ -14,8 +14,8 @@
 // LDS: 16-byte pieces, swizzled on their way in by choosing which piece a
 // lane copies.  By rows piece p of row r lies at p ^ (r / 2 & 7), so that the
 // 16 rows that a quarter of a wave reads lie in different banks; by columns
-// piece p of row k lies at p ^ 4 (k & 3), since half a wave reads four
-// neighbouring pieces of four rows.
+// piece p of row k lies at p ^ 4 (k & 3) (as far as its row has pieces), since
+// half a wave reads four neighbouring pieces of four rows.
 #pragma once
 
 #include "../ring.h"
@@ -58,7 +58,6 @@ struct XOperand {
 // One operand's side of a tile of B indices, from index i0 on.
 template <int B, bool COL>
 struct XSide {
-  static_assert(!COL || B >= 128, "sixteen pieces of a row, at least");
   const uint8_t* base;
   int64_t plane, pitch;
   uint32_t records;  // by rows: bytes that the tile has; by columns: what a row's end leaves out
@@ -76,7 +75,7 @@ struct XSide {
       base = o.p + i0 * 2;
       records = (uint32_t)i0 * 2;
       const int k = tid / P, p = tid % P;
-      vo = (uint32_t)(k * pitch) + (p ^ (4 * (k & 3))) * 16;
+      vo = (uint32_t)(k * pitch) + (p ^ (4 * (k & 3) & (P - 1))) * 16;
     }
   }
   static constexpr int kStep = COL ? 2048 / B : 32;  // rows from one copy to the next
@@ -106,13 +105,13 @@ struct XSide {
     } else {
       // Of a quarter's 16 lanes, four hold 16 neighbouring indices of one k,
       // four k in all; the read hands lane i index i of the four.
-      constexpr int RB = B * 2;
+      constexpr int RB = B * 2, P = B / 8;
       const int i = lane & 15, s = (lane >> 4) & 1, h = lane >> 5;
       u32x4_t v;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int k = 4 * r + (i >> 2);  // its last three bits
-        const int piece = (first / 8 + 4 * f + 2 * s + ((i & 3) >> 1)) ^ (4 * (k & 3));
+        const int piece = (first / 8 + 4 * f + 2 * s + ((i & 3) >> 1)) ^ (4 * (k & 3) & (P - 1));
         const u32x2_t x = read_turned((lds_s16x4_t*)(at + (16 * j + 8 * h + k) * RB + piece * 16 + 8 * (i & 1)));
         v[2 * r] = x.x;
         v[2 * r + 1] = x.y;

@@ -73,8 +73,8 @@ class AdamWDesc(ctypes.Structure):
     """Mirror of ds4moe_adamw."""
     _fields_ = [
         ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
-        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
-        ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
+        ("n_params", ctypes.c_int32), ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p), ("run", ctypes.c_int64), ("blocks", ctypes.c_int64),
     ]
 
 
@@ -120,9 +120,10 @@ def lib() -> ctypes.CDLL:
         L.ds4moe_norm_workspace_bytes.argtypes = [NP, I64]
         L.ds4moe_group_workspace_bytes.restype = SZ
         L.ds4moe_group_workspace_bytes.argtypes = [I64, N32, N32]
-        AP, PP, F32 = ctypes.POINTER(AdamWDesc), ctypes.POINTER(ParamDesc), ctypes.c_float
-        for name, args in {"balance": [I64, N32, N32], "xent": [I32, I64, I64, N32, I32], "adamw": [PP, N32]}.items():
-            fn = getattr(L, f"ds4moe_{name}_workspace_bytes")
+        AP, F32 = ctypes.POINTER(AdamWDesc), ctypes.c_float
+        for name, args in {"balance_workspace": [I64, N32, N32], "xent_workspace": [I32, I64, I64, N32, I32],
+                           "adamw_workspace": [AP], "adamw_table": [P, N32]}.items():
+            fn = getattr(L, f"ds4moe_{name}_bytes")
             fn.restype = SZ
             fn.argtypes = args
         for name, args in {
@@ -142,8 +143,9 @@ def lib() -> ctypes.CDLL:
             "balance_grad": [P, I32, I64, N32, P, N32, P, N32, P, P, P, P, P, P],
             "xent": [P, P, I32, I64, I64, N32, F32, P, P, P, P, SZ, P],
             "xent_grad": [P, P, I32, I64, I64, N32, F32, P, P, P, P, P, P, SZ, P],
-            "adamw_step": [AP, PP, N32, I64, P, P],
-            "adamw_norm": [AP, PP, N32, F32, P, P, SZ, P],
+            "adamw_table": [AP, P, N32, P, SZ],
+            "adamw_step": [AP, P, I64, P, P],
+            "adamw_norm": [AP, P, F32, P, P, SZ, P],
         }.items():
             fn = getattr(L, "ds4moe_" + name)
             fn.restype = I32
@@ -170,7 +172,8 @@ EXPORTS = ["ds4moe_packed_bytes", "ds4moe_quantize", "ds4moe_dequantize", "ds4mo
            "ds4moe_combine", "ds4moe_combine_grad", "ds4moe_mx_quantize", "ds4moe_mx_dequantize",
            "ds4moe_mx_product", "ds4moe_mx_product_grad", "ds4moe_balance_workspace_bytes", "ds4moe_balance",
            "ds4moe_balance_grad", "ds4moe_xent_workspace_bytes", "ds4moe_xent", "ds4moe_xent_grad",
-           "ds4moe_adamw_workspace_bytes", "ds4moe_adamw_step", "ds4moe_adamw_norm"]
+           "ds4moe_adamw_table_bytes", "ds4moe_adamw_table", "ds4moe_adamw_workspace_bytes", "ds4moe_adamw_step",
+           "ds4moe_adamw_norm"]
 
 
 def strerror(status: int) -> str:
@@ -484,93 +487,92 @@ def xent_grad(h, w, dtype, T, vocab, d, scale, target, lse, dloss, dh, dw, ws, w
 
 
 class AdamW:
-    """Tensors that AdamW updates (lists of equal length, CUDA tensors on one
-    GPU) plus the ds4moe_adamw descriptor and its ds4moe_param table.
+    """Tensors that AdamW updates (lists of equal length, on the current GPU) plus
+    the ds4moe_adamw descriptor and its table on the GPU.
 
     params, grads: float32 or bfloat16, one type each; master: float32, or None
     (for all, or in a tensor's place); m, v: float32, or torch.float8_e4m3fn (or
     uint8) codes with m_scale and v_scale, float32 with one value for each 256.
     weight_decay: one value, or one a tensor.  lr_dev float32 [1] and step_dev
-    int32 [1] on the GPU take lr's and the step's place (for captured graphs).
-    A step that gets its gradients in other tensors calls set_grads first."""
+    int32 [1] on the GPU take lr's and the step's place (for captured graphs);
+    desc.lr may be set between steps.  The table holds addresses: gradients stay
+    in their tensors from step to step, or set_grads makes a new one."""
 
     _TYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+    _CODES = (torch.float8_e4m3fn, torch.uint8)
 
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None, lr=1e-3, beta1=0.9, beta2=0.999,
                  eps=1e-8, weight_decay=0.0, lr_dev=None, step_dev=None):
-        self.n = len(params)
-        self.gpu = None
         fp8 = m_scale is not None or v_scale is not None
-        none = [None] * self.n
-        decay = [weight_decay] * self.n if isinstance(weight_decay, (int, float)) else list(weight_decay)
-        sizes = [p.numel() for p in params]
-        blocks = [(n + 255) // 256 for n in sizes]
-        state = (torch.float8_e4m3fn, torch.uint8) if fp8 else (torch.float32,)
-        f32 = (torch.float32,)
-        self.sizes = sizes
-        self.tensors = dict(
-            param=self._take("params", params, sizes, tuple(self._TYPES)),
-            grad=self._take("grads", grads, sizes, tuple(self._TYPES)),
-            master=self._take("master", none if master is None else master, sizes, f32, optional=True),
-            m=self._take("m", m, sizes, state), v=self._take("v", v, sizes, state),
-            m_scale=self._take("m_scale", m_scale, blocks, f32) if fp8 else none,
-            v_scale=self._take("v_scale", v_scale, blocks, f32) if fp8 else none)
-        if len(decay) != self.n:
-            raise ValueError("weight_decay: expected one value, or one a tensor")
-        for name, t, dtype in (("lr_dev", lr_dev, torch.float32), ("step_dev", step_dev, torch.int32)):
-            if t is not None:
-                self._take(name, [t], [1], (dtype,))
+        self.sizes = [p.numel() for p in params]
+        self.tensors = dict(param=params, grad=grads, master=master, m=m, v=v, m_scale=m_scale, v_scale=v_scale)
         self.devices = (lr_dev, step_dev)
-        one = lambda ts: self._TYPES[ts[0].dtype] if ts else DT_F32  # noqa: E731
-        self.desc = AdamWDesc(one(params), one(grads), STATE_FP8 if fp8 else STATE_F32, lr, beta1, beta2, eps, _ptr(lr_dev),
-                              _ptr(step_dev))
-        self.table = (ParamDesc * max(self.n, 1))()
-        for i in range(self.n):
-            q = self.table[i]
-            for name, ts in self.tensors.items():
-                setattr(q, name, _ptr(ts[i]))
-            q.n, q.weight_decay = sizes[i], decay[i]
+        self.weight_decay = weight_decay
+        self.gpu = _current_gpu()
+        one = lambda name, ts: self._type(name, ts[0]) if ts else DT_F32  # noqa: E731
+        lr_at, step_at = self._check([(lr_dev, 1, DT_F32), (step_dev, 1, _I32)])
+        self.desc = AdamWDesc(one("params", params), one("grads", grads), STATE_FP8 if fp8 else STATE_F32, 0, lr, beta1,
+                              beta2, eps, lr_at, step_at, 0, 0)
+        self.table = None
+        self._make_table()
 
-    def _take(self, name, tensors, sizes, types, optional=False):
-        """The tensors as a list, if they are what a call takes."""
-        if tensors is None or len(tensors) != len(sizes):
-            raise ValueError(f"{name}: expected {len(sizes)} tensors")
-        tensors = list(tensors)
-        for t, n in zip(tensors, sizes):
-            if optional and t is None:
+    def _type(self, name, t):
+        if t.dtype not in self._TYPES:
+            raise ValueError(f"{name}: a tensor of dtype {t.dtype}")
+        return self._TYPES[t.dtype]
+
+    def _check(self, args):
+        return (_addresses or _load_addresses())("AdamW", self.gpu, tuple(args))
+
+    def _make_table(self):
+        import numpy as np
+        n, desc = len(self.sizes), self.desc
+        fp8 = desc.state == STATE_FP8
+        rows = np.zeros(n, dtype=[(f[0], "<i8" if f[0] == "n" else "<f8" if f[0] == "weight_decay" else "<u8")
+                                  for f in ParamDesc._fields_])
+        blocks = [(k + 255) // 256 for k in self.sizes]
+        held = dict(param=desc.param_dtype, grad=desc.grad_dtype)
+        for name, ts in self.tensors.items():
+            scale = name.endswith("_scale")
+            if ts is None and (name == "master" or scale and not fp8):
                 continue
-            if t.dtype not in types or t.dtype != tensors[0].dtype and not optional:
-                raise ValueError(f"{name}: a tensor of dtype {t.dtype}")
-            if t.numel() != n or not t.is_contiguous():
-                raise ValueError(f"{name}: expected {n} contiguous values, got {tuple(t.shape)}")
-            if not t.is_cuda or self.gpu not in (None, t.get_device()):
-                raise ValueError(f"{name}: expected all tensors on one GPU")
-            self.gpu = t.get_device()
-        return tensors
+            if ts is None or len(ts) != n:
+                raise ValueError(f"{name}: expected {n} tensors")
+            codes = fp8 and name in ("m", "v")
+            if codes and any(t.dtype not in self._CODES for t in ts):
+                raise ValueError(f"{name}: codes are float8_e4m3fn or uint8")
+            what = _BYTES if codes else held.get(name, DT_F32)
+            at = self._check([(t, k, what) for t, k in zip(ts, blocks if scale else self.sizes)])
+            rows[name] = [0 if a is None else a for a in at]
+        rows["n"] = self.sizes
+        rows["weight_decay"] = self.weight_decay
+        size = int(lib().ds4moe_adamw_table_bytes(rows.ctypes.data, n))
+        table = torch.empty(size, dtype=torch.uint8)
+        _check(lib().ds4moe_adamw_table(ctypes.byref(desc), rows.ctypes.data, n, _ptr(table), size), "ds4moe_adamw_table")
+        self.table = table.cuda() if self.gpu >= 0 else None
 
     def set_grads(self, grads) -> None:
-        self.tensors["grad"] = self._take("grads", grads, self.sizes, tuple(self._TYPES))
+        self.tensors["grad"] = grads
         if grads:
-            self.desc.grad_dtype = self._TYPES[grads[0].dtype]
-        for i, g in enumerate(self.tensors["grad"]):
-            self.table[i].grad = _ptr(g)
+            self.desc.grad_dtype = self._type("grads", grads[0])
+        self._make_table()
 
     def workspace_bytes(self) -> int:
-        return int(lib().ds4moe_adamw_workspace_bytes(self.table, self.n))
+        return int(lib().ds4moe_adamw_workspace_bytes(ctypes.byref(self.desc)))
 
 
 def _adamw_on_gpu(opt):
-    if opt.gpu is not None and opt.gpu != _current_gpu():
+    if opt.gpu != _current_gpu():
         raise ValueError("the optimizer's tensors are not on the current GPU")
     return opt.desc
 
 
 def adamw_step(opt: AdamW, step, grad_scale=None, stream=None) -> None:
-    _call("ds4moe_adamw_step", stream, _adamw_on_gpu(opt), opt.table, opt.n, step, (grad_scale, 1, DT_F32))
+    _call("ds4moe_adamw_step", stream, _adamw_on_gpu(opt), (opt.table, 1, _BYTES), step, (grad_scale, 1, DT_F32))
 
 
 def adamw_norm(opt: AdamW, max_norm, out, ws, ws_bytes, stream=None) -> None:
-    _call("ds4moe_adamw_norm", stream, _adamw_on_gpu(opt), opt.table, opt.n, max_norm, (out, 2, DT_F32),
+    _call("ds4moe_adamw_norm", stream, _adamw_on_gpu(opt), (opt.table, 1, _BYTES), max_norm, (out, 2, DT_F32),
           (ws, ws_bytes, _BYTES), ws_bytes)
 
 

@@ -544,40 +544,49 @@ int ds4moe_xent_grad(const void *h, const void *w, int dtype, int64_t T, int64_t
  * rounded to codes.  States start as zeros. */
 enum { DS4MOE_STATE_F32 = 0, DS4MOE_STATE_FP8 = 1 };
 
-/* One tensor.  Plain data: read during the call, not retained.  Pointers are
- * aligned as their type; 16 bytes (8 for codes) is faster. */
+/* One tensor.  Pointers are device pointers aligned as their type; 16 bytes (8
+ * for codes) is faster. */
 typedef struct {
   void *param;          /* [n] fp32 or bf16, updated */
   const void *grad;     /* [n] fp32 or bf16 */
   float *master;        /* [n] fp32: updated in param's place, which gets it rounded; or NULL */
   void *m, *v;          /* [n] states: fp32, or codes */
   float *m_scale, *v_scale; /* [(n + 255) / 256] with DS4MOE_STATE_FP8, else not read */
-  int64_t n;            /* 0 <= n <= 2^40 */
+  int64_t n;            /* >= 0; at most 2^40 in all tensors */
   double weight_decay;  /* finite */
 } ds4moe_param;
 
 typedef struct {
-  int32_t param_dtype, grad_dtype; /* DS4MOE_DT_*, of all tensors of a call */
+  int32_t param_dtype, grad_dtype; /* DS4MOE_DT_*, of all tensors */
   int32_t state;                   /* DS4MOE_STATE_* */
+  int32_t n_params;                /* this and the last two are ds4moe_adamw_table's to fill in */
   double lr, beta1, beta2, eps;    /* finite; 0 <= beta < 1; eps > 0 as an fp32 */
   const float *lr_dev;             /* device: the learning rate in lr's place, or NULL */
   const int32_t *step_dev;         /* device: the step in the argument's place, or NULL */
+  int64_t run, blocks;
 } ds4moe_adamw;
 
-/* One step over params[0 .. n_params) (host array; 0 <= n_params <= 2^20, no two
- * overlap).  step counts from 1 (below 1 on the device: 1).  grad_scale: device,
+/* The tensors as a table, laid out once: ds4moe_adamw_table checks them (no two
+ * may overlap; 0 <= n_params <= 2^20) and writes the table to host memory
+ * (8-byte aligned, ds4moe_adamw_table_bytes), which the program copies to the
+ * device, 16-byte aligned, for the calls below.  It holds the tensors'
+ * addresses: where one moves, a new table is made.  The other fields of A may
+ * change between steps. */
+size_t ds4moe_adamw_table_bytes(const ds4moe_param *params, int32_t n_params);
+int ds4moe_adamw_table(ds4moe_adamw *A, const ds4moe_param *params, int32_t n_params, void *table, size_t table_bytes);
+
+/* One step.  step counts from 1 (below 1 on the device: 1).  grad_scale: device,
  * s, or NULL for 1; where it is not finite nothing changes, which is how
  * a step without finite gradients is left out. */
-int ds4moe_adamw_step(const ds4moe_adamw *A, const ds4moe_param *params, int32_t n_params, int64_t step,
-                      const float *grad_scale, void *stream);
+int ds4moe_adamw_step(const ds4moe_adamw *A, const void *table, int64_t step, const float *grad_scale, void *stream);
 
 /* out[0] = sqrt(sum of the squares of all gradients), summed in fp64 in a fixed
  * order; out[1] = min(1, max_norm / out[0]), NaN where out[0] is not finite:
- * the grad_scale of a clipped step.  fp32 [2], device.  Of params only grad and
- * n are read.  max_norm > 0.  ws, 256-byte aligned, need not be cleared. */
-size_t ds4moe_adamw_workspace_bytes(const ds4moe_param *params, int32_t n_params);
-int ds4moe_adamw_norm(const ds4moe_adamw *A, const ds4moe_param *params, int32_t n_params, float max_norm, float *out,
-                      void *ws, size_t ws_bytes, void *stream);
+ * the grad_scale of a clipped step.  fp32 [2], device.  max_norm > 0.  ws,
+ * 256-byte aligned, need not be cleared. */
+size_t ds4moe_adamw_workspace_bytes(const ds4moe_adamw *A);
+int ds4moe_adamw_norm(const ds4moe_adamw *A, const void *table, float max_norm, float *out, void *ws, size_t ws_bytes,
+                      void *stream);
 
 /* Opt-in per-kernel timing (profiling aid).  While enabled, every kernel
  * the library launches is bracketed by two HIP events on its stream, which

@@ -93,62 +93,101 @@ def param(**kw):
 
 
 def opts(**kw):
-    v = dict(param_dtype=0, grad_dtype=0, state=0, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, lr_dev=None, step_dev=None)
+    v = dict(param_dtype=0, grad_dtype=0, state=0, n_params=1, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, lr_dev=None,
+             step_dev=None, run=4096, blocks=1)
     v.update(kw)
     return D.AdamWDesc(*(v[f[0]] for f in D.AdamWDesc._fields_))
 
 
-def step(o=None, p=None, n=1, at=1, scale=None):
+def table(o=None, p=None, n=1, to=True, nb=1 << 16):
     o = opts() if o is None else o
-    table = (D.ParamDesc * 2)(param() if p is None else p, param(n=0, param=None, grad=None, m=None, v=None))
-    return status("adamw_step", ctypes.byref(o) if o else None, table, n, at, scale, None)
+    ps = (D.ParamDesc * 2)(param() if p is None else p, param(n=0, param=None, grad=None, m=None, v=None))
+    buf = ctypes.create_string_buffer(1 << 16)
+    return status("adamw_table", ctypes.byref(o) if o else None, ctypes.addressof(ps), n, ctypes.addressof(buf) if to else None,
+                  nb)
 
 
-def norm(o=None, p=None, n=1, most=1.0, out=A, ws=A, nb=BIG):
-    table = (D.ParamDesc * 2)(param() if p is None else p, param(n=0))
-    return status("adamw_norm", ctypes.byref(opts() if o is None else o), table, n, most, out, ws, nb, None)
+def step(o=None, t=A, at=1, scale=None):
+    return status("adamw_step", ctypes.byref(opts() if o is None else o), t, at, scale, None)
 
 
-def test_adamw_errors():
+def norm(o=None, t=A, most=1.0, out=A, ws=A, nb=BIG):
+    return status("adamw_norm", ctypes.byref(opts() if o is None else o), t, most, out, ws, nb, None)
+
+
+def test_adamw_option_errors():
     for kw in (dict(param_dtype=2), dict(grad_dtype=-1), dict(state=2), dict(lr=NAN), dict(lr=INF), dict(beta1=1.0),
                dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=NAN), dict(eps=0.0), dict(eps=NAN), dict(eps=INF),
                dict(eps=1e-60)):
-        assert step(o=opts(**kw)) == D.EINVAL, kw
-    assert step(o=opts(lr_dev=A + 2)) == D.EALIGN and step(o=opts(step_dev=A + 2)) == D.EALIGN
-    assert step(at=0) == D.EINVAL and step(at=-3) == D.EINVAL and step(scale=A + 2) == D.EALIGN
-    assert step(n=-1) == D.ESHAPE
+        assert table(o=opts(**kw)) == step(o=opts(**kw)) == norm(o=opts(**kw)) == D.EINVAL, kw
+    for kw in (dict(lr_dev=A + 2), dict(step_dev=A + 2)):
+        assert table(o=opts(**kw)) == step(o=opts(**kw)) == D.EALIGN
+    for name, args in (("table", (0, 0, A, BIG)), ("step", (A, 1, None, None)), ("norm", (A, 1.0, A, A, BIG, None))):
+        assert status("adamw_" + name, None, *args) == D.EINVAL
+
+
+def test_adamw_table_errors():
     for kw in (dict(param=None), dict(grad=None), dict(m=None), dict(v=None), dict(weight_decay=NAN)):
-        assert step(p=param(**kw)) == D.EINVAL, kw
+        assert table(p=param(**kw)) == D.EINVAL, kw
     for kw in (dict(n=-1), dict(n=(1 << 40) + 1)):
-        assert step(p=param(**kw)) == D.ESHAPE and norm(p=param(**kw)) == D.ESHAPE
+        assert table(p=param(**kw)) == D.ESHAPE
+        ps = (D.ParamDesc * 1)(param(**kw))
+        assert D.lib().ds4moe_adamw_table_bytes(ctypes.addressof(ps), 1) == 0
     for kw in (dict(param=A + 2), dict(grad=A + 2), dict(m=A + 2), dict(v=A + 1), dict(master=A + 2)):
-        assert step(p=param(**kw)) == D.EALIGN, kw
-    assert step(o=opts(param_dtype=1), p=param(param=A + 1)) == D.EALIGN
+        assert table(p=param(**kw)) == D.EALIGN, kw
+    assert table(o=opts(param_dtype=1), p=param(param=A + 1)) == D.EALIGN
     fp8 = opts(state=D.STATE_FP8)
     for kw in (dict(m_scale=None), dict(v_scale=None)):
-        assert step(o=fp8, p=param(**kw)) == D.EINVAL
-    assert step(o=fp8, p=param(m_scale=A + 2, m=A + 1)) == D.EALIGN
-    assert status("adamw_step", None, None, 0, 1, None, None) == D.EINVAL
-    assert status("adamw_step", ctypes.byref(opts()), None, 1, 1, None, None) == D.EINVAL
-    # nothing to do launches nothing
-    assert status("adamw_step", ctypes.byref(opts()), None, 0, 1, None, None) == D.OK
+        assert table(o=fp8, p=param(**kw)) == D.EINVAL
+        assert table(p=param(**kw)) == D.OK
+    assert table(o=fp8, p=param(m_scale=A + 2, m=A + 1)) == D.EALIGN and table(o=fp8, p=param(m=A + 1)) == D.OK
+    assert table(n=-1) == D.ESHAPE and table(n=0) == D.OK and table(n=2) == D.OK
+    assert table(to=False) == D.EINVAL and table(nb=8) == D.EWORKSPACE
+    assert D.lib().ds4moe_adamw_table_bytes(None, 1) == 0
 
 
-def test_norm_errors():
-    for kw in (dict(most=0.0), dict(most=-1.0), dict(most=NAN), dict(out=None), dict(ws=None), dict(p=param(grad=None)),
-               dict(o=opts(grad_dtype=3))):
+def test_adamw_table_covers_every_value_once():
+    sizes = [1, 4096, 4097, 0, 100000]
+    ps = (D.ParamDesc * 5)(*(param(n=n) for n in sizes))
+    o = opts()
+    nb = D.lib().ds4moe_adamw_table_bytes(ctypes.addressof(ps), 5)
+    buf = ctypes.create_string_buffer(nb)
+    assert status("adamw_table", ctypes.byref(o), ctypes.addressof(ps), 5, ctypes.addressof(buf), nb) == D.OK
+    assert o.n_params == 5 and o.run == 4096 and o.blocks == sum(-(-n // 4096) for n in sizes)
+    assert buf.raw[:72 * 5] == bytes(ps)
+    at = (72 * 5 + 15) // 16 * 16
+    pairs = [tuple(int.from_bytes(buf.raw[at + 8 * i + 4 * j:at + 8 * i + 4 * j + 4], "little") for j in (0, 1))
+             for i in range(o.blocks)]
+    assert pairs == [(i, r) for i, n in enumerate(sizes) for r in range(-(-n // 4096))]
+    # few blocks however long the tensors are
+    ps = (D.ParamDesc * 3)(*(param(n=n) for n in (1 << 38, 5, 1 << 30)))
+    nb = D.lib().ds4moe_adamw_table_bytes(ctypes.addressof(ps), 3)
+    buf = ctypes.create_string_buffer(nb)
+    assert status("adamw_table", ctypes.byref(o), ctypes.addressof(ps), 3, ctypes.addressof(buf), nb) == D.OK
+    assert o.run % 4096 == 0 and o.blocks <= (1 << 17) + 3 and o.blocks * o.run >= (1 << 38) + (1 << 30)
+
+
+def test_adamw_step_and_norm_errors():
+    for call in (step, norm):
+        for kw in (dict(n_params=-1), dict(n_params=(1 << 20) + 1), dict(blocks=-1), dict(blocks=1 << 30), dict(run=0),
+                   dict(run=300)):
+            assert call(o=opts(**kw)) == D.ESHAPE, kw
+        assert call(t=None) == D.EINVAL and call(t=A + 8) == D.EALIGN
+    assert step(at=0) == D.EINVAL and step(at=-3) == D.EINVAL and step(scale=A + 2) == D.EALIGN
+    for kw in (dict(most=0.0), dict(most=-1.0), dict(most=NAN), dict(out=None), dict(ws=None)):
         assert norm(**kw) == D.EINVAL, kw
-    for kw in (dict(out=A + 2), dict(ws=A + 64), dict(p=param(grad=A + 2))):
-        assert norm(**kw) == D.EALIGN, kw
-    need = D.lib().ds4moe_adamw_workspace_bytes((D.ParamDesc * 1)(param(n=1 << 30)), 1)
-    assert need > 0 and norm(p=param(n=1 << 30), nb=need - 1) == D.EWORKSPACE
-    assert D.lib().ds4moe_adamw_workspace_bytes(None, 1) == 0
-    assert D.lib().ds4moe_adamw_workspace_bytes((D.ParamDesc * 1)(param(n=-1)), 1) == 0
+    assert norm(out=A + 2) == D.EALIGN and norm(ws=A + 64) == D.EALIGN
+    o = opts(blocks=100000)
+    need = D.lib().ds4moe_adamw_workspace_bytes(ctypes.byref(o))
+    assert need > 0 and norm(o=o, nb=need - 1) == D.EWORKSPACE
+    assert D.lib().ds4moe_adamw_workspace_bytes(None) == 0
+    # nothing to do launches nothing
+    assert step(o=opts(n_params=0, blocks=0)) == D.OK
 
 
 def test_struct_sizes():
     """The structures as the header lays them out on a 64-bit host."""
-    assert ctypes.sizeof(D.ParamDesc) == 72 and ctypes.sizeof(D.AdamWDesc) == 64
+    assert ctypes.sizeof(D.ParamDesc) == 72 and ctypes.sizeof(D.AdamWDesc) == 80
 
 
 # ---------------------------------------------------------------- binding
@@ -182,17 +221,21 @@ def test_refused_tensors(name, dt, code):
                 f(*given)
 
 
-def test_optimizer_refuses_host_tensors_and_lists_that_do_not_match():
-    t = [torch.zeros(4)]
-    with pytest.raises(ValueError, match="one GPU"):
+def test_optimizer_refuses_what_a_step_cannot_take():
+    """Lists that do not match, types, and tensors that are not on the GPU."""
+    t = [torch.zeros(300)]
+    with pytest.raises(ValueError, match="current GPU"):
         D.AdamW(t, t, t, t)
-    with pytest.raises(ValueError, match="expected 0 tensors"):
+    with pytest.raises(ValueError, match="grad: expected 0 tensors"):
         D.AdamW([], t, [], [])
-    with pytest.raises(ValueError, match="dtype"):
-        D.AdamW([torch.zeros(4, dtype=torch.float16)], t, t, t)
-    with pytest.raises(ValueError, match="contiguous"):
-        D.AdamW([torch.zeros(8)[::2]], t, t, t)
-    assert D.AdamW([], [], [], []).n == 0
+    for bad in (torch.float16, torch.int32):
+        with pytest.raises(ValueError, match="dtype"):
+            D.AdamW([t[0].to(bad)], t, t, t)
+    with pytest.raises(ValueError, match="v_scale: expected 0 tensors"):
+        D.AdamW([], [], [], [], m_scale=[])
+    with pytest.raises(ValueError, match="dtype|current GPU"):
+        D.AdamW([], [], [], [], lr_dev=torch.zeros(1, dtype=torch.float64))
+    assert D.AdamW([], [], [], []).desc.blocks == 0
 
 
 def test_optimizer_of_another_device_is_refused():
