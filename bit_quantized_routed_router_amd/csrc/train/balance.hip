@@ -23,32 +23,55 @@ constexpr int kBalThreads = 256;
 // Lanes of a row: a quarter of its experts, from 4 to 64.
 static int bal_lanes(int E) { return E <= 16 ? 4 : E <= 64 ? 16 : 64; }
 
-// Tokens of a block.  At least 32, so that the join has few runs to add; no
-// more than 1024 blocks, so that it need not add many.
-static int bal_run(int64_t T) { return (int)std::max<int64_t>(32, (T + 1023) / 1024); }
+// Tokens of a block.  At least 16, so that the join has few runs to add; no
+// more than 2048 blocks, so that it need not add many.
+static int bal_run(int64_t T) { return (int)std::max<int64_t>(16, (T + 2047) / 2048); }
 // Up to this many tokens a sequence is one run and needs no join.
 static bool bal_one(int64_t T) { return T <= 32; }
 
-struct BalRow {  // of the ws: sums of probabilities [E], counts [E], tokens
-  static __host__ __device__ inline int64_t words(int E) { return 2 * (int64_t)E + 4; }
+struct BalRow {  // of the ws: (sum of probabilities, count) [E, to an even number], tokens; 16-byte aligned
+  static __host__ __device__ inline int64_t pairs(int E) { return ((int64_t)E + 1) / 2 * 2 + 2; }
 };
 size_t balance_ws_bytes(int64_t T, int E, int seqs) {
   if (bal_one(T)) return 256;
   const int run = bal_run(T);
-  return (size_t)(T / run + seqs + 1) * BalRow::words(E) * 4;
+  return (size_t)(T / run + seqs + 1) * BalRow::pairs(E) * 8;
 }
 
+// Largest value and sum over the G lanes of a row, in every lane: quads, rows
+// of 16 by rotation, the wave's four rows through scalar registers.
+template <int CTRL>
+__device__ inline float dpp_move(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
 template <int G>
 __device__ inline float group_max(float v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+  v = fmaxf(v, dpp_move<0xB1>(v));
+  v = fmaxf(v, dpp_move<0x4E>(v));
+  if constexpr (G >= 16) {
+    v = fmaxf(v, dpp_move<0x124>(v));
+    v = fmaxf(v, dpp_move<0x128>(v));
+  }
+  if constexpr (G == 64)
+    v = fmaxf(fmaxf(lane_float(v, 0), lane_float(v, 16)), fmaxf(lane_float(v, 32), lane_float(v, 48)));
   return v;
 }
 template <int G>
 __device__ inline float group_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o);
+  if constexpr (G == 64) return wave_sum(v);
+  v += dpp_move<0xB1>(v);
+  v += dpp_move<0x4E>(v);
+  if constexpr (G >= 16) {
+    v += dpp_move<0x124>(v);
+    v += dpp_move<0x128>(v);
+  }
   return v;
+}
+// Lane J's value of the row, in all of its lanes (16 or 64 of them).
+template <int G, int J>
+__device__ inline int group_lane(int v) {
+  if constexpr (G == 64) return __builtin_amdgcn_readlane(v, J);
+  return __builtin_amdgcn_update_dpp(0, v, 0x150 + J, 0xF, 0xF, false);  // row_newbcast:J
 }
 
 // The lane's logits of row t: elements 4 (g + G v) .. + 3; -inf past the last.
@@ -116,7 +139,7 @@ template <int G, int NV, bool BF, bool ONE>
 __global__ __launch_bounds__(kBalThreads) void k_balance(const void* __restrict__ z, int64_t T, int E, int k,
                                                          const int32_t* __restrict__ idx,
                                                          const int32_t* __restrict__ off, int seqs, int run, bool vec,
-                                                         float* __restrict__ ws, int32_t* __restrict__ counts,
+                                                         float2* __restrict__ ws, int32_t* __restrict__ counts,
                                                          int32_t* __restrict__ tokens, float* __restrict__ loss) {
   constexpr int ROWS = 64 / G, W = kBalThreads / 64, EM = 4 * G * NV;
   __shared__ float psum[W][EM];
@@ -209,70 +232,93 @@ __global__ __launch_bounds__(kBalThreads) void k_balance(const void* __restrict_
     }
   } else {
     // run i of sequence b has row lo / run + b: ascending, and no two alike
-    float* row = ws + (int64_t)(rt.lo / run + rt.e) * BalRow::words(E);
-    for (int e = tid; e < E; e += kBalThreads) {
-      row[e] = (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]);
-      ((int32_t*)row)[E + e] = cnt[e];
-    }
-    if (tid == 0) ((int32_t*)row)[2 * E] = n;
+    float2* row = ws + (int64_t)(rt.lo / run + rt.e) * BalRow::pairs(E);
+    for (int e = tid; e < E; e += kBalThreads)
+      row[e] = float2{(psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]), __builtin_bit_cast(float, cnt[e])};
+    if (tid == 0) row[BalRow::pairs(E) - 1].x = __builtin_bit_cast(float, n);
   }
 }
 
-// A block joins the runs of a sequence: EB experts (a power of two) by
-// 1024 / EB shares of the runs.
-__global__ __launch_bounds__(1024) void k_balance_join(const float* __restrict__ ws, int T, int E, int eb, int k,
+// A block joins the runs of a sequence: two experts to a thread, cb threads (a
+// power of two) to a run, 1024 / cb runs at a time.
+__global__ __launch_bounds__(1024) void k_balance_join(const float2* __restrict__ ws, int T, int E, int cb, int k,
                                                        const int32_t* __restrict__ off, int run,
                                                        int32_t* __restrict__ counts, int32_t* __restrict__ tokens,
                                                        float* __restrict__ loss) {
-  __shared__ double sums[1024];
-  __shared__ int cnts[1024];
-  __shared__ int toks[1024];
+  __shared__ double sums[2][1024];
+  __shared__ int cnts[2][1024];
   __shared__ double lsum[16];
-  const int tid = threadIdx.x, b = blockIdx.x, e = tid & (eb - 1), share = tid / eb, shares = 1024 / eb;
+  __shared__ int ltok[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
+  const int col = tid & (cb - 1), share = tid / cb, shares = 1024 / cb;
   const int lo = off ? min(max(off[b], 0), T) : 0, hi = off ? min(max(off[b + 1], 0), T) : T;
   const int runs = hi > lo ? (hi - lo + run - 1) / run : 0;
-  const int64_t words = BalRow::words(E);
-  const float* row = ws + (int64_t)(lo / run + b) * words;
-  double p = 0.0;
-  int c = 0, n = 0;
-  if (e < E) {
-#pragma unroll 8
-    for (int i = share; i < runs; i += shares) {
-      p += row[i * words + e];
-      c += ((const int32_t*)row)[i * words + E + e];
+  const int64_t pairs = BalRow::pairs(E);
+  const float2* row = ws + (int64_t)(lo / run + b) * pairs;
+  double p0 = 0.0, p1 = 0.0;
+  int c0 = 0, c1 = 0, n = 0;
+  if (tid < runs) n = __builtin_bit_cast(int, row[tid * pairs + pairs - 1].x);
+  for (int i = tid + 1024; i < runs; i += 1024) n += __builtin_bit_cast(int, row[i * pairs + pairs - 1].x);
+  if (2 * col < E) {
+    constexpr int U = 8;
+    for (int i0 = share; i0 < runs; i0 += U * shares) {
+      float4_t v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {  // (a run's second may be past the last expert)
+        const int i = i0 + u * shares;
+        v[u] = float4_t{0.f, 0.f, 0.f, 0.f};
+        if (i < runs) v[u] = *(const float4_t*)(row + i * pairs + 2 * col);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float n0 = v[u].y, n1 = v[u].w;  // (a bit cast of an element would take the vector's first)
+        p0 += v[u].x;
+        c0 += __builtin_bit_cast(int, n0);
+        p1 += v[u].z;
+        c1 += __builtin_bit_cast(int, n1);
+      }
     }
   }
-  for (int i = tid; i < runs; i += 1024) n += ((const int32_t*)row)[i * words + 2 * E];
-  sums[tid] = p;
-  cnts[tid] = c;
-  toks[tid] = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
+  if (lane == 0) ltok[wave] = n;
+  sums[0][tid] = p0;
+  sums[1][tid] = p1;
+  cnts[0][tid] = c0;
+  cnts[1][tid] = c1;
   __syncthreads();
-  for (int o = 512; o >= eb; o >>= 1) {
+  for (int o = 512; o >= cb; o >>= 1) {
     if (tid < o) {
-      sums[tid] += sums[tid + o];
-      cnts[tid] += cnts[tid + o];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        sums[q][tid] += sums[q][tid + o];
+        cnts[q][tid] += cnts[q][tid + o];
+      }
     }
-    __syncthreads();
-  }
-  for (int o = 512; o >= 1; o >>= 1) {
-    if (tid < o) toks[tid] += toks[tid + o];
     __syncthreads();
   }
   double s = 0.0;
-  if (tid < E) {
-    counts[(int64_t)b * E + tid] = cnts[tid];
-    s = cnts[tid] * sums[tid];
+  if (tid < cb) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (2 * tid + q >= E) continue;
+      counts[(int64_t)b * E + 2 * tid + q] = cnts[q][tid];
+      s += cnts[q][tid] * sums[q][tid];
+    }
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
-  if ((tid & 63) == 0) lsum[tid >> 6] = s;
+  if (lane == 0) lsum[wave] = s;
   __syncthreads();
   if (tid != 0) return;
   s = 0.0;
-  for (int i = 0; i < 16; ++i) s += lsum[i];
-  const double m = toks[0];
-  tokens[b] = toks[0];
-  loss[b] = toks[0] ? (float)(s * E / (k * m * m)) : 0.f;
+  n = 0;
+  for (int i = 0; i < 16; ++i) {
+    s += lsum[i];
+    n += ltok[i];
+  }
+  tokens[b] = n;
+  loss[b] = n ? (float)(s * E / ((double)k * n * n)) : 0.f;
 }
 
 // ---------------------------------------------------------------- backward
@@ -373,21 +419,25 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* __rest
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[v][i] = live ? factor * r[u].z[v][i] * (c[v][i] - dot) : 0.f;
       if (dslots) {
-        for (int j = 0; j < k; ++j) {
-          int e;
-          float s;
-          if constexpr (G >= 16) {
-            e = __shfl(named[u], rg * G + j);
-            s = __shfl(slot[u], rg * G + j);
-          } else {
-            e = on ? idx[(int64_t)t * k + j] : -1;
-            s = on ? dslots[(int64_t)t * k + j] : 0.f;
-          }
-          // (an expert out of range is no lane's, or that of places past the last)
+        // (an expert out of range is no lane's, or that of places past the last)
+        auto add = [&](int e, float s) __attribute__((always_inline)) {
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[v][i] += e == 4 * (g + G * v) + i ? s : 0.f;
+        };
+        if constexpr (G >= 16) {
+          const int sb = __builtin_bit_cast(int, slot[u]);
+#define DS4_SLOT(J) \
+  if (J < k) add(group_lane<G, J>(named[u]), __builtin_bit_cast(float, group_lane<G, J>(sb)))
+          DS4_SLOT(0); DS4_SLOT(1); DS4_SLOT(2); DS4_SLOT(3); DS4_SLOT(4); DS4_SLOT(5); DS4_SLOT(6); DS4_SLOT(7);
+          if (k > 8) {
+            DS4_SLOT(8); DS4_SLOT(9); DS4_SLOT(10); DS4_SLOT(11); DS4_SLOT(12); DS4_SLOT(13); DS4_SLOT(14); DS4_SLOT(15);
+          }
+#undef DS4_SLOT
+        } else {
+          for (int j = 0; j < k; ++j)
+            add(on ? idx[(int64_t)t * k + j] : -1, on ? dslots[(int64_t)t * k + j] : 0.f);
         }
       }
 #pragma unroll
@@ -424,15 +474,15 @@ static hipError_t balance_fwd(const BalanceCall& c) {
   const int run = bal_run(c.T);
   if (bal_one(c.T)) {
     DS4_LAUNCH((k_balance<G, NV, BF, true>), dim3(c.seqs), dim3(kBalThreads), 0, c.st, c.z, c.T, c.E, c.k, c.idx, c.off,
-               c.seqs, run, bal_vec(c), (float*)nullptr, c.counts, c.tokens, c.loss);
+               c.seqs, run, bal_vec(c), (float2*)nullptr, c.counts, c.tokens, c.loss);
     return hipGetLastError();
   }
   const int64_t blocks = max_tiles(c.T, c.seqs, c.off != nullptr, run);
   DS4_LAUNCH((k_balance<G, NV, BF, false>), dim3((unsigned)blocks), dim3(kBalThreads), 0, c.st, c.z, c.T, c.E, c.k,
-             c.idx, c.off, c.seqs, run, bal_vec(c), (float*)c.ws, c.counts, c.tokens, c.loss);
-  int eb = 64;
-  while (eb < c.E) eb *= 2;
-  DS4_LAUNCH(k_balance_join, dim3(c.seqs), dim3(1024), 0, c.st, (const float*)c.ws, (int)c.T, c.E, eb, c.k, c.off, run,
+             c.idx, c.off, c.seqs, run, bal_vec(c), (float2*)c.ws, c.counts, c.tokens, c.loss);
+  int cb = 64;
+  while (2 * cb < c.E) cb *= 2;
+  DS4_LAUNCH(k_balance_join, dim3(c.seqs), dim3(1024), 0, c.st, (const float2*)c.ws, (int)c.T, c.E, cb, c.k, c.off, run,
              c.counts, c.tokens, c.loss);
   return hipGetLastError();
 }

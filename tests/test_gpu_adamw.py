@@ -259,3 +259,32 @@ def test_adamw_past_32_bits():
     for i, a in enumerate(places):
         assert float(p[a]) == -1.0 and abs(float(ms[a // 256]) - (i + 1) / 2 / 448) < 1e-7, a
     assert int((p != 0).sum()) == len(places) and int((vs != 0).sum()) == len(places)
+
+
+@pytest.mark.parametrize("scale", [None, 0.37])
+def test_adamw_codes_are_those_of_ieee_operations(scale):
+    """States in 8 bits bit for bit: products, sums, root and quotient each
+    rounded on the host as on the GPU, two steps in a row."""
+    n = 1 << 18
+    ts = make([n], "f32", "f32", True, seed=40)
+    t = ts[0]
+    for at in (5, 6):
+        o = step(ts, at=at, scale=scale)[0]
+        f = lambda x: torch.tensor(x, dtype=torch.float32)  # noqa: E731
+        d = t["g"] * f(1.0 if scale is None else scale)
+        m = t["m"].float() * t["ms"].repeat_interleave(256)
+        r = t["v"].float() * t["vs"].repeat_interleave(256)
+        m = f(HYPER["b1"]) * m + f(1 - HYPER["b1"]) * d
+        v = f(HYPER["b2"]) * (r * r) + f(1 - HYPER["b2"]) * (d * d)
+        # (a root in 64 bits, rounded, is the root rounded; the host's own in 32 bits is not)
+        for q, s, x, root in (("m", "ms", m, False), ("v", "vs", torch.sqrt(v.double()).float(), True)):
+            b = x.reshape(-1, 256)
+            want = b.abs().amax(1) * f(1 / 448)
+            assert torch.equal(o[s], want)
+            y = b / want[:, None]
+            if root:
+                y = torch.where(b > 0, y.clamp(min=2.0 ** -9), y)
+            codes = y.reshape(-1).to(FP8).view(torch.uint8)
+            assert torch.equal(o[q].view(torch.uint8), codes), (q, int((o[q].view(torch.uint8) != codes).sum()))
+            t[q], t[s] = o[q], o[s]
+        t["p"] = o["p"]
