@@ -27,7 +27,10 @@ namespace ds4 {
 // What grows with rows and words is bounded by taking words a piece at a time
 // (ds, and the planes of an fp32 w) and, in the forward pass, rows (the partial
 // sums).
-constexpr int64_t kXentPiece = 128 << 20;   // bytes that either aims at
+constexpr int64_t kXentPiece = 256 << 20;   // bytes that either aims at
+// fp32 operands of up to so many rows go through the fp32 instruction as they
+// are, of more as planes (times forward / forward and back, us):
+constexpr int64_t kXentF32Rows = 384;
 constexpr int kXentSlabs = 8;               // parts of the sum over words in dh, at most
 
 template <typename T>
@@ -37,36 +40,54 @@ static T round_up(T v, T m) {
 
 // Shapes of a product's tiles (a's by b's), and the words that a wave of one
 // has, which a partial sum covers.
-enum { kFew, kSmall, kMid, kBig };  // 128 x 32, 64 x 64, 128 x 128, 256 x 256
-constexpr int kXentPart[] = {32, 32, 64, 128};
+enum { kFew, kNarrow, kSmall, kMid, kBig };  // 128 x 32, 128 x 64, 64 x 64, 128 x 128, 256 x 256
+constexpr int kXentPart[] = {32, 32, 32, 64, 128};
 
-// Which: 256 x 256 (one block to a CU) where it has blocks for more than half
-// of the chip's CUs, else 128 x 128 (two to a CU) on the same condition, else 64 x 64.
-static int xent_shape(int64_t a, int64_t b, int64_t splits) {
-  auto blocks = [&](int64_t m) { return (a + m - 1) / m * ((b + m - 1) / m) * splits; };
-  return blocks(256) > 128 ? kBig : blocks(128) > 128 ? kMid : kSmall;
+// Relative time of a product's blocks in a shape: rounds of 512 blocks, two to
+// a CU, and a last one that has up to 256 CUs to themselves; 256 x 256 tiles have
+// one to a CU, and are faster where not all CUs have any.  Measured against a
+// round of 256 x 256 tiles, 4096 x 65536 x 4096: 128 x 128 tiles 0.62 of the time for
+// half of the work, 64 x 64 0.33 for an eighth; alone on a CU little more than
+// half of that.  In fp32 the instruction is what takes time.
+static double xent_time(int parts, int shape, int64_t a, int64_t b, int64_t splits) {
+  const int64_t m = shape == kBig ? 256 : shape == kMid ? 128 : 64;
+  const int64_t n = (a + m - 1) / m * ((b + m - 1) / m) * splits;
+  if (shape == kBig) return (double)(n / 256) + (n % 256 ? 0.75 + 0.25 / 256 * (double)(n % 256) : 0.0);
+  const double pair = parts == 0 ? (shape == kMid ? 2.0 : 0.55) : shape == kMid ? 0.62 : 0.33;
+  const int64_t rest = n % 512;
+  return (double)(n / 512) * pair + (rest == 0 ? 0.0 : rest <= 256 ? 0.55 * pair : pair);
+}
+static int xent_shape(int parts, int64_t a, int64_t b, int64_t splits) {
+  if (b <= 64) return b <= 32 ? kFew : kNarrow;
+  int best = kSmall;
+  for (int s = kMid; s <= (parts > 0 ? kBig : kMid); ++s)
+    if (xent_time(parts, s, a, b, splits) <= xent_time(parts, best, a, b, splits)) best = s;
+  return best;
 }
 
 // A product over `words` words by `rows` rows (or columns) as one launch, or
-// as two: full rounds of 256 blocks, and what a last round would leave more than
-// half of the chip idle for in smaller tiles.
+// as two where that is faster: full rounds of 256 x 256 tiles, and the rest in smaller ones.
 struct XentLaunch {
   int shape;
   int64_t w0, words;
 };
-static int xent_launches(int64_t words, int64_t rows, XentLaunch (&l)[2]) {
-  l[0] = {xent_shape(words, rows, 1), 0, words};
-  if (l[0].shape != kBig) return 1;
-  const int64_t per = (rows + 255) / 256, blocks = (words + 255) / 256 * per, rest = blocks % 256;
+static int xent_launches(int parts, int64_t words, int64_t rows, XentLaunch (&l)[2]) {
+  l[0] = {xent_shape(parts, words, rows, 1), 0, words};
+  if (parts == 0 || rows <= 64) return 1;
+  const int64_t per = (rows + 255) / 256, blocks = (words + 255) / 256 * per;
   const int64_t first = blocks / 256 * 256 / per * 256;
-  if (rest == 0 || rest > 128 || first == 0 || first >= words) return 1;
-  l[0].words = first;
-  l[1] = {xent_shape(words - first, rows, 1), first, words - first};
+  if (first == 0 || first >= words) return 1;
+  const int rest = xent_shape(parts, words - first, rows, 1);
+  const double one = xent_time(parts, l[0].shape, words, rows, 1);
+  if (xent_time(parts, kBig, first, rows, 1) + xent_time(parts, rest, words - first, rows, 1) >= 0.97 * one) return 1;
+  l[0] = {kBig, 0, first};
+  l[1] = {rest, first, words - first};
   return 2;
 }
 
 struct XentPlan {
-  int parts;          // bfloat16 planes of an operand
+  int parts;          // bfloat16 planes of an operand; 0: fp32 as it is
+  int es;             // bytes of its values, in all planes
   int64_t piece;      // words of a piece, a multiple of 256
   int pieces;
   int64_t rows;       // rows of a forward pass over the vocabulary
@@ -75,13 +96,12 @@ struct XentPlan {
   size_t hc, wp, n, live, y, lse, g, ds, slab, zt, part, bytes;
 };
 
-static bool xent_few(int64_t T) { return T <= 32; }
-
 static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
   XentPlan p{};
-  p.parts = dt == DS4MOE_DT_F32 ? 3 : 1;
+  p.parts = dt != DS4MOE_DT_F32 ? 1 : T <= kXentF32Rows ? 0 : 3;
+  p.es = p.parts == 0 ? 4 : 2 * p.parts;
   // bytes per word of what a piece keeps: ds, and the planes of an fp32 w
-  const int64_t per = 2 * p.parts * std::max<int64_t>(grad ? T : 0, p.parts == 3 ? d : 0);
+  const int64_t per = p.es * std::max<int64_t>(grad ? T : 0, p.parts == 3 ? d : 0);
   const int64_t all = round_up<int64_t>(V, 256), tr = (T + 255) / 256, td = d / 256;
   const int64_t most = per ? std::max<int64_t>(2048, kXentPiece / per / 256 * 256) : all;
   // words of a piece whose products are full rounds of blocks
@@ -104,7 +124,7 @@ static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
     at += round_up<size_t>(bytes, 256);
     return here;
   };
-  if (p.parts == 3 || grad) p.hc = take((size_t)2 * p.parts * T * d);
+  if (p.parts == 3 || grad) p.hc = take((size_t)p.es * T * d);
   if (p.parts == 3) p.wp = take((size_t)6 * p.piece * d);
   if (grad) {
     p.n = take(8);
@@ -112,19 +132,18 @@ static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
     p.y = take(4 * T);
     p.lse = take(4 * T);
     p.g = take(4 * T);
-    p.ds = take((size_t)2 * p.parts * T * p.piece);
+    p.ds = take((size_t)p.es * T * p.piece);
     p.slab = take((size_t)4 * p.slabs * T * d);
   } else {
-    const int64_t parts = all / (xent_few(T) ? 32 : 128);
-    p.rows = std::min(T, std::max<int64_t>(1024, kXentPiece / (8 * parts) / 256 * 256));
+    p.rows = std::min(T, std::max<int64_t>(1024, kXentPiece / (8 * (all / 128)) / 256 * 256));
     p.zt = take(4 * p.rows);
     auto sums = [&](int64_t rows) {  // partial sums of that many rows
       int64_t n = 0;
       for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         XentLaunch l[2];
-        const int m = xent_launches(std::min(p.piece, V - v0), rows, l);
+        const int m = xent_launches(p.parts, std::min(p.piece, V - v0), rows, l);
         for (int i = 0; i < m; ++i) {
-          const int per = kXentPart[xent_few(T) ? kFew : l[i].shape];
+          const int per = kXentPart[l[i].shape];
           n += (l[i].words + per - 1) / per;
         }
       }
@@ -209,33 +228,49 @@ __device__ inline void xsplit8(const float (&x)[8], u32x4_t (&o)[3]) {
   }
 }
 
-// Rows of src (live[r], or r itself) side by side, as planes; dh of a row
-// without a target is zero.  A block takes a row.
-template <bool BF>
+// Live rows of src side by side, as planes; dh of a row without a target is
+// zero.  A block takes a row.
+template <int PARTS>
 __global__ __launch_bounds__(256) void k_xent_rows(const void* __restrict__ src, const int32_t* __restrict__ n,
                                                    const int32_t* __restrict__ live, int64_t rows, int d,
                                                    uint8_t* __restrict__ dst, int64_t plane, void* __restrict__ dh) {
+  constexpr bool BF = PARTS == 1;
+  const int n_live = *n;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const int64_t from = live ? live[r] : r;
-    const bool on = !n || r < *n;
+    const int64_t from = live[r];
+    const bool on = r < n_live;
     for (int i = 8 * threadIdx.x; i < d; i += 2048) {
       if (on) {
         const Raw8<BF> v = ld8<BF>(src, from * d + i);
-        if constexpr (BF) {
-          *(u32x4_t*)(dst + (r * d + i) * 2) = v.a;
-        } else {
+        if constexpr (PARTS == 3) {
           float x[8];
           u32x4_t o[3];
           unpack8<BF>(v, x);
           xsplit8(x, o);
 #pragma unroll
           for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + (r * d + i) * 2) = o[s];
+        } else {
+          *(Raw8<BF>*)(dst + (r * d + i) * (BF ? 2 : 4)) = v;
         }
       } else if (dh) {
         const float zero[8] = {};
         st8<BF>(dh, from * d + i, zero);
       }
     }
+  }
+}
+// All of n fp32 values (a multiple of 8) as planes.
+__global__ __launch_bounds__(256) void k_xent_split(const float* __restrict__ src, int64_t n, uint8_t* __restrict__ dst,
+                                                    int64_t plane) {
+  const int64_t step = (int64_t)gridDim.x * 2048;
+#pragma unroll 2
+  for (int64_t i = (int64_t)blockIdx.x * 2048 + 8 * threadIdx.x; i < n; i += step) {
+    float x[8];
+    u32x4_t o[3];
+    unpack8<false>(ld8<false>(src, i), x);
+    xsplit8(x, o);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + i * 2) = o[s];
   }
 }
 
@@ -293,11 +328,12 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
   int ta, tb, s;
   if (!xtile((int)((x.a_rows + S::BM - 1) / S::BM), (int)((b_rows + S::BN - 1) / S::BN), x.splits, ta, tb, s)) return;
   const int64_t a0 = (int64_t)ta * S::BM, b0 = (int64_t)tb * S::BN;
-  XSide<S::BM, ACOL> A;
-  XSide<S::BN, BCOL> B;
+  XSide<S::BM, ACOL, PARTS == 0> A;
+  XSide<S::BN, BCOL, PARTS == 0> B;
   A.init(x.a, a0, x.a_rows, tid);
   B.init(x.b, b0, b_rows, tid);
-  const int nk = (int)((K + 63) / 64);
+  constexpr int KC = PARTS == 0 ? 32 : 64;
+  const int nk = (int)((K + KC - 1) / KC);
   const int kc0 = (int)((int64_t)nk * s / x.splits), kc1 = (int)((int64_t)nk * (s + 1) / x.splits);
   const int am = (wave % S::WM) * 32 * S::FM, bn = (wave / S::WM) * 32 * S::FN;
   float16_t acc[S::FM][S::FN] = {};
@@ -375,7 +411,8 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
     }
   } else if constexpr (EPI == XE_DS) {
     // words past the vocabulary's end are zeros: the products with ds run over whole pieces
-    uint8_t* const turn = smem + wave * 32 * xturn_pitch<S::FM, 2>();
+    constexpr int ES = PARTS == 0 ? 4 : 2;
+    uint8_t* const turn = smem + wave * 32 * xturn_pitch<S::FM, ES>();
     const float by = 1.0f / *x.top;
 #pragma unroll
     for (int i = 0; i < S::FN; ++i) {
@@ -384,13 +421,13 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
       const float lse = on ? x.lse[t] : 0.f, g = on ? x.g[t] * by : 0.f;
       const int y = on ? x.y[t] - x.v0 - (int)a0 - am : -1;
       // lse to base 2 in two parts where the values are held to fp32
-      const float l = 1.44269504f * lse, ll = PARTS == 3 ? fmaf(1.44269504f, lse, -l) + 1.92596299e-8f * lse : 0.f;
+      const float l = 1.44269504f * lse, ll = PARTS != 1 ? fmaf(1.44269504f, lse, -l) + 1.92596299e-8f * lse : 0.f;
 #pragma unroll
       for (int f = 0; f < S::FM; ++f)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           float e = fmaf(k2, acc[f][i][v], -l);
-          if (PARTS == 3) e -= ll;
+          if (PARTS != 1) e -= ll;
           acc[f][i][v] = __builtin_amdgcn_exp2f(e);
         }
       if (__ballot(y >= 0 && y < 32 * S::FM)) {
@@ -411,12 +448,12 @@ __global__ __launch_bounds__(256, S::lds > 80 * 1024 ? 1 : 2) void k_xent_gemm(X
         for (int v = 0; v < 16; ++v) acc[f][i][v] *= g;
       // by planes: what the bfloat16 before leaves
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        xturn<S::FM, 2>(
+      for (int q = 0; q < std::max(PARTS, 1); ++q) {
+        xturn<S::FM, ES>(
             turn, lane, [&](int f, int v) { return acc[f][i][v]; },
             [&](int row, int ch, u32x4_t v) {
               const int64_t r = b0 + bn + 32 * i + row;
-              if (r < b_rows) *(u32x4_t*)(x.out + q * x.out_plane + r * x.out_pitch + (a0 + am) * 2 + ch * 16) = v;
+              if (r < b_rows) *(u32x4_t*)(x.out + q * x.out_plane + r * x.out_pitch + (a0 + am) * ES + ch * 16) = v;
             });
         if (q + 1 < PARTS) {
 #pragma unroll
@@ -511,7 +548,8 @@ __global__ __launch_bounds__(256) void k_xent_dh(const float* __restrict__ slab,
 }
 
 // ---------------------------------------------------------------- launches
-using XFew = XShape<4, 1, 1, 1, 3>;    // two blocks to a CU, as the next two have
+using XFew = XShape<4, 1, 1, 1, 3>;    // two blocks to a CU, as the next three have
+using XNarrow = XShape<4, 1, 1, 2, 3>;
 using XSmall = XShape<2, 2, 1, 1, 4>;
 using XMid = XShape<2, 2, 2, 2, 2>;
 using XBig = XShape<2, 2, 4, 4, 2>;
@@ -524,26 +562,30 @@ static hipError_t xent_launch(const XArgs& x, hipStream_t st) {
 }
 template <int EPI, int PARTS, bool OBF>
 static hipError_t xent_shaped(int shape, const XArgs& x, hipStream_t st) {
-  if constexpr (EPI == XE_SUM) {
+  if constexpr (EPI != XE_ROWS) {
     if (shape == kFew) return xent_launch<XFew, EPI, PARTS, OBF>(x, st);
+    if (shape == kNarrow) return xent_launch<XNarrow, EPI, PARTS, OBF>(x, st);
   }
   if (shape == kSmall) return xent_launch<XSmall, EPI, PARTS, OBF>(x, st);
-  if (shape == kMid) return xent_launch<XMid, EPI, PARTS, OBF>(x, st);
-  return xent_launch<XBig, EPI, PARTS, OBF>(x, st);
+  if constexpr (PARTS > 0) {
+    if (shape == kBig) return xent_launch<XBig, EPI, PARTS, OBF>(x, st);
+  }
+  return xent_launch<XMid, EPI, PARTS, OBF>(x, st);
 }
 // The product of a piece: its words are a's, or b's (dw); the sum over words
 // of dh is one launch.
 template <int EPI, int PARTS, bool OBF>
-static hipError_t xent_gemm(XArgs& x, bool few, hipStream_t st) {
-  if (EPI == XE_SLAB) return xent_shaped<EPI, PARTS, OBF>(xent_shape(x.a_rows, x.b_rows, x.splits), x, st);
+static hipError_t xent_gemm(XArgs& x, hipStream_t st) {
+  if (EPI == XE_SLAB) return xent_shaped<EPI, PARTS, OBF>(xent_shape(PARTS, x.a_rows, x.b_rows, x.splits), x, st);
   constexpr bool of_b = EPI == XE_ROWS;
+  constexpr int kES = PARTS == 0 ? 4 : 2;
   XentLaunch l[2];
-  const int n = xent_launches(of_b ? x.b_rows : x.a_rows, of_b ? x.a_rows : x.b_rows, l);
+  const int n = xent_launches(PARTS, of_b ? x.b_rows : x.a_rows, of_b ? x.a_rows : x.b_rows, l);
   for (int i = 0; i < n; ++i) {
     XArgs y = x;
-    const int shape = few ? kFew : l[i].shape;
+    const int shape = of_b && l[i].shape < kSmall ? kSmall : l[i].shape;
     if (of_b) {
-      y.b.p += 2 * l[i].w0;
+      y.b.p += kES * l[i].w0;
       y.b_rows = l[i].words;
       y.out += l[i].w0 * y.out_pitch;
     } else {
@@ -551,7 +593,7 @@ static hipError_t xent_gemm(XArgs& x, bool few, hipStream_t st) {
       y.a_rows = l[i].words;
       y.V = (int)l[i].words;
       y.v0 += (int)l[i].w0;
-      y.out += 2 * l[i].w0;
+      y.out += kES * l[i].w0;
       x.part0 += (int)((l[i].words + kXentPart[shape] - 1) / kXentPart[shape]);
     }
     const hipError_t e = xent_shaped<EPI, PARTS, OBF>(shape, y, st);
@@ -561,33 +603,32 @@ static hipError_t xent_gemm(XArgs& x, bool few, hipStream_t st) {
 }
 static unsigned xent_row_blocks(int64_t rows) { return (unsigned)std::min<int64_t>(rows, 8192); }
 
-// all rows of an fp32 matrix as planes
-static void xent_copy(const void* src, int64_t rows, int d, uint8_t* dst, int64_t plane, hipStream_t st) {
-  DS4_LAUNCH(k_xent_rows<false>, dim3(xent_row_blocks(rows)), dim3(256), 0, st, src, (const int32_t*)nullptr,
-             (const int32_t*)nullptr, rows, d, dst, plane, (void*)nullptr);
+static void xent_split(const void* src, int64_t n, uint8_t* dst, int64_t plane, hipStream_t st) {
+  DS4_LAUNCH(k_xent_split, dim3((unsigned)std::min<int64_t>((n + 2047) / 2048, 4096)), dim3(256), 0, st, (const float*)src,
+             n, dst, plane);
 }
 
 template <int PARTS>
 static hipError_t xent_forward(const XentCall& c) {
   const XentPlan p = xent_plan(c.dt, c.T, c.V, c.d, false);
   uint8_t* w = c.ws;
-  const bool few = xent_few(c.T);
-  const int64_t pitch = 2 * (int64_t)c.d;
+  constexpr int kES = PARTS == 0 ? 4 : 2, kIn = PARTS == 1 ? 2 : 4;  // bytes of an operand's value, of an input's
+  const int64_t pitch = kES * (int64_t)c.d;
   XOperand h = {(const uint8_t*)c.h, 0, pitch};
   if (PARTS == 3) {
     h = {w + p.hc, c.T * pitch, pitch};
-    xent_copy(c.h, c.T, c.d, w + p.hc, h.plane, c.st);
+    xent_split(c.h, c.T * c.d, w + p.hc, h.plane, c.st);
   }
   for (int64_t r0 = 0; r0 < c.T; r0 += p.rows) {
     const int64_t rows = std::min(c.T - r0, p.rows);
     int parts = 0;
     for (int i = 0; i < p.pieces; ++i) {
       const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
-      const uint8_t* src = (const uint8_t*)c.w + v0 * pitch * (PARTS == 3 ? 2 : 1);
+      const uint8_t* src = (const uint8_t*)c.w + v0 * c.d * kIn;
       XArgs x{};
       x.a = {src, 0, pitch};
       if (PARTS == 3) {
-        xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
+        xent_split(src, words * c.d, w + p.wp, p.piece * pitch, c.st);
         x.a = {w + p.wp, p.piece * pitch, pitch};
       }
       x.b = {h.p + r0 * h.pitch, h.plane, h.pitch};
@@ -603,7 +644,7 @@ static hipError_t xent_forward(const XentCall& c) {
       x.part = (float2*)(w + p.part);
       x.part0 = parts;
       x.zt = (float*)(w + p.zt);
-      const hipError_t e = xent_gemm<XE_SUM, PARTS, false>(x, few, c.st);
+      const hipError_t e = xent_gemm<XE_SUM, PARTS, false>(x, c.st);
       if (e) return e;
       parts = x.part0;
     }
@@ -620,25 +661,26 @@ static hipError_t xent_forward(const XentCall& c) {
 template <int PARTS>
 static hipError_t xent_backward(const XentCall& c) {
   constexpr bool BF = PARTS == 1;
+  constexpr int kES = PARTS == 0 ? 4 : 2, kIn = PARTS == 1 ? 2 : 4;
   const XentPlan p = xent_plan(c.dt, c.T, c.V, c.d, true);
   uint8_t* w = c.ws;
-  const int64_t pitch = 2 * (int64_t)c.d;
+  const int64_t pitch = kES * (int64_t)c.d;
   int32_t* const n = (int32_t*)(w + p.n);
   int32_t* const live = (int32_t*)(w + p.live);
   hipError_t e;
   DS4_LAUNCH(k_xent_live, dim3(1), dim3(1024), 0, c.st, c.target, (int)c.T, (int)c.V, c.scale, c.lse_in, c.dloss, n, live,
              (int32_t*)(w + p.y), (float*)(w + p.lse), (float*)(w + p.g));
-  DS4_LAUNCH((k_xent_rows<PARTS == 1>), dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, c.h, (const int32_t*)n,
+  DS4_LAUNCH((k_xent_rows<PARTS>), dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, c.h, (const int32_t*)n,
              (const int32_t*)live, c.T, c.d, w + p.hc, c.T * pitch, c.dh);
   for (int i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
-    const uint8_t* src = (const uint8_t*)c.w + v0 * pitch * (PARTS == 3 ? 2 : 1);
+    const uint8_t* src = (const uint8_t*)c.w + v0 * c.d * kIn;
     XOperand wop = {src, 0, pitch};
     if (PARTS == 3) {
-      xent_copy(src, words, c.d, w + p.wp, p.piece * pitch, c.st);
+      xent_split(src, words * c.d, w + p.wp, p.piece * pitch, c.st);
       wop = {w + p.wp, p.piece * pitch, pitch};
     }
-    const XOperand hop = {w + p.hc, c.T * pitch, pitch}, dsop = {w + p.ds, 2 * c.T * p.piece, 2 * p.piece};
+    const XOperand hop = {w + p.hc, c.T * pitch, pitch}, dsop = {w + p.ds, kES * c.T * p.piece, kES * p.piece};
     XArgs x{};
     x.a = wop;
     x.b = hop;
@@ -658,7 +700,7 @@ static hipError_t xent_backward(const XentCall& c) {
     x.out_pitch = dsop.pitch;
     x.out_plane = dsop.plane;
     // the last tile's words past the end are written too: as zeros
-    if ((e = xent_gemm<XE_DS, PARTS, false>(x, false, c.st))) return e;
+    if ((e = xent_gemm<XE_DS, PARTS, false>(x, c.st))) return e;
     if (c.dh) {
       XArgs u{};
       u.a = wop;
@@ -672,7 +714,7 @@ static hipError_t xent_backward(const XentCall& c) {
       u.out_pitch = 4 * (int64_t)c.d;
       u.out_plane = 4 * c.T * c.d;
       u.add = i > 0;
-      if ((e = xent_gemm<XE_SLAB, PARTS, false>(u, false, c.st))) return e;
+      if ((e = xent_gemm<XE_SLAB, PARTS, false>(u, c.st))) return e;
     }
     if (c.dw) {
       XArgs u{};
@@ -684,9 +726,9 @@ static hipError_t xent_backward(const XentCall& c) {
       u.n = n;
       u.top = (const float*)n + 1;
       u.splits = 1;
-      u.out = (uint8_t*)c.dw + v0 * c.d * (BF ? 2 : 4);
-      u.out_pitch = c.d * (int64_t)(BF ? 2 : 4);
-      if ((e = xent_gemm<XE_ROWS, PARTS, BF>(u, false, c.st))) return e;
+      u.out = (uint8_t*)c.dw + v0 * c.d * kIn;
+      u.out_pitch = c.d * (int64_t)kIn;
+      if ((e = xent_gemm<XE_ROWS, PARTS, BF>(u, c.st))) return e;
     }
   }
   if (c.dh)
@@ -695,11 +737,14 @@ static hipError_t xent_backward(const XentCall& c) {
   return hipGetLastError();
 }
 
+static int xent_parts(const XentCall& c) { return xent_plan(c.dt, c.T, c.V, c.d, false).parts; }
 hipError_t launch_xent(const XentCall& c) {
-  return c.dt == DS4MOE_DT_F32 ? xent_forward<3>(c) : xent_forward<1>(c);
+  const int parts = xent_parts(c);
+  return parts == 0 ? xent_forward<0>(c) : parts == 1 ? xent_forward<1>(c) : xent_forward<3>(c);
 }
 hipError_t launch_xent_grad(const XentCall& c) {
-  return c.dt == DS4MOE_DT_F32 ? xent_backward<3>(c) : xent_backward<1>(c);
+  const int parts = xent_parts(c);
+  return parts == 0 ? xent_backward<0>(c) : parts == 1 ? xent_backward<1>(c) : xent_backward<3>(c);
 }
 
 }  // namespace ds4

@@ -9,13 +9,17 @@
 // turned by the transposing LDS read).  fp32 operands come as three bfloat16
 // planes whose sum they are, and a chunk is multiplied six times: hi hi, hi
 // mid, mid hi, mid mid, hi lo, lo hi.  What is left out is below 2^-24 of the
-// product, fp32's own rounding.
+// product, fp32's own rounding.  For few rows, where reading the operands is
+// what takes time, they stay fp32 and go through v_mfma_f32_32x32x2_f32, 32 k a
+// chunk: lane l's four values of a 16-byte piece take four products, in which
+// the two halves of the wave hold k's four apart in both operands.
 //
 // LDS: 16-byte pieces, swizzled on their way in by choosing which piece a
 // lane copies.  By rows piece p of row r lies at p ^ (r / 2 & 7), so that the
 // 16 rows that a quarter of a wave reads lie in different banks; by columns
 // piece p of row k lies at p ^ 4 (k & 3) (as far as its row has pieces), since
-// half a wave reads four neighbouring pieces of four rows.
+// half a wave reads four neighbouring pieces of four rows; in fp32 at
+// p ^ 8 (k / 4 & 1), since its halves read eight pieces of rows four apart.
 #pragma once
 
 #include "../ring.h"
@@ -30,6 +34,15 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 __device__ inline float16_t mfma32(u32x4_t a, u32x4_t b, float16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);
+}
+
+__device__ inline float16_t mfma32_f32(u32x4_t a, u32x4_t b, float16_t c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = a[e], y = b[e];
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y), c, 0, 0, 0);
+  }
+  return c;
 }
 
 // The transposing read.  The argument's __restrict__ is what the compiler knows
@@ -56,12 +69,17 @@ struct XOperand {
 };
 
 // One operand's side of a tile of B indices, from index i0 on.
-template <int B, bool COL>
+template <int B, bool COL, bool F32>
 struct XSide {
+  static constexpr int ES = F32 ? 4 : 2, KC = 128 / ES;  // bytes of a value, k of a chunk
+  static constexpr int RB = B * ES, P = RB / 16;         // by columns: bytes and pieces of a k
+  static constexpr int kStep = COL ? 4096 / RB : 32;     // rows from one copy to the next
+  static_assert(!COL || !F32 || kStep % 8 == 0, "the swizzle of a thread's copies is one");
   const uint8_t* base;
   int64_t plane, pitch;
   uint32_t records;  // by rows: bytes that the tile has; by columns: what a row's end leaves out
   uint32_t vo;       // the lane's piece
+  static __device__ inline int swizzle(int k) { return (F32 ? 8 * (k >> 2 & 1) : 4 * (k & 3)) & (P - 1); }
   __device__ inline void init(const XOperand& o, int64_t i0, int64_t rows, int tid) {
     plane = o.plane;
     pitch = o.pitch;
@@ -71,22 +89,20 @@ struct XSide {
       const int r = tid >> 3;
       vo = (uint32_t)(r * pitch) + ((tid ^ (r >> 1)) & 7) * 16;
     } else {
-      constexpr int P = B / 8;  // pieces of a row
-      base = o.p + i0 * 2;
-      records = (uint32_t)i0 * 2;
+      base = o.p + i0 * ES;
+      records = (uint32_t)i0 * ES;
       const int k = tid / P, p = tid % P;
-      vo = (uint32_t)(k * pitch) + (p ^ (4 * (k & 3) & (P - 1))) * 16;
+      vo = (uint32_t)(k * pitch) + (p ^ swizzle(k)) * 16;
     }
   }
-  static constexpr int kStep = COL ? 2048 / B : 32;  // rows from one copy to the next
   // chunk kc of plane q; K: how many k there are
   __device__ __attribute__((always_inline)) inline __amdgpu_buffer_rsrc_t chunk(int kc, int q, int64_t K) const {
     const uint8_t* src = base + q * plane;
     if constexpr (!COL) {
       return buf_rsrc(src + (int64_t)kc * 128, kc * 128 < (int)records ? records - kc * 128 : 0);
     } else {
-      const int64_t left = K - (int64_t)kc * 64;
-      return buf_rsrc(src + (int64_t)kc * 64 * pitch, left > 0 ? (uint32_t)((left < 64 ? left : 64) * pitch) - records : 0);
+      const int64_t left = K - (int64_t)kc * KC;
+      return buf_rsrc(src + (int64_t)kc * KC * pitch, left > 0 ? (uint32_t)((left < KC ? left : KC) * pitch) - records : 0);
     }
   }
   // copy i of the thread (B / 32 in all), of a chunk that lies at dst
@@ -95,23 +111,29 @@ struct XSide {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(dst + i * 4096 + wave * 1024),
                                              16, on ? (int)vo : (int)kOob, (int)(i * kStep * pitch), 0, 0);
   }
-  // Fragment f (32 indices from first on) of step j (16 k): lane l gets index
-  // l & 31 and k 8 (l >> 5) .. + 7.
+  // Fragment f (32 indices from first on) of step j, a quarter of the chunk:
+  // lane l gets index l & 31 and k 8 (l >> 5) .. + 7 of the step's 16; in fp32
+  // k 4 (l >> 5) .. + 3 of its 8.
   static __device__ __attribute__((always_inline)) inline u32x4_t read(const uint8_t* at, int first, int f, int j,
                                                                        int lane) {
     if constexpr (!COL) {
       const int c = lane & 31, h = lane >> 5;
       return *(const u32x4_t*)(at + (first + 32 * f + c) * 128 + (((2 * j + h) ^ (c >> 1)) & 7) * 16);
+    } else if constexpr (F32) {
+      const int c = lane & 31, h = lane >> 5, piece = (first / 4 + 8 * f + (c >> 2)) ^ swizzle(4 * h);
+      u32x4_t v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *(const uint32_t*)(at + (8 * j + 4 * h + e) * RB + piece * 16 + 4 * (c & 3));
+      return v;
     } else {
       // Of a quarter's 16 lanes, four hold 16 neighbouring indices of one k,
       // four k in all; the read hands lane i index i of the four.
-      constexpr int RB = B * 2, P = B / 8;
       const int i = lane & 15, s = (lane >> 4) & 1, h = lane >> 5;
       u32x4_t v;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int k = 4 * r + (i >> 2);  // its last three bits
-        const int piece = (first / 8 + 4 * f + 2 * s + ((i & 3) >> 1)) ^ (4 * (k & 3) & (P - 1));
+        const int piece = (first / 8 + 4 * f + 2 * s + ((i & 3) >> 1)) ^ swizzle(k);
         const u32x2_t x = read_turned((lds_s16x4_t*)(at + (16 * j + 8 * h + k) * RB + piece * 16 + 8 * (i & 1)));
         v[2 * r] = x.x;
         v[2 * r + 1] = x.y;
@@ -125,7 +147,8 @@ struct XSide {
 __device__ inline int plane_a(int q) { return (0x200110 >> (4 * (5 - q))) & 3; }
 __device__ inline int plane_b(int q) { return (0x021010 >> (4 * (5 - q))) & 3; }
 
-// Chunks kc0 .. kc1 - 1 of the tile into acc[FM][FN] of this wave.
+// Chunks kc0 .. kc1 - 1 of the tile into acc[FM][FN] of this wave.  PARTS: the
+// bfloat16 planes of an operand, 0 for fp32 as it is.
 //
 // One chunk after another, with R - 1 of them under way.  256 x 256 tiles are
 // written out further: with one wave to a SIMD nothing else hides a wait, so a
@@ -133,8 +156,8 @@ __device__ inline int plane_b(int q) { return (0x021010 >> (4 * (5 - q))) & 3; }
 // the chunk's border too, and the copies are dealt out between products, which
 // would otherwise wait behind a run of them.
 template <class S, bool ACOL, bool BCOL, int PARTS>
-__device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, ACOL>& A, const XSide<S::BN, BCOL>& B,
-                                                            int64_t K, int kc0, int kc1, uint8_t* smem,
+__device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, ACOL, PARTS == 0>& A,
+                                                            const XSide<S::BN, BCOL, PARTS == 0>& B, int64_t K, int kc0, int kc1, uint8_t* smem,
                                                             float16_t (&acc)[S::FM][S::FN], int wave, int lane) {
   constexpr int Q = PARTS == 3 ? 6 : 1;
   const int n = (kc1 - kc0) * Q;
@@ -159,8 +182,8 @@ __device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, A
     auto copy_a = [&](const Chunk& x, int i, uint8_t* dst) __attribute__((always_inline)) { A.copy(x.a, x.on, i, dst, wave); };
     auto copy_b = [&](const Chunk& x, int i, uint8_t* dst) __attribute__((always_inline)) { B.copy(x.b, x.on, i, dst, wave); };
     auto read1 = [&](Frags& N, int p, const uint8_t* sa, const uint8_t* sb, int j) __attribute__((always_inline)) {
-      if (p < 4) N.a[p] = XSide<S::BM, ACOL>::read(sa, am, p, j, lane);
-      else if (p < 8) N.b[p - 4] = XSide<S::BN, BCOL>::read(sb, bn, p - 4, j, lane);
+      if (p < 4) N.a[p] = XSide<S::BM, ACOL, PARTS == 0>::read(sa, am, p, j, lane);
+      else if (p < 8) N.b[p - 4] = XSide<S::BN, BCOL, PARTS == 0>::read(sb, bn, p - 4, j, lane);
     };
     // A step's 16 products; between them the reads of the next step's
     // fragments (step j of the chunk at sa and sb), and copies.
@@ -220,9 +243,9 @@ __device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, A
     };
     auto read = [&](Frags& F, const uint8_t* slot, int j) __attribute__((always_inline)) {
   #pragma unroll
-      for (int f = 0; f < S::FM; ++f) F.a[f] = XSide<S::BM, ACOL>::read(slot, am, f, j, lane);
+      for (int f = 0; f < S::FM; ++f) F.a[f] = XSide<S::BM, ACOL, PARTS == 0>::read(slot, am, f, j, lane);
   #pragma unroll
-      for (int f = 0; f < S::FN; ++f) F.b[f] = XSide<S::BN, BCOL>::read(slot + S::BM * 128, bn, f, j, lane);
+      for (int f = 0; f < S::FN; ++f) F.b[f] = XSide<S::BN, BCOL, PARTS == 0>::read(slot + S::BM * 128, bn, f, j, lane);
     };
 #pragma unroll
     for (int u = 0; u < S::R - 1; ++u) {
@@ -250,7 +273,8 @@ __device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, A
 #pragma unroll
         for (int i = 0; i < S::FN; ++i)
 #pragma unroll
-          for (int f = 0; f < S::FM; ++f) acc[f][i] = mfma32(F.a[f], F.b[i], acc[f][i]);
+          for (int f = 0; f < S::FM; ++f)
+            acc[f][i] = PARTS == 0 ? mfma32_f32(F.a[f], F.b[i], acc[f][i]) : mfma32(F.a[f], F.b[i], acc[f][i]);
       }
       u = u + 1 == S::R ? 0 : u + 1;
     }
