@@ -267,7 +267,7 @@ __global__ __launch_bounds__(kAdamThreads) void k_adamw_squares(const ds4moe_par
     const void* grad = params[r.tensor].grad;
     const int64_t at = r.run * run, end = min(at + take * run, params[r.tensor].n);
     const bool vec = ((uintptr_t)grad & 15) == 0;
-    constexpr int U = 4;
+    constexpr int U = 2;
     for (int64_t i0 = at + 8 * threadIdx.x; i0 < end; i0 += U * 8 * kAdamThreads) {
       float g[U][8];
 #pragma unroll

@@ -338,14 +338,15 @@ __device__ inline int ends_before(const int32_t* __restrict__ off, int seqs, int
 }
 
 template <int G, int NV, bool BF>
-__global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* __restrict__ z, int T, int E, int k,
+// (z and dz may be one: a wave reads its rows before it writes them)
+__global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* z, int T, int E, int k,
                                                               const int32_t* __restrict__ idx,
                                                               const int32_t* __restrict__ off, int seqs, bool vec,
                                                               const int32_t* __restrict__ counts,
                                                               const int32_t* __restrict__ tokens,
                                                               const float* __restrict__ dloss,
                                                               const float* __restrict__ dslots, int run,
-                                                              void* __restrict__ dz) {
+                                                              void* dz) {
   constexpr int ROWS = 64 / G, W = kBalThreads / 64;
   const int lane = threadIdx.x & 63, g = lane % G, rg = lane / G;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

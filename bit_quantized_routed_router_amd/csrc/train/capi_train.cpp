@@ -4,6 +4,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <utility>
+#include <vector>
 
 #include "../trace.h"
 #include "train.h"
@@ -59,6 +61,33 @@ static int check_options(const ds4moe_adamw* A) {
   if (!(A->beta1 >= 0.0 && A->beta1 < 1.0) || !(A->beta2 >= 0.0 && A->beta2 < 1.0)) return DS4MOE_EINVAL;
   return al(A->lr_dev, 4) && al(A->step_dev, 4) ? DS4MOE_OK : DS4MOE_EALIGN;
 }
+// types and states that a table was made for
+static int64_t kinds_of(const ds4moe_adamw* A) { return 8 | A->param_dtype | A->grad_dtype << 1 | A->state << 2; }
+// Whether two of the ranges that a step writes overlap.
+static bool overlap(const ds4moe_adamw* A, const ds4moe_param* p, int32_t n) {
+  const bool fp8 = A->state == DS4MOE_STATE_FP8;
+  std::vector<std::pair<uintptr_t, uintptr_t>> r;
+  r.reserve((size_t)n * (fp8 ? 6 : 4));
+  for (int32_t i = 0; i < n; ++i) {
+    const ds4moe_param& q = p[i];
+    if (q.n == 0) continue;
+    auto add = [&](const void* at, int64_t bytes) {
+      if (at) r.emplace_back((uintptr_t)at, (uintptr_t)at + (uintptr_t)bytes);
+    };
+    add(q.param, q.n * dt_size(A->param_dtype));
+    add(q.master, q.n * 4);
+    add(q.m, q.n * (fp8 ? 1 : 4));
+    add(q.v, q.n * (fp8 ? 1 : 4));
+    if (fp8) {
+      add(q.m_scale, (q.n + 255) / 256 * 4);
+      add(q.v_scale, (q.n + 255) / 256 * 4);
+    }
+  }
+  std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].second) return true;
+  return false;
+}
 static int check_params(const ds4moe_adamw* A, const ds4moe_param* p, int32_t n) {
   const bool fp8 = A->state == DS4MOE_STATE_FP8;
   for (int32_t i = 0; i < n; ++i) {
@@ -79,7 +108,7 @@ static int check_table(const ds4moe_adamw* A, const void* table) {
   if (A->n_params < 0 || A->n_params > kAdamMaxTensors || A->blocks < 0 || A->blocks > kAdamMaxBlocks || A->run < 256 ||
       A->run % 256)
     return DS4MOE_ESHAPE;
-  if (!table) return DS4MOE_EINVAL;
+  if (!table || A->kinds != kinds_of(A)) return DS4MOE_EINVAL;
   return al(table, 16) ? DS4MOE_OK : DS4MOE_EALIGN;
 }
 
@@ -212,7 +241,13 @@ int ds4moe_adamw_table(ds4moe_adamw* A, const ds4moe_param* params, int32_t n_pa
   if ((rc = check_params(A, params, n_params))) return rc;
   if (!al(table, 8)) return DS4MOE_EALIGN;
   if (table_bytes < adam_table_bytes(params, n_params)) return DS4MOE_EWORKSPACE;
+  try {  // (the ranges take host memory)
+    if (overlap(A, params, n_params)) return DS4MOE_EINVAL;
+  } catch (...) {
+    return DS4MOE_EWORKSPACE;
+  }
   adam_table(A, params, n_params, table);
+  A->kinds = kinds_of(A);
   return DS4MOE_OK;
 }
 

@@ -75,6 +75,7 @@ class AdamWDesc(ctypes.Structure):
         ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
         ("n_params", ctypes.c_int32), ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
         ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p), ("run", ctypes.c_int64), ("blocks", ctypes.c_int64),
+        ("kinds", ctypes.c_int64),
     ]
 
 
@@ -512,7 +513,7 @@ class AdamW:
         one = lambda name, ts: self._type(name, ts[0]) if ts else DT_F32  # noqa: E731
         lr_at, step_at = self._check([(lr_dev, 1, DT_F32), (step_dev, 1, _I32)])
         self.desc = AdamWDesc(one("params", params), one("grads", grads), STATE_FP8 if fp8 else STATE_F32, 0, lr, beta1,
-                              beta2, eps, lr_at, step_at, 0, 0)
+                              beta2, eps, lr_at, step_at, 0, 0, 0)
         self.table = None
         self._make_table()
 

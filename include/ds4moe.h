@@ -559,19 +559,19 @@ typedef struct {
 typedef struct {
   int32_t param_dtype, grad_dtype; /* DS4MOE_DT_*, of all tensors */
   int32_t state;                   /* DS4MOE_STATE_* */
-  int32_t n_params;                /* this and the last two are ds4moe_adamw_table's to fill in */
+  int32_t n_params;                /* this and the last three are ds4moe_adamw_table's to fill in */
   double lr, beta1, beta2, eps;    /* finite; 0 <= beta < 1; eps > 0 as an fp32 */
   const float *lr_dev;             /* device: the learning rate in lr's place, or NULL */
   const int32_t *step_dev;         /* device: the step in the argument's place, or NULL */
-  int64_t run, blocks;
+  int64_t run, blocks, kinds;
 } ds4moe_adamw;
 
-/* The tensors as a table, laid out once: ds4moe_adamw_table checks them (no two
- * may overlap; 0 <= n_params <= 2^20) and writes the table to host memory
- * (8-byte aligned, ds4moe_adamw_table_bytes), which the program copies to the
- * device, 16-byte aligned, for the calls below.  It holds the tensors'
- * addresses: where one moves, a new table is made.  The other fields of A may
- * change between steps. */
+/* The tensors as a table, laid out once: ds4moe_adamw_table checks them
+ * (0 <= n_params <= 2^20; what a step writes must not overlap: DS4MOE_EINVAL) and
+ * writes the table to host memory (8-byte aligned, ds4moe_adamw_table_bytes), which the
+ * program copies to the device, 16-byte aligned, for the calls below.  It holds
+ * the tensors' addresses: where one moves, or types or states change, a new
+ * table is made.  lr, betas, eps, lr_dev and step_dev may change between steps. */
 size_t ds4moe_adamw_table_bytes(const ds4moe_param *params, int32_t n_params);
 int ds4moe_adamw_table(ds4moe_adamw *A, const ds4moe_param *params, int32_t n_params, void *table, size_t table_bytes);
 

@@ -209,8 +209,8 @@ def test_norm(sizes, g, shift):
     ts = make(sizes, "f32", g, seed=30)
     total = math.sqrt(sum(float(t["g"].double().square().sum()) for t in ts))
     grads = [put(t["g"], shift)[0] for t in ts]
-    z = [torch.zeros(n, device="cuda") for n in sizes]
-    opt = D.AdamW(z, grads, z, z)
+    p, m, v = ([torch.zeros(n, device="cuda") for n in sizes] for _ in range(3))
+    opt = D.AdamW(p, grads, m, v)
     n = opt.workspace_bytes()
     ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
     for most in (total * 0.5, total * 2, float("inf"), 1e-30):
@@ -225,7 +225,8 @@ def test_norm(sizes, g, shift):
 def test_norm_of_large_small_and_no_gradients():
     def norm(*gs):
         gs = [torch.tensor(g, device="cuda") for g in gs]
-        opt = D.AdamW(gs, gs, gs, gs)
+        p, m, v = ([torch.zeros_like(g) for g in gs] for _ in range(3))
+        opt = D.AdamW(p, gs, m, v)
         n = opt.workspace_bytes()
         out = torch.zeros(2, device="cuda")
         D.adamw_norm(opt, 1.0, out, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
