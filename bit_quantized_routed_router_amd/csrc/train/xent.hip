@@ -29,8 +29,10 @@ namespace ds4 {
 // sums).
 constexpr int64_t kXentPiece = 256 << 20;   // bytes that either aims at
 // fp32 operands of up to so many rows go through the fp32 instruction as they
-// are, of more as planes (times forward / forward and back, us):
+// are, of more as planes (forward / forward and back: 384 x 30000 x 1024 209 /
+// 825 us, as planes 227 / 841; 512 x 60000 x 1024 570 / 2007, as planes 399 / 1682)
 constexpr int64_t kXentF32Rows = 384;
+constexpr int64_t kXentCounted = 2048;      // rows up to which every block counts the live ones before it
 constexpr int kXentSlabs = 8;               // parts of the sum over words in dh, at most
 
 template <typename T>
@@ -157,6 +159,10 @@ static XentPlan xent_plan(int dt, int64_t T, int64_t V, int d, bool grad) {
 size_t xent_ws_bytes(int dt, int64_t T, int64_t V, int d, bool grad) { return xent_plan(dt, T, V, d, grad).bytes; }
 
 // ---------------------------------------------------------------- rows that have a target
+// The largest |g|, where its reciprocal has fp32's range too.
+__device__ inline float xent_top(float top) {
+  return top >= 1.17549435e-38f && top <= 8.507059e37f ? top : 1.0f;
+}
 // live: the rows with a target in order, then the others from the end; n: how
 // many; y, lse, g: theirs; top: the largest |g|, or 1.  One block: rows are
 // few beside the products.
@@ -203,8 +209,7 @@ __global__ __launch_bounds__(1024) void k_xent_live(const int32_t* __restrict__ 
   if (tid != 0) return;
   for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w]);
   n[0] = base;
-  // a range that its reciprocal stays within, too
-  ((float*)n)[1] = top >= 1.17549435e-38f && top <= 8.507059e37f ? top : 1.0f;
+  ((float*)n)[1] = xent_top(top);
 }
 
 // x as three bfloat16 values whose sum it is (8 + 8 + 8 bits, by truncation;
@@ -228,36 +233,89 @@ __device__ inline void xsplit8(const float (&x)[8], u32x4_t (&o)[3]) {
   }
 }
 
-// Live rows of src side by side, as planes; dh of a row without a target is
-// zero.  A block takes a row.
+// Row `from` of src as row r of the live rows, as planes; dh of a row without a
+// target is zero.
+template <int PARTS>
+__device__ inline void xent_row(const void* __restrict__ src, int64_t from, int64_t r, bool on, int d,
+                                uint8_t* __restrict__ dst, int64_t plane, void* __restrict__ dh) {
+  constexpr bool BF = PARTS == 1;
+  for (int i = 8 * threadIdx.x; i < d; i += 2048) {
+    if (on) {
+      const Raw8<BF> v = ld8<BF>(src, from * d + i);
+      if constexpr (PARTS == 3) {
+        float x[8];
+        u32x4_t o[3];
+        unpack8<BF>(v, x);
+        xsplit8(x, o);
+#pragma unroll
+        for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + (r * d + i) * 2) = o[s];
+      } else {
+        *(Raw8<BF>*)(dst + (r * d + i) * (BF ? 2 : 4)) = v;
+      }
+    } else if (dh) {
+      const float zero[8] = {};
+      st8<BF>(dh, from * d + i, zero);
+    }
+  }
+}
 template <int PARTS>
 __global__ __launch_bounds__(256) void k_xent_rows(const void* __restrict__ src, const int32_t* __restrict__ n,
                                                    const int32_t* __restrict__ live, int64_t rows, int d,
                                                    uint8_t* __restrict__ dst, int64_t plane, void* __restrict__ dh) {
-  constexpr bool BF = PARTS == 1;
   const int n_live = *n;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const int64_t from = live[r];
-    const bool on = r < n_live;
-    for (int i = 8 * threadIdx.x; i < d; i += 2048) {
-      if (on) {
-        const Raw8<BF> v = ld8<BF>(src, from * d + i);
-        if constexpr (PARTS == 3) {
-          float x[8];
-          u32x4_t o[3];
-          unpack8<BF>(v, x);
-          xsplit8(x, o);
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) xent_row<PARTS>(src, live[r], r, r < n_live, d, dst, plane, dh);
+}
+// k_xent_live and k_xent_rows in one, for as many rows as a block counts in a
+// moment: block t counts the live rows before row t, the last one all of them.
+template <int PARTS>
+__global__ __launch_bounds__(256) void k_xent_live_rows(const int32_t* __restrict__ target, int T, int V, float scale,
+                                                        const float* __restrict__ lse, const float* __restrict__ dloss,
+                                                        int32_t* __restrict__ n, int32_t* __restrict__ live,
+                                                        int32_t* __restrict__ y, float* __restrict__ lse_c,
+                                                        float* __restrict__ g_c, const void* __restrict__ src, int d,
+                                                        uint8_t* __restrict__ dst, int64_t plane, void* __restrict__ dh) {
+  __shared__ int counts[4];
+  __shared__ float tops[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x;
+  int count = 0;
+  float top = 0.f;
+  for (int i0 = 0; i0 < t; i0 += 256) {
+    const int i = i0 + tid;
+    const int v = i < t ? target[i] : -1;
+    const bool on = v >= 0 && v < V;
+    count += on;
+    if (t == T && on) top = fmaxf(top, fabsf(scale * (dloss ? dloss[i] : 1.0f)));
+  }
 #pragma unroll
-          for (int s = 0; s < 3; ++s) *(u32x4_t*)(dst + s * plane + (r * d + i) * 2) = o[s];
-        } else {
-          *(Raw8<BF>*)(dst + (r * d + i) * (BF ? 2 : 4)) = v;
-        }
-      } else if (dh) {
-        const float zero[8] = {};
-        st8<BF>(dh, from * d + i, zero);
-      }
+  for (int o = 1; o < 64; o <<= 1) {
+    count += __shfl_xor(count, o);
+    top = fmaxf(top, __shfl_xor(top, o));
+  }
+  if (lane == 0) {
+    counts[wave] = count;
+    tops[wave] = top;
+  }
+  __syncthreads();
+  count = (counts[0] + counts[1]) + (counts[2] + counts[3]);
+  if (t == T) {
+    if (tid == 0) {
+      n[0] = count;
+      ((float*)n)[1] = xent_top(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+    }
+    return;
+  }
+  const int v = target[t];
+  const bool on = v >= 0 && v < V;
+  const int r = on ? count : T - 1 - (t - count);
+  if (tid == 0) {
+    live[r] = t;
+    if (on) {
+      y[r] = v;
+      lse_c[r] = lse[t];
+      g_c[r] = scale * (dloss ? dloss[t] : 1.0f);
     }
   }
+  xent_row<PARTS>(src, t, r, on, d, dst, plane, dh);
 }
 // All of n fp32 values (a multiple of 8) as planes.
 __global__ __launch_bounds__(256) void k_xent_split(const float* __restrict__ src, int64_t n, uint8_t* __restrict__ dst,
@@ -668,10 +726,16 @@ static hipError_t xent_backward(const XentCall& c) {
   int32_t* const n = (int32_t*)(w + p.n);
   int32_t* const live = (int32_t*)(w + p.live);
   hipError_t e;
-  DS4_LAUNCH(k_xent_live, dim3(1), dim3(1024), 0, c.st, c.target, (int)c.T, (int)c.V, c.scale, c.lse_in, c.dloss, n, live,
-             (int32_t*)(w + p.y), (float*)(w + p.lse), (float*)(w + p.g));
-  DS4_LAUNCH((k_xent_rows<PARTS>), dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, c.h, (const int32_t*)n,
-             (const int32_t*)live, c.T, c.d, w + p.hc, c.T * pitch, c.dh);
+  if (c.T <= kXentCounted) {
+    DS4_LAUNCH((k_xent_live_rows<PARTS>), dim3((unsigned)c.T + 1), dim3(256), 0, c.st, c.target, (int)c.T, (int)c.V, c.scale,
+               c.lse_in, c.dloss, n, live, (int32_t*)(w + p.y), (float*)(w + p.lse), (float*)(w + p.g), c.h, c.d, w + p.hc,
+               c.T * pitch, c.dh);
+  } else {
+    DS4_LAUNCH(k_xent_live, dim3(1), dim3(1024), 0, c.st, c.target, (int)c.T, (int)c.V, c.scale, c.lse_in, c.dloss, n, live,
+               (int32_t*)(w + p.y), (float*)(w + p.lse), (float*)(w + p.g));
+    DS4_LAUNCH((k_xent_rows<PARTS>), dim3(xent_row_blocks(c.T)), dim3(256), 0, c.st, c.h, (const int32_t*)n,
+               (const int32_t*)live, c.T, c.d, w + p.hc, c.T * pitch, c.dh);
+  }
   for (int i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.piece, words = std::min(p.piece, c.V - v0);
     const uint8_t* src = (const uint8_t*)c.w + v0 * c.d * kIn;

@@ -514,8 +514,8 @@ int ds4moe_balance_grad(const void *logits, int l_dtype, int64_t T, int32_t n_ex
  * (and its lse) and takes no part in the gradients.  loss and lse fp32 [T].
  * 1 <= T <= 1048576, 1 <= vocab <= 1048576, d a multiple of 256, <= 16384; scale
  * finite.  Products of bf16 are exact and summed in fp32; fp32 operands are
- * multiplied as three bf16 parts each, to fp32 rounding (what lies under
- * 2^-133 is lost).  ws need not be cleared. */
+ * multiplied to fp32 rounding (beyond a few hundred rows as three bf16 parts
+ * each, where what lies under 2^-133 is lost).  ws need not be cleared. */
 size_t ds4moe_xent_workspace_bytes(int dtype, int64_t T, int64_t vocab, int32_t d, int with_grad);
 int ds4moe_xent(const void *h, const void *w, int dtype, int64_t T, int64_t vocab, int32_t d, float scale,
                 const int32_t *target, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
@@ -524,8 +524,8 @@ int ds4moe_xent(const void *h, const void *w, int dtype, int64_t T, int64_t voca
  *   ds_tv = dloss_t scale (e^(z_tv - lse_t) - [v = target_t])
  *   dh = ds w,  dw = ds^T h          [T][d], [vocab][d], in dtype
  * lse as ds4moe_xent wrote it; dloss fp32 [T], or NULL for ones.  dh of a row
- * without a target is zero.  dh or dw may be NULL, not both.  ds is held in
- * bf16 for bf16 operands, in three bf16 parts for fp32; sums are fp32.  One
+ * without a target is zero.  dh or dw may be NULL, not both.  ds is rounded to
+ * bf16 for bf16 operands, to fp32 for fp32; sums are fp32.  One
  * workspace of the size with_grad = 1 gives serves both calls. */
 int ds4moe_xent_grad(const void *h, const void *w, int dtype, int64_t T, int64_t vocab, int32_t d, float scale,
                      const int32_t *target, const float *lse, const float *dloss, void *dh, void *dw, void *ws,
