@@ -23,9 +23,9 @@ constexpr int kBalThreads = 256;
 // Lanes of a row: a quarter of its experts, from 4 to 64.
 static int bal_lanes(int E) { return E <= 16 ? 4 : E <= 64 ? 16 : 64; }
 
-// Tokens of a block.  At least 16, so that the join has few runs to add; no
-// more than 2048 blocks, so that it need not add many.
-static int bal_run(int64_t T) { return (int)std::max<int64_t>(16, (T + 2047) / 2048); }
+// Tokens of a block: 16, and 32 where there are enough blocks, so that the join
+// has few runs to add; no more than 2048 blocks, so that it need not add many.
+static int bal_run(int64_t T) { return (int)std::max<int64_t>(T <= 8192 ? 16 : 32, (T + 2047) / 2048); }
 // Up to this many tokens a sequence is one run and needs no join.
 static bool bal_one(int64_t T) { return T <= 32; }
 
@@ -353,6 +353,8 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* z, int
   const int w0 = (blockIdx.x * W + wave) * run;  // the wave's tokens: run of them, a multiple of its rows
   if (w0 >= T) return;
   int b = off ? ends_before(off, seqs, w0, lane) : 0;
+  // the sequence's first token, and the next one's
+  int first = off && b < seqs ? off[b] : 0, next = !off ? T : b < seqs ? off[b + 1] : INT32_MAX;
   int of = -1;  // the sequence that c holds
   float c[NV][4] = {}, factor = 0.f;
   constexpr int U = NV == 1 ? 2 : 1;
@@ -377,11 +379,11 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* z, int
       const int t = t0 + u * ROWS;
       const bool on = t < end;
       r[u].softmax();
-      bool in = on;
-      if (off) {
-        while (on && b < seqs && t >= off[b + 1]) ++b;
-        in = on && b < seqs && t >= off[b];
+      while (on && t >= next) {
+        first = next;
+        next = ++b < seqs ? off[b + 1] : INT32_MAX;
       }
+      const bool in = on && b < seqs && t >= first;
       if (in && b != of) {
         of = b;
         const int n = tokens[b];
