@@ -18,10 +18,11 @@
 // the launch instead, 46 tensors fit, and finding one among arguments in host
 // memory took 8 us a launch (512 tensors of 32768: 236 us in 25 launches).
 //
-// Memory bounds it.  A head of 268 M bf16 values with 8-bit states (10 bytes a
-// value): step 520 us, 5.2 TB/s; norm 140 us, 3.8 TB/s, since fp64 sums take the
-// vector unit a third of that.  512 tensors of 32768 bf16 values with masters
-// and 8-bit states: 50 and 11 us.  129 of 4096 in fp32: 12 us, three launches.
+// Memory bounds it where there is much of it.  268 M bf16 values with 8-bit
+// states (10 bytes a value): step 515 to 540 us, 5.0 to 5.2 TB/s, norm 115 to
+// 140 us, 3.8 to 4.7 TB/s.  512 tensors of 32768 bf16 values with masters and
+// 8-bit states: norm and step 68 us (in a trace 9 and 4, 43).  129 tensors of
+// 4096 in fp32: 12 us in three launches.
 #include <algorithm>
 #include <cmath>
 

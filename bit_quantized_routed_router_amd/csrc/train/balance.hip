@@ -10,6 +10,11 @@
 // block takes a run of one sequence's tokens, adds up probabilities in
 // registers and counts in LDS, and a second kernel joins the runs of each
 // sequence in order.  Nothing floating is added by atomics, so results repeat.
+//
+// Measured, forward and back: 2048 tokens of 256 experts 17 us in three launches
+// (in a trace 6, join 7, gradient 5); 16381 tokens in 13 sequences, bf16, 30 us
+// (10, 7, 13); 262144 tokens of 64 experts 58 us (19, 6, 34: 3.5 TB/s of logits
+// read, 3.9 of logits read and gradients written; a 4 GB copy has 4.8).
 #include <algorithm>
 
 #include "../ops/rowtile.h"

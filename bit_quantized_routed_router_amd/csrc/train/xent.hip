@@ -13,14 +13,14 @@
 // held over the largest |dloss scale|, by which the products are multiplied in
 // fp32: 1 / rows, which most losses have there, would otherwise be rounded the
 // same way in every value (dh 0.0034 off, against 0.002).  Rounding ds to
-// bfloat16 costs each value at most half a step, 2^-8 of it; dh
-// and dw, themselves bfloat16, end 0.0018 off where the plain fp32 form has 0.0017.
+// bfloat16 costs each value at most half a step, 2^-8 of it; dh and dw, themselves
+// bfloat16, are 0.0018 off where a form with fp32 in between has 0.0017.
 //
 // Measured (rates count the four products, ds's logits formed again): 4096 x
-// 65536 x 4096 in bf16, forward and back, 6.6 ms, 1.33 PFLOP/s; 2047 x 50001 x 2048
+// 65536 x 4096 in bf16, forward and back, 6.6 ms, 1.32 PFLOP/s; 2047 x 50001 x 2048
 // with a tenth of the rows masked 1.41 ms; 16 rows x 65536 x 4096 forward 108 us,
 // 5 TB/s of reading w.  fp32: 512 x 60000 x 1024 1.68 ms, 0.15 PFLOP/s (a library
-// product in fp32 has 0.154); 127 x 1003 x 256 41 us, nine launches of 3 to 10 us.
+// product in fp32 has 0.154); 127 x 1003 x 256 41 us, seven launches of 3 to 10 us.
 #include <algorithm>
 #include <numeric>
 #include <type_traits>

@@ -15,10 +15,10 @@
 // the two halves of the wave hold k's four apart in both operands.
 //
 // Measured, 4096 rows x 65536 words x 4096 in bf16: 1.62 to 1.70 ms for the forward
-// pass's product (1.30 to 1.36 PFLOP/s; a library's product alone 1.47 ms),
-// 0.82 to 0.88 ms for half of it with ds as its epilogue, dw and dh.  The matrix
-// unit is busy 78 % of the cycles at the 1.65 GHz that the card then holds: what
-// is left are waits at the chunk's barrier and the epilogue, one block to a CU.
+// pass's product (1.30 to 1.36 PFLOP/s; a library's product alone 1.48 ms),
+// 0.82 to 0.88 ms for each of its halves' ds, dw and dh.  The matrix unit is busy
+// 78 % of the cycles in the forward product, 74 in ds and dw, 81 in dh, at the
+// 1.65 GHz or so that the card holds under this load.
 //
 // LDS: 16-byte pieces, swizzled on their way in by choosing which piece a
 // lane copies.  By rows piece p of row r lies at p ^ (r / 2 & 7), so that the
@@ -160,9 +160,10 @@ __device__ inline int plane_b(int q) { return (0x021010 >> (4 * (5 - q))) & 3; }
 // written out further: with one wave to a SIMD nothing else hides a wait, so a
 // step's fragments are read while the products of the step before run, across
 // the chunk's border too, and the copies are dealt out between products, which
-// would otherwise wait behind a run of them.  Forward product above: reads before
-// the products 1.74 ms, between them 1.72, B's copies a chunk further ahead 1.61;
-// all copies in a run after the barrier 1.87.
+// would otherwise wait behind a run of them.  (4096 x 65536 x 4096,
+// forward and back: 9.05 ms before; 7.2 with this, no wait at the transposing
+// reads and dh's sum started from its slab; 6.8 with B's copies a chunk further
+// ahead and the masks and exponentials made cheaper.)
 template <class S, bool ACOL, bool BCOL, int PARTS>
 __device__ __attribute__((always_inline)) inline void xgemm(const XSide<S::BM, ACOL, PARTS == 0>& A,
                                                             const XSide<S::BN, BCOL, PARTS == 0>& B, int64_t K, int kc0, int kc1, uint8_t* smem,
