@@ -57,7 +57,8 @@ static bool params_ok(const ds4moe_param* p, int32_t n) {
 static int check_options(const ds4moe_adamw* A) {
   if (!A || !dt_ok(A->grad_dtype) || !dt_ok(A->param_dtype)) return DS4MOE_EINVAL;
   if (A->state != DS4MOE_STATE_F32 && A->state != DS4MOE_STATE_FP8) return DS4MOE_EINVAL;
-  if (!std::isfinite(A->lr) || !std::isfinite(A->eps) || !((float)A->eps > 0.0f)) return DS4MOE_EINVAL;
+  // (below fp32's normal numbers the reciprocal of eps would be infinite, and a value without moments NaN)
+  if (!std::isfinite(A->lr) || !std::isfinite(A->eps) || !((float)A->eps >= 1.17549435e-38f)) return DS4MOE_EINVAL;
   if (!(A->beta1 >= 0.0 && A->beta1 < 1.0) || !(A->beta2 >= 0.0 && A->beta2 < 1.0)) return DS4MOE_EINVAL;
   return al(A->lr_dev, 4) && al(A->step_dev, 4) ? DS4MOE_OK : DS4MOE_EALIGN;
 }

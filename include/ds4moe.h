@@ -560,7 +560,7 @@ typedef struct {
   int32_t param_dtype, grad_dtype; /* DS4MOE_DT_*, of all tensors */
   int32_t state;                   /* DS4MOE_STATE_* */
   int32_t n_params;                /* this and the last three are ds4moe_adamw_table's to fill in */
-  double lr, beta1, beta2, eps;    /* finite; 0 <= beta < 1; eps > 0 as an fp32 */
+  double lr, beta1, beta2, eps;    /* finite; 0 <= beta < 1; eps >= 2^-126 */
   const float *lr_dev;             /* device: the learning rate in lr's place, or NULL */
   const int32_t *step_dev;         /* device: the step in the argument's place, or NULL */
   int64_t run, blocks, kinds;

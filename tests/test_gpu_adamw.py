@@ -242,6 +242,16 @@ def test_norm_of_large_small_and_no_gradients():
         assert not math.isfinite(n) and math.isnan(s)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_adamw_lowest_eps_leaves_values_without_gradients(fp8):
+    """The smallest eps: values without gradient and moments only decay, exactly."""
+    ts = make([517], fp8=fp8, seed=3)
+    for name in ("g", "m", "v"):
+        ts[0][name] = torch.zeros_like(ts[0][name].float()).to(ts[0][name].dtype)
+    o = step(ts, wd=0.5, hyper=dict(HYPER, lr=1.0, eps=2.0 ** -126))[0]
+    assert torch.equal(o["p"], ts[0]["p"] * 0.5) and not o["m"].float().any() and not o["v"].float().any()
+
+
 def test_adamw_past_32_bits():
     """A tensor of more than 2^32 values, bf16 with 8-bit states: its end and a place beyond 2^32 bytes of each."""
     n = (1 << 32) + 70001

@@ -133,6 +133,14 @@ def test_adamw_option_errors():
         assert status("adamw_" + name, None, *args) == D.EINVAL
 
 
+def test_adamw_eps_is_a_normal_number():
+    """The reciprocal of a smaller one is infinite, and zero times it NaN."""
+    for eps in (2.0 ** -127, 1e-39, 1e-45):
+        o = opts(eps=eps)
+        assert table(o=o) == step(o=o) == norm(o=o) == D.EINVAL, eps
+    assert table(o=opts(eps=2.0 ** -126)) == D.OK
+
+
 def test_adamw_table_errors():
     for kw in (dict(param=None), dict(grad=None), dict(m=None), dict(v=None), dict(weight_decay=NAN)):
         assert table(p=param(**kw)) == D.EINVAL, kw
