@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <utility>
 #include <vector>
 
 #include "../trace.h"
@@ -64,29 +63,38 @@ static int check_options(const ds4moe_adamw* A) {
 }
 // types and states that a table was made for
 static int64_t kinds_of(const ds4moe_adamw* A) { return 8 | A->param_dtype | A->grad_dtype << 1 | A->state << 2; }
-// Whether two of the ranges that a step writes overlap.
+// Whether a range that a step writes overlaps another, or a gradient.  Gradients may share memory: they are read only.
 static bool overlap(const ds4moe_adamw* A, const ds4moe_param* p, int32_t n) {
   const bool fp8 = A->state == DS4MOE_STATE_FP8;
-  std::vector<std::pair<uintptr_t, uintptr_t>> r;
-  r.reserve((size_t)n * (fp8 ? 6 : 4));
+  struct Range {
+    uintptr_t at, end;
+    bool written;
+  };
+  std::vector<Range> r;
+  r.reserve((size_t)n * (fp8 ? 7 : 5));
   for (int32_t i = 0; i < n; ++i) {
     const ds4moe_param& q = p[i];
     if (q.n == 0) continue;
-    auto add = [&](const void* at, int64_t bytes) {
-      if (at) r.emplace_back((uintptr_t)at, (uintptr_t)at + (uintptr_t)bytes);
+    auto add = [&](const void* at, int64_t bytes, bool written) {
+      if (at) r.push_back({(uintptr_t)at, (uintptr_t)at + (uintptr_t)bytes, written});
     };
-    add(q.param, q.n * dt_size(A->param_dtype));
-    add(q.master, q.n * 4);
-    add(q.m, q.n * (fp8 ? 1 : 4));
-    add(q.v, q.n * (fp8 ? 1 : 4));
+    add(q.grad, q.n * dt_size(A->grad_dtype), false);
+    add(q.param, q.n * dt_size(A->param_dtype), true);
+    add(q.master, q.n * 4, true);
+    add(q.m, q.n * (fp8 ? 1 : 4), true);
+    add(q.v, q.n * (fp8 ? 1 : 4), true);
     if (fp8) {
-      add(q.m_scale, (q.n + 255) / 256 * 4);
-      add(q.v_scale, (q.n + 255) / 256 * 4);
+      add(q.m_scale, (q.n + 255) / 256 * 4, true);
+      add(q.v_scale, (q.n + 255) / 256 * 4, true);
     }
   }
-  std::sort(r.begin(), r.end());
-  for (size_t i = 1; i < r.size(); ++i)
-    if (r[i].first < r[i - 1].second) return true;
+  std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.at < b.at; });
+  uintptr_t written = 0, read = 0;  // where those before end
+  for (const Range& x : r) {
+    if (x.at < written || (x.written && x.at < read)) return true;
+    uintptr_t& end = x.written ? written : read;
+    end = std::max(end, x.end);
+  }
   return false;
 }
 static int check_params(const ds4moe_adamw* A, const ds4moe_param* p, int32_t n) {

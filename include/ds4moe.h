@@ -567,9 +567,10 @@ typedef struct {
 } ds4moe_adamw;
 
 /* The tensors as a table, laid out once: ds4moe_adamw_table checks them
- * (0 <= n_params <= 2^20; what a step writes must not overlap: DS4MOE_EINVAL) and
- * writes the table to host memory (8-byte aligned, ds4moe_adamw_table_bytes), which the
- * program copies to the device, 16-byte aligned, for the calls below.  It holds
+ * (0 <= n_params <= 2^20; what a step writes must overlap neither itself nor a
+ * gradient: DS4MOE_EINVAL) and writes the table to host memory (8-byte aligned,
+ * ds4moe_adamw_table_bytes), which the program copies to the device, 16-byte
+ * aligned, for the calls below.  It holds
  * the tensors' addresses: where one moves, or types or states change, a new
  * table is made.  lr, betas, eps, lr_dev and step_dev may change between steps. */
 size_t ds4moe_adamw_table_bytes(const ds4moe_param *params, int32_t n_params);

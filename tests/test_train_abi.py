@@ -91,7 +91,7 @@ FAR = 1 << 44  # between stand-in addresses that a step would write
 
 
 def param(i=0, **kw):
-    v = dict(param=A + 6 * i * FAR, grad=A, master=None, m=A + (6 * i + 1) * FAR, v=A + (6 * i + 2) * FAR,
+    v = dict(param=A + 6 * i * FAR, grad=A + (6 * i + 5) * FAR, master=None, m=A + (6 * i + 1) * FAR, v=A + (6 * i + 2) * FAR,
              m_scale=A + (6 * i + 3) * FAR, v_scale=A + (6 * i + 4) * FAR, n=100, weight_decay=0.1)
     v.update(kw)
     return D.ParamDesc(*(v[f[0]] for f in D.ParamDesc._fields_))
@@ -194,10 +194,15 @@ def test_adamw_table_refuses_tensors_that_overlap():
     for kw in (dict(param=a.param + 396), dict(m=a.v), dict(v=a.param - 396), dict(master=a.m)):
         assert both(a, param(1, **kw)) == D.EINVAL, kw
     # side by side, or read alone, is no overlap
-    for kw in (dict(param=a.param + 400), dict(grad=a.param), dict(m_scale=a.m_scale), dict(n=0, param=a.param)):
+    for kw in (dict(param=a.param + 400), dict(grad=a.grad), dict(grad=a.param + 400), dict(m_scale=a.m_scale), dict(n=0, param=a.param)):
         assert both(a, param(1, **kw)) == D.OK, kw
     assert both(a, param(1, m_scale=a.m_scale), opts(state=D.STATE_FP8)) == D.EINVAL
     assert table(p=param(master=A)) == D.EINVAL  # its own
+    # a gradient that a step would change: its own values', another tensor's
+    for kw in (dict(grad=a.param), dict(grad=a.m + 4)):
+        assert table(p=param(0, **kw)) == both(a, param(1, **kw)) == both(param(1, **kw), a) == D.EINVAL, kw
+    # one that begins before it and ends behind it
+    assert both(a, param(1, n=100000, grad=a.param - 400)) == D.EINVAL
 
 
 def test_a_table_is_for_its_types():
