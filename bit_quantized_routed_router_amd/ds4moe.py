@@ -497,7 +497,8 @@ class AdamW:
     weight_decay: one value, or one a tensor.  lr_dev float32 [1] and step_dev
     int32 [1] on the GPU take lr's and the step's place (for captured graphs);
     desc.lr may be set between steps.  The table holds addresses: gradients stay
-    in their tensors from step to step, or set_grads makes a new one."""
+    in their tensors from step to step, or set_grads writes them anew.  A captured
+    step reads the table when it runs: the object has to outlive the graph."""
 
     _TYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
     _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -515,7 +516,7 @@ class AdamW:
         self.desc = AdamWDesc(one("params", params), one("grads", grads), STATE_FP8 if fp8 else STATE_F32, 0, lr, beta1,
                               beta2, eps, lr_at, step_at, 0, 0, 0)
         self.table = None
-        self._make_table()
+        self._make_table(self.tensors)
 
     def _type(self, name, t):
         if t.dtype not in self._TYPES:
@@ -525,7 +526,7 @@ class AdamW:
     def _check(self, args):
         return (_addresses or _load_addresses())("AdamW", self.gpu, tuple(args))
 
-    def _make_table(self):
+    def _make_table(self, tensors):
         import numpy as np
         n, desc = len(self.sizes), self.desc
         fp8 = desc.state == STATE_FP8
@@ -533,7 +534,7 @@ class AdamW:
                                   for f in ParamDesc._fields_])
         blocks = [(k + 255) // 256 for k in self.sizes]
         held = dict(param=desc.param_dtype, grad=desc.grad_dtype)
-        for name, ts in self.tensors.items():
+        for name, ts in tensors.items():
             scale = name.endswith("_scale")
             if ts is None and (name == "master" or scale and not fp8):
                 continue
@@ -550,13 +551,20 @@ class AdamW:
         size = int(lib().ds4moe_adamw_table_bytes(rows.ctypes.data, n))
         table = torch.empty(size, dtype=torch.uint8)
         _check(lib().ds4moe_adamw_table(ctypes.byref(desc), rows.ctypes.data, n, _ptr(table), size), "ds4moe_adamw_table")
-        self.table = table.cuda() if self.gpu >= 0 else None
+        if self.table is not None:  # in place, once no step reads it any more
+            torch.cuda.synchronize(self.gpu)
+            self.table.copy_(table)
+        elif self.gpu >= 0:
+            self.table = table.cuda()
 
     def set_grads(self, grads) -> None:
-        self.tensors["grad"] = grads
-        if grads:
-            self.desc.grad_dtype = self._type("grads", grads[0])
-        self._make_table()
+        """Gradients in other tensors, of the type they had.  The table keeps its
+        place, so a captured step takes them too.  Waits for the GPU."""
+        if grads and self._type("grads", grads[0]) != self.desc.grad_dtype:
+            raise ValueError(f"grads: a tensor of dtype {grads[0].dtype} where the table has another")
+        tensors = dict(self.tensors, grad=grads)
+        self._make_table(tensors)
+        self.tensors = tensors
 
     def workspace_bytes(self) -> int:
         return int(lib().ds4moe_adamw_workspace_bytes(ctypes.byref(self.desc)))

@@ -252,6 +252,42 @@ def test_adamw_lowest_eps_leaves_values_without_gradients(fp8):
     assert torch.equal(o["p"], ts[0]["p"] * 0.5) and not o["m"].float().any() and not o["v"].float().any()
 
 
+def test_adamw_other_gradients_reach_a_captured_step():
+    """set_grads writes the table in its place: a graph captured before takes
+    the new gradients, and a refused list leaves the old ones."""
+    ts = make([300, 4097], seed=8)
+    on = {n: [t[n].cuda() for t in ts] for n in ("p", "g", "m", "v")}
+    start = {n: [x.clone() for x in on[n]] for n in ("p", "m", "v")}
+    opt = D.AdamW(on["p"], on["g"], on["m"], on["v"], lr=HYPER["lr"], beta1=HYPER["b1"], beta2=HYPER["b2"],
+                  eps=HYPER["eps"], weight_decay=0.1)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        D.adamw_step(opt, 7)
+
+    def replayed():
+        for n, xs in start.items():
+            for a, b in zip(on[n], xs):
+                a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        return [dict({n: on[n][i].cpu() for n in ("p", "m", "v")}, g=opt.tensors["grad"][i].cpu()) for i in range(2)]
+
+    at = opt.table.data_ptr()
+    check(ts, replayed())
+    for bad in (on["g"][:1], [g.bfloat16() for g in on["g"]], [on["g"][0], on["g"][1][:-1]], [on["p"][0], on["g"][1]]):
+        with pytest.raises((ValueError, D.Ds4moeError)):
+            opt.set_grads(bad)
+    check(ts, replayed())
+    for t in ts:
+        t["g"] = -2 * t["g"]
+    opt.set_grads([t["g"].cuda() for t in ts])
+    assert opt.table.data_ptr() == at
+    check(ts, replayed())
+    check(ts, replayed())
+
+
 def test_adamw_past_32_bits():
     """A tensor of more than 2^32 values, bf16 with 8-bit states: its end and a place beyond 2^32 bytes of each."""
     n = (1 << 32) + 70001

@@ -283,6 +283,16 @@ def test_optimizer_refuses_what_a_step_cannot_take():
     assert D.AdamW([], [], [], []).desc.blocks == 0
 
 
+def test_refused_gradients_leave_the_optimizer_as_it_was():
+    opt = D.AdamW([], [], [], [])
+    t = [torch.zeros(300)]
+    with pytest.raises(ValueError, match="grad: expected 0 tensors"):
+        opt.set_grads(t)
+    with pytest.raises(ValueError, match="dtype"):
+        opt.set_grads([t[0].bfloat16()])
+    assert opt.tensors["grad"] == [] and opt.desc.grad_dtype == D.DT_F32
+
+
 def test_optimizer_of_another_device_is_refused():
     opt = D.AdamW([], [], [], [])
     opt.gpu = 63
