@@ -506,8 +506,11 @@ class AdamW:
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None, lr=1e-3, beta1=0.9, beta2=0.999,
                  eps=1e-8, weight_decay=0.0, lr_dev=None, step_dev=None):
         fp8 = m_scale is not None or v_scale is not None
+        given = dict(param=params, grad=grads, master=master, m=m, v=v, m_scale=m_scale, v_scale=v_scale)
+        # (lists of its own: what the table points to stays, whatever becomes of the caller's)
+        self.tensors = {name: None if ts is None else list(ts) for name, ts in given.items()}
+        params, grads = self.tensors["param"], self.tensors["grad"]
         self.sizes = [p.numel() for p in params]
-        self.tensors = dict(param=params, grad=grads, master=master, m=m, v=v, m_scale=m_scale, v_scale=v_scale)
         self.devices = (lr_dev, step_dev)
         self.weight_decay = weight_decay
         self.gpu = _current_gpu()
@@ -560,6 +563,7 @@ class AdamW:
     def set_grads(self, grads) -> None:
         """Gradients in other tensors, of the type they had.  The table keeps its
         place, so a captured step takes them too.  Waits for the GPU."""
+        grads = list(grads)
         if grads and self._type("grads", grads[0]) != self.desc.grad_dtype:
             raise ValueError(f"grads: a tensor of dtype {grads[0].dtype} where the table has another")
         tensors = dict(self.tensors, grad=grads)

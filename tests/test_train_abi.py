@@ -293,6 +293,13 @@ def test_refused_gradients_leave_the_optimizer_as_it_was():
     assert opt.tensors["grad"] == [] and opt.desc.grad_dtype == D.DT_F32
 
 
+def test_the_optimizer_keeps_lists_of_its_own():
+    given = []
+    opt = D.AdamW(given, given, given, given)
+    given.append(torch.zeros(3))
+    assert opt.tensors["param"] == opt.tensors["grad"] == opt.tensors["m"] == opt.tensors["v"] == []
+
+
 def test_optimizer_of_another_device_is_refused():
     opt = D.AdamW([], [], [], [])
     opt.gpu = 63
