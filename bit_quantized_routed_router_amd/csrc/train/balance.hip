@@ -357,17 +357,12 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* z, int
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w0 = (blockIdx.x * W + wave) * run;  // the wave's tokens: run of them, a multiple of its rows
   if (w0 >= T) return;
-  int b = off ? ends_before(off, seqs, w0, lane) : 0;
-  // the sequence's first token, and the next one's
-  int first = off && b < seqs ? off[b] : 0, next = !off ? T : b < seqs ? off[b + 1] : INT32_MAX;
-  int of = -1;  // the sequence that c holds
-  float c[NV][4] = {}, factor = 0.f;
   constexpr int U = NV == 1 ? 2 : 1;
   const int end = min(T, w0 + run);
-  for (int t0 = w0 + rg; t0 - rg < end; t0 += U * ROWS) {
-    BalZ<G, NV, BF> r[U];
-    int named[U];
-    float slot[U];
+  BalZ<G, NV, BF> r[U];
+  int named[U];
+  float slot[U];
+  auto load = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = t0 + u * ROWS;
@@ -379,6 +374,14 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* z, int
         if (dslots) slot[u] = dslots[(int64_t)t * k + g];
       }
     }
+  };
+  load(w0 + rg);  // under way while the sequence is searched for
+  int b = off ? ends_before(off, seqs, w0, lane) : 0;
+  // the sequence's first token, and the next one's
+  int first = off && b < seqs ? off[b] : 0, next = !off ? T : b < seqs ? off[b + 1] : INT32_MAX;
+  int of = -1;  // the sequence that c holds
+  float c[NV][4] = {}, factor = 0.f;
+  for (int t0 = w0 + rg;;) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = t0 + u * ROWS;
@@ -468,6 +471,9 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_grad(const void* z, int
         }
       }
     }
+    t0 += U * ROWS;
+    if (t0 - rg >= end) break;
+    load(t0);
   }
 }
 
