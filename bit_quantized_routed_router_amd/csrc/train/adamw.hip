@@ -19,7 +19,7 @@
 // memory took 8 us a launch (512 tensors of 32768: 236 us in 25 launches).
 //
 // Memory bounds it where there is much of it.  268 M bf16 values with 8-bit
-// states (10 bytes a value): step 515 to 540 us, 5.0 to 5.2 TB/s, norm 115 to
+// states (10 bytes a value): step 501 us, 5.4 TB/s, norm 115 to
 // 140 us, 3.8 to 4.7 TB/s.  512 tensors of 32768 bf16 values with masters and
 // 8-bit states: norm and step 68 us (in a trace 9 and 4, 43).  129 tensors of
 // 4096 in fp32: 12 us in three launches.
@@ -32,9 +32,12 @@
 namespace ds4 {
 
 constexpr int kAdamThreads = 256;
-constexpr int64_t kAdamRun = 4096;           // values of a block, or a power of two more:
-constexpr int64_t kAdamBlocks = 1 << 17;     // that many blocks are enough
-constexpr int64_t kAdamParts = 1 << 13;      // and that many sums of squares
+// Values of a block: 4096, or a power of two more where that many blocks are
+// enough.  Norm and step with 4096 / 8192 / 16384: 268 M values with 8-bit states 678 / 653 /
+// 655 us; 61 tensors of 1 to 5 M with fp32 states 26 / 29 / 31 (2048: 30).
+constexpr int64_t kAdamRun = 4096;
+constexpr int64_t kAdamBlocks = 1 << 15;
+constexpr int64_t kAdamParts = 1 << 13;  // sums of squares, at most
 
 // The table: ds4moe_param [n], then for each block (tensor, run).
 struct AdamRun {

@@ -12,7 +12,7 @@ constexpr int kBalMaxSeqs = 16384;         // sequences of a balance call
 constexpr int64_t kXentMaxV = 1 << 20;     // words of a vocabulary
 constexpr int64_t kAdamMaxN = 1ll << 40;   // values of all tensors
 constexpr int kAdamMaxTensors = 1 << 20;
-constexpr int64_t kAdamMaxBlocks = (1 << 17) + 2 * kAdamMaxTensors;
+constexpr int64_t kAdamMaxBlocks = (1 << 15) + 2 * kAdamMaxTensors;
 
 // ---------------------------------------------------------------- balance
 struct BalanceCall {
