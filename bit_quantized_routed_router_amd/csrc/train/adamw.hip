@@ -19,8 +19,8 @@
 // memory took 8 us a launch (512 tensors of 32768: 236 us in 25 launches).
 //
 // Memory bounds it where there is much of it.  268 M bf16 values with 8-bit
-// states (10 bytes a value): step 501 us, 5.4 TB/s, norm 115 to
-// 140 us, 3.8 to 4.7 TB/s.  512 tensors of 32768 bf16 values with masters and
+// states (10 bytes a value): step 500 us, 5.4 TB/s (573 in a trace, its
+// first runs among them), norm 112 to 142 us, 3.8 to 4.8 TB/s.  512 tensors of 32768 bf16 values with masters and
 // 8-bit states: norm and step 68 us (in a trace 9 and 4, 43).  129 tensors of
 // 4096 in fp32: 12 us in three launches.
 #include <algorithm>
