@@ -1,0 +1,48 @@
+"""AdamW at the ends of fp32's range: second moments below its normal numbers."""
+
+import pytest
+import torch
+
+from bit_quantized_routed_router_amd import ds4moe as D
+from tests.ops_ref import U
+
+pytestmark = pytest.mark.gpu
+
+
+def fresh(p, g, fp8, **kw):
+    """An optimizer of one tensor with zero states, and what it updates."""
+    n = p.numel()
+    t = dict(p=p.cuda(), g=g.cuda())
+    kind = torch.uint8 if fp8 else torch.float32
+    t["m"], t["v"] = (torch.zeros(n, dtype=kind, device="cuda") for _ in range(2))
+    if fp8:
+        t["ms"], t["vs"] = (torch.zeros((n + 255) // 256, device="cuda") for _ in range(2))
+    opt = D.AdamW([t["p"]], [t["g"]], [t["m"]], [t["v"]], m_scale=[t["ms"]] if fp8 else None,
+                  v_scale=[t["vs"]] if fp8 else None, **kw)
+    return opt, t
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("eps", [1e-30, 2.0 ** -126])
+def test_adamw_root_of_a_second_moment_below_normal_numbers(eps, fp8):
+    """First steps from gradients whose squares are subnormal or nothing.
+
+    A subnormal v is a whole number of 2^-149, off by at most one of them (half
+    for the square's rounding, times 1 - beta2; half for its own), and by four
+    roundings.  The update lies between those of the v's at both ends; beside it
+    m has two roundings, its factors, the denominator, its reciprocal and the
+    products no more than twenty."""
+    b1, b2 = 0.9, 0.999
+    mags = [10.0 ** (-17 - 0.01 * i) for i in range(700)]  # 1e-17 down to 1e-24
+    g = torch.tensor([m if i % 3 else -m for i, m in enumerate(mags)], dtype=torch.float32)
+    opt, t = fresh(torch.zeros(700), g, fp8, lr=1.0, beta1=b1, beta2=b2, eps=eps)
+    D.adamw_step(opt, 1)
+    got = t["p"].cpu().double()
+    gd = g.double()
+    v = (1 - b2) * gd * gd
+    ev = 4 * U * v + 2.0 ** -149
+    den = lambda x: torch.sqrt(x.clamp(min=0) / (1 - b2)) + eps  # noqa: E731
+    least, most = gd.abs() / den(v + ev) * (1 - 22 * U), gd.abs() / den(v - ev) * (1 + 22 * U)
+    assert (got.sign() == -gd.sign()).all()
+    off = (got.abs() < least) | (got.abs() > most)
+    assert not off.any(), (int(off.sum()), float(gd[off][0]), float(got[off][0]), float(least[off][0]), float(most[off][0]))
