@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import torch
 
@@ -498,7 +499,10 @@ class AdamW:
     int32 [1] on the GPU take lr's and the step's place (for captured graphs);
     desc.lr may be set between steps.  The table holds addresses: gradients stay
     in their tensors from step to step, or set_grads writes them anew.  A captured
-    step reads the table when it runs: the object has to outlive the graph."""
+    step reads the table when it runs: the object has to outlive the graph.
+    Otherwise it may go while steps are pending: where one was called on another
+    stream than the one current at construction, which the table's memory belongs
+    to, its end waits for the GPU."""
 
     _TYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
     _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -514,6 +518,8 @@ class AdamW:
         self.devices = (lr_dev, step_dev)
         self.weight_decay = weight_decay
         self.gpu = _current_gpu()
+        # the stream that the table's memory belongs to, and whether another one may read it
+        self.home, self.away = _stream(None), False
         one = lambda name, ts: self._type(name, ts[0]) if ts else DT_F32  # noqa: E731
         lr_at, step_at = self._check([(lr_dev, 1, DT_F32), (step_dev, 1, _I32)])
         self.desc = AdamWDesc(one("params", params), one("grads", grads), STATE_FP8 if fp8 else STATE_F32, 0, lr, beta1,
@@ -560,6 +566,15 @@ class AdamW:
         elif self.gpu >= 0:
             self.table = table.cuda()
 
+    def __del__(self):
+        if getattr(self, "table", None) is None or not self.away or sys.is_finalizing():
+            return
+        if torch.cuda.is_current_stream_capturing():  # no waiting here: it goes with the next one
+            _left.append(self.table)
+        else:
+            torch.cuda.synchronize(self.gpu)
+            _left.clear()
+
     def set_grads(self, grads) -> None:
         """Gradients in other tensors, of the type they had.  The table keeps its
         place, so a captured step takes them too.  Waits for the GPU."""
@@ -574,18 +589,25 @@ class AdamW:
         return int(lib().ds4moe_adamw_workspace_bytes(ctypes.byref(self.desc)))
 
 
-def _adamw_on_gpu(opt):
+_left = []  # tables whose optimizers went during a capture
+
+
+def _adamw_stream(opt, stream):
+    """The call's stream, noted where the table's memory belongs to another."""
     if opt.gpu != _current_gpu():
         raise ValueError("the optimizer's tensors are not on the current GPU")
-    return opt.desc
+    at = _stream(stream) if stream is not None or opt.gpu < 0 else _raw_stream(opt.gpu)
+    if at != opt.home:
+        opt.away = True
+    return at
 
 
 def adamw_step(opt: AdamW, step, grad_scale=None, stream=None) -> None:
-    _call("ds4moe_adamw_step", stream, _adamw_on_gpu(opt), (opt.table, 1, _BYTES), step, (grad_scale, 1, DT_F32))
+    _call("ds4moe_adamw_step", _adamw_stream(opt, stream), opt.desc, (opt.table, 1, _BYTES), step, (grad_scale, 1, DT_F32))
 
 
 def adamw_norm(opt: AdamW, max_norm, out, ws, ws_bytes, stream=None) -> None:
-    _call("ds4moe_adamw_norm", stream, _adamw_on_gpu(opt), (opt.table, 1, _BYTES), max_norm, (out, 2, DT_F32),
+    _call("ds4moe_adamw_norm", _adamw_stream(opt, stream), opt.desc, (opt.table, 1, _BYTES), max_norm, (out, 2, DT_F32),
           (ws, ws_bytes, _BYTES), ws_bytes)
 
 
