@@ -8,11 +8,13 @@
 // columns (its own index contiguous: 64 rows of the tile's width per chunk,
 // turned by the transposing LDS read).  fp32 operands come as three bfloat16
 // planes whose sum they are, and a chunk is multiplied six times: hi hi, hi
-// mid, mid hi, mid mid, hi lo, lo hi.  What is left out is below 2^-24 of the
-// product, fp32's own rounding.  For few rows, where reading the operands is
-// what takes time, they stay fp32 and go through v_mfma_f32_32x32x2_f32, 32 k a
-// chunk: lane l's four values of a 16-byte piece take four products, in which
-// the two halves of the wave hold k's four apart in both operands.
+// mid, mid hi, mid mid, hi lo, lo hi.  What is left out (mid lo, lo mid, lo lo)
+// is within 2^-24 of the product, fp32's own rounding, and of either sign,
+// since each plane is what is left rounded to nearest.  For few rows, where
+// reading the operands is what takes time, they stay fp32 and go through
+// v_mfma_f32_32x32x2_f32, 32 k a chunk: lane l's four values of a 16-byte piece
+// take four products, in which the two halves of the wave hold k's four apart
+// in both operands.
 //
 // Measured, 4096 rows x 65536 words x 4096 in bf16: 1.62 to 1.70 ms for the forward
 // pass's product (1.30 to 1.36 PFLOP/s; a library's product alone 1.48 ms),
