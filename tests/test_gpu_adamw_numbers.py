@@ -1,10 +1,10 @@
-"""AdamW at the ends of fp32's range: second moments below its normal numbers."""
-
+"""AdamW at the ends of fp32's range: second moments below its normal numbers,
+decays of a few of its steps."""
 import pytest
 import torch
 
 from bit_quantized_routed_router_amd import ds4moe as D
-from tests.ops_ref import U
+from tests.ops_ref import U, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,19 @@ def test_adamw_root_of_a_second_moment_below_normal_numbers(eps, fp8):
     assert (got.sign() == -gd.sign()).all()
     off = (got.abs() < least) | (got.abs() > most)
     assert not off.any(), (int(off.sum()), float(gd[off][0]), float(got[off][0]), float(least[off][0]), float(most[off][0]))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("decay", [4e-8, 1e-7, 3.3e-7, 1e-3])
+def test_adamw_decay_is_rounded_once(decay, fp8):
+    """Without gradients and moments only the decay is left: the value less it,
+    rounded once to fp32 (half a step: U of the value), the decay itself off by
+    two roundings."""
+    p = torch.randn(3001, generator=gen(50))
+    opt, t = fresh(p, torch.zeros(3001), fp8, lr=1e-3, weight_decay=decay * 1e3)
+    D.adamw_step(opt, 1)
+    want = p.double() * (1 - decay)
+    # half a step of the value's power of two
+    half = torch.exp2(torch.floor(torch.log2(want.abs())) - 24)
+    off = (t["p"].cpu().double() - want).abs()
+    assert (off <= half * (1 + 2.0 ** -20) + 2 * U * decay * p.abs()).all(), float((off / half).max())
