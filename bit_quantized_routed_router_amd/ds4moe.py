@@ -509,6 +509,7 @@ class AdamW:
 
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None, lr=1e-3, beta1=0.9, beta2=0.999,
                  eps=1e-8, weight_decay=0.0, lr_dev=None, step_dev=None):
+        import numpy as np
         fp8 = m_scale is not None or v_scale is not None
         given = dict(param=params, grad=grads, master=master, m=m, v=v, m_scale=m_scale, v_scale=v_scale)
         # (lists of its own: what the table points to stays, whatever becomes of the caller's)
@@ -516,7 +517,7 @@ class AdamW:
         params, grads = self.tensors["param"], self.tensors["grad"]
         self.sizes = [p.numel() for p in params]
         self.devices = (lr_dev, step_dev)
-        self.weight_decay = weight_decay
+        self.weight_decay = np.array(weight_decay, dtype=np.float64)  # (a copy, as the lists are)
         self.gpu = _current_gpu()
         # the stream that the table's memory belongs to, and whether another one may read it
         self.home, self.away = _stream(None), False
