@@ -1,5 +1,7 @@
 """AdamW at the ends of fp32's range: second moments below its normal numbers,
 decays of a few of its steps."""
+import math
+
 import pytest
 import torch
 
@@ -62,3 +64,32 @@ def test_adamw_decay_is_rounded_once(decay, fp8):
     half = torch.exp2(torch.floor(torch.log2(want.abs())) - 24)
     off = (t["p"].cpu().double() - want).abs()
     assert (off <= half * (1 + 2.0 ** -20) + 2 * U * decay * p.abs()).all(), float((off / half).max())
+
+
+@pytest.mark.parametrize("g", [torch.float32, torch.bfloat16])
+def test_norm_of_more_blocks_than_partial_sums(g):
+    """20000 tensors, most of them one block, every seventh two to five: more
+    than three times as many blocks as there are partial sums, so a sum takes blocks
+    of several tensors and several of one."""
+    r = gen(51)
+    sizes = [4096 + (i * 977) % 16000 if i % 7 == 3 else (i * 31) % 40 + 1 for i in range(20000)]
+    places, at = [], 0
+    for n in sizes:
+        places.append((at, n))
+        at += (n + 3) // 4 * 4  # aligned to 16 bytes here and there only
+    x = torch.randn(at, generator=r).to(g)
+    used = torch.zeros(at, dtype=torch.bool)
+    for a, n in places:
+        used[a:a + n] = True
+    x[~used] = float("nan")  # between the tensors
+    dev = {n: torch.zeros(at, device="cuda") for n in ("p", "m", "v")}
+    dev["g"] = x.cuda()
+    cut = lambda t: [t[a:a + n] for a, n in places]  # noqa: E731
+    opt = D.AdamW(cut(dev["p"]), cut(dev["g"]), cut(dev["m"]), cut(dev["v"]))
+    assert opt.desc.run == 4096 and opt.desc.blocks > 3 * 8192
+    nb = opt.workspace_bytes()
+    ws, out = torch.full((nb,), 0xFF, dtype=torch.uint8, device="cuda"), torch.zeros(2, device="cuda")
+    D.adamw_norm(opt, 1.0, out, ws, nb)
+    total = math.sqrt(float(x[used].double().square().sum()))
+    norm, scale = out.tolist()
+    assert abs(norm - total) <= 2 * U * total and abs(scale - 1 / total) <= 6 * U * scale
