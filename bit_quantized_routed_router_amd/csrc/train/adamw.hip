@@ -33,8 +33,16 @@ namespace ds4 {
 
 constexpr int kAdamThreads = 256;
 // Values of a block: 4096, or a power of two more where that many blocks are
-// enough.  Norm and step with 4096 / 8192 / 16384: 268 M values with 8-bit states 678 / 653 /
-// 655 us; 61 tensors of 1 to 5 M with fp32 states 26 / 29 / 31 (2048: 30).
+// enough.  Norm and step of one bf16 tensor, us, with runs of 4096 / 8192 /
+// 16384 / 32768 values (* what the rule takes):
+//   8-bit states  201 M    503 /  488*
+//                 268 M    658 /  631*
+//                 537 M   1294 / 1235 / 1254*
+//                1074 M          2457 / 2467 / 2510*
+//   fp32 states   268 M   1227 / 1244*
+//                 537 M   2434 / 2467 / 2497*
+//                1074 M          4893 / 4957 / 5036*
+// 61 tensors of 1 to 5 M with fp32 states 26* / 29 / 31 (2048: 30).
 constexpr int64_t kAdamRun = 4096;
 constexpr int64_t kAdamBlocks = 1 << 15;
 constexpr int64_t kAdamParts = 1 << 13;  // sums of squares, at most
@@ -277,14 +285,10 @@ __global__ __launch_bounds__(kAdamThreads) void k_adamw_squares(const ds4moe_par
   __shared__ double lds[kAdamThreads / 64];
   double sum = 0.0;
   const int64_t last = min(blocks, ((int64_t)blockIdx.x + 1) * group);
-  const AdamRun end_run = map[last - 1];
-  for (int64_t b = (int64_t)blockIdx.x * group; b < last;) {
-    // runs of one tensor are read as one: finding each apart left 3.7 of 5.2 TB/s
+  for (int64_t b = (int64_t)blockIdx.x * group; b < last; ++b) {
     const AdamRun r = map[b];
-    const int64_t take = r.tensor == end_run.tensor ? last - b : 1;
-    b += take;
     const void* grad = params[r.tensor].grad;
-    const int64_t at = r.run * run, end = min(at + take * run, params[r.tensor].n);
+    const int64_t at = r.run * run, end = min(at + run, params[r.tensor].n);
     const bool vec = ((uintptr_t)grad & 15) == 0;
     constexpr int U = 2;
     for (int64_t i0 = at + 8 * threadIdx.x; i0 < end; i0 += U * 8 * kAdamThreads) {
