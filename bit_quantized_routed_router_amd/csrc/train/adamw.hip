@@ -5,11 +5,11 @@
 //   norm = sqrt(sum g^2),  s = min(1, max_norm / norm)
 //
 // States in fp32, or m and sqrt(v) as E4M3 codes with an fp32 scale (largest
-// magnitude / 448) per 256 values.  The root halves the exponents that v
+// magnitude times the fp32 nearest to 1/448) per 256 values.  The root halves the exponents that v
 // spans, and what is positive of it is held as the lowest code at least: a v
 // that became 0 would make its value's next step as large as eps allows.  The
 // scale is no power of two, so that a block that only decays is still followed.
-// m, v, the root and the quotient by the scale are each rounded as IEEE
+// m, v, the root, the scale and the quotient by it are each rounded as IEEE
 // operations are, so that the codes can be computed elsewhere bit for bit.
 //
 // A block takes a run of one tensor, 8 values to a thread: 32 lanes hold a
@@ -19,10 +19,11 @@
 // memory took 8 us a launch (512 tensors of 32768: 236 us in 25 launches).
 //
 // Memory bounds it where there is much of it.  268 M bf16 values with 8-bit
-// states (10 bytes a value): step 500 us, 5.4 TB/s (573 in a trace, its
-// first runs among them), norm 112 to 142 us, 3.8 to 4.8 TB/s.  512 tensors of 32768 bf16 values with masters and
-// 8-bit states: norm and step 68 us (in a trace 9 and 4, 43).  129 tensors of
-// 4096 in fp32: 12 us in three launches.
+// states (10 bytes a value): norm and step 647 us; in a trace the step 504 us,
+// 5.3 TB/s (583 in the mean, first runs among them), the norm 115 to 132 us, 4.1
+// to 4.7 TB/s.  512 tensors of 32768 bf16 values with masters and 8-bit states:
+// norm and step 68 us (in a trace 10 and 5, 43).  129 tensors of 4096 in fp32:
+// 11 to 12 us in three launches.
 #include <algorithm>
 #include <cmath>
 
@@ -134,8 +135,8 @@ __device__ inline void get8_codes(const void* p, int64_t i, int left, bool whole
     v[4 * q + 3] = b.y * scale;
   }
 }
-// The block of 256 that 32 lanes hold.  Its scale: largest / 448; 0 (and codes
-// of 0) where that is below fp32's normal numbers; NaN, and so the whole
+// The block of 256 that 32 lanes hold.  Its scale: largest times 1/448; 0 (and
+// codes of 0) where that is below fp32's normal numbers; NaN, and so the whole
 // block, where a value is not finite.
 template <bool ROOT>
 __device__ inline float put8_codes(void* p, int64_t i, int left, bool whole, const float (&v)[8]) {

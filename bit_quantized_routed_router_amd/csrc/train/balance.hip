@@ -12,8 +12,8 @@
 // sequence in order.  Nothing floating is added by atomics, so results repeat.
 //
 // Measured, forward and back: 2048 tokens of 256 experts 17 us in three launches
-// (in a trace 6, join 6, gradient 6); 16381 tokens in 13 sequences, bf16, 28 us
-// (10, 7, 12); 262144 tokens of 64 experts 57 to 61 us (19, 6, 31: 3.6 TB/s of logits
+// (in a trace 6, join 6, gradient 5); 16381 tokens in 13 sequences, bf16, 28 us
+// (10, 7, 12); 262144 tokens of 64 experts 61 to 62 us (19, 6, 30: 3.6 TB/s of logits
 // read, 4.4 of logits read and gradients written; a 4 GB copy has 4.8).
 #include <algorithm>
 

@@ -17,10 +17,11 @@
 // bfloat16, are 0.0018 off where a form with fp32 in between has 0.0017.
 //
 // Measured (rates count the four products, ds's logits formed again): 4096 x
-// 65536 x 4096 in bf16, forward and back, 6.6 ms, 1.32 PFLOP/s; 2047 x 50001 x 2048
-// with a tenth of the rows masked 1.41 ms; 16 rows x 65536 x 4096 forward 108 us,
-// 5 TB/s of reading w.  fp32: 512 x 60000 x 1024 1.68 ms, 0.15 PFLOP/s (a library
-// product in fp32 has 0.154); 127 x 1003 x 256 41 us, seven launches of 3 to 10 us.
+// 65536 x 4096 in bf16, forward and back, 6.7 to 6.8 ms, 1.3 PFLOP/s; 2047 x 50001 x
+// 2048 with a tenth of the rows masked 1.38 to 1.42 ms; 16 rows x 65536 x 4096
+// forward 107 us, 5 TB/s of reading w.  fp32: 512 x 60000 x 1024 1.51 to 1.61 ms, 0.16
+// PFLOP/s (a library product in fp32 has 0.154); 127 x 1003 x 256 41 us, seven
+// launches of 3 to 10 us.
 #include <algorithm>
 #include <numeric>
 #include <type_traits>
@@ -37,8 +38,14 @@ namespace ds4 {
 // sums).
 constexpr int64_t kXentPiece = 256 << 20;   // bytes that either aims at
 // fp32 operands of up to so many rows go through the fp32 instruction as they
-// are, of more as planes (forward / forward and back: 384 x 30000 x 1024 209 /
-// 825 us, as planes 227 / 841; 512 x 60000 x 1024 570 / 2007, as planes 399 / 1682)
+// are, of more as planes.  The rows at which planes are faster depend on d; this
+// is between them.  Forward / forward and back, us, as they are and as planes:
+//   256 x 30000 x 1024   134 /  544    157 /  537
+//   384 x 30000 x 1024   212 /  811    215 /  768
+//   384 x 65536 x  512   203 /  846    218 /  824
+//   384 x 10000 x 4096   272 / 1051    378 / 1163
+//   512 x 60000 x 1024   578 / 2081    461 / 1609
+//   512 x 10000 x 4096   359 / 1365    428 / 1297
 constexpr int64_t kXentF32Rows = 384;
 constexpr int64_t kXentCounted = 2048;      // rows up to which every block counts the live ones before it
 constexpr int kXentSlabs = 32;              // parts of the sum over words in dh, at most

@@ -515,7 +515,11 @@ int ds4moe_balance_grad(const void *logits, int l_dtype, int64_t T, int32_t n_ex
  * 1 <= T <= 1048576, 1 <= vocab <= 1048576, d a multiple of 256, <= 16384; scale
  * finite.  Products of bf16 are exact and summed in fp32; fp32 operands are
  * multiplied to fp32 rounding (beyond a few hundred rows as three bf16 parts
- * each, where what lies under 2^-133 is lost).  ws need not be cleared. */
+ * each, where what lies under 2^-133 is lost and an infinite value makes NaN
+ * of the logits that it has part in).  ws need not be cleared.  Beside rows of
+ * h's and dh's size it holds ds of a piece of the vocabulary: 256 MB, or 2048
+ * words of T rows where those are more (at T = 1048576 4 GB in bf16, 12 GB in
+ * fp32), and up to 256 MB of w's parts in fp32. */
 size_t ds4moe_xent_workspace_bytes(int dtype, int64_t T, int64_t vocab, int32_t d, int with_grad);
 int ds4moe_xent(const void *h, const void *w, int dtype, int64_t T, int64_t vocab, int32_t d, float scale,
                 const int32_t *target, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
@@ -536,8 +540,8 @@ int ds4moe_xent_grad(const void *h, const void *w, int dtype, int64_t T, int64_t
  *   p  = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
  * in fp32.  States: fp32 m and v; or DS4MOE_STATE_FP8: m and sqrt(v) as OCP
  * E4M3 codes (torch.float8_e4m3fn) to the nearest of scale times code, with an fp32
- * scale, largest magnitude / 448, for each 256 consecutive values (the last
- * block of a tensor may be shorter).  A positive sqrt(v) is held as the lowest
+ * scale for each 256 consecutive values (the last block of a tensor may be
+ * shorter): their largest magnitude times the fp32 nearest to 1/448, one rounding.  A positive sqrt(v) is held as the lowest
  * positive code at least; a scale below 2^-126 is 0, and so is its block;
  * a block with a value that is not finite gets the scale NaN and reads back
  * as NaN.  The update takes the new m and v as they are before they are
