@@ -5,10 +5,11 @@
 //   norm = sqrt(sum g^2),  s = min(1, max_norm / norm)
 //
 // States in fp32, or m and sqrt(v) as E4M3 codes with an fp32 scale (largest
-// magnitude times the fp32 nearest to 1/448) per 256 values.  The root halves the exponents that v
-// spans, and what is positive of it is held as the lowest code at least: a v
-// that became 0 would make its value's next step as large as eps allows.  The
-// scale is no power of two, so that a block that only decays is still followed.
+// magnitude times the fp32 nearest to 1/448) per 256 values.  The root halves
+// the exponents that v spans, and what is positive of it is held as the lowest
+// code at least: a v that became 0 would make its value's next step as large as
+// eps allows.  The scale is no power of two, so that a block that only decays is
+// still followed.
 // m, v, the root, the scale and the quotient by it are each rounded as IEEE
 // operations are, so that the codes can be computed elsewhere bit for bit.
 //

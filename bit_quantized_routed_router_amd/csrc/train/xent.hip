@@ -234,8 +234,9 @@ __global__ __launch_bounds__(1024) void k_xent_live(const int32_t* __restrict__ 
 // (what lies under 2^-133 is lost).  So the second and third are within 2^-8 and
 // 2^-17 of the power of two below x, of either sign: what xgemm leaves out is
 // within 2^-24 of the product and has no bias.  (By truncation it would be up to
-// 2^-21, always towards zero: 0.7 x 2^-24 in the mean.)  Finite values above bfloat16's largest have
-// that as their first part; an infinity or a NaN is its first part.
+// 2^-21, always towards zero: 0.7 x 2^-24 in the mean.)  Finite values above
+// bfloat16's largest have that as their first part; an infinity or a NaN is its
+// first part.
 __device__ inline void xsplit8(const float (&x)[8], u32x4_t (&o)[3]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {

@@ -539,13 +539,13 @@ int ds4moe_xent_grad(const void *h, const void *w, int dtype, int64_t T, int64_t
  *   g' = s g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *   p  = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
  * in fp32.  States: fp32 m and v; or DS4MOE_STATE_FP8: m and sqrt(v) as OCP
- * E4M3 codes (torch.float8_e4m3fn) to the nearest of scale times code, with an fp32
- * scale for each 256 consecutive values (the last block of a tensor may be
- * shorter): their largest magnitude times the fp32 nearest to 1/448, one rounding.  A positive sqrt(v) is held as the lowest
- * positive code at least; a scale below 2^-126 is 0, and so is its block;
- * a block with a value that is not finite gets the scale NaN and reads back
- * as NaN.  The update takes the new m and v as they are before they are
- * rounded to codes.  States start as zeros. */
+ * E4M3 codes (torch.float8_e4m3fn) to the nearest of scale times code, with an
+ * fp32 scale for each 256 consecutive values (the last block of a tensor may be
+ * shorter): their largest magnitude times the fp32 nearest to 1/448, one
+ * rounding.  A positive sqrt(v) is held as the lowest positive code at least; a
+ * scale below 2^-126 is 0, and so is its block; a block with a value that is
+ * not finite gets the scale NaN and reads back as NaN.  The update takes the new
+ * m and v as they are before they are rounded to codes.  States start as zeros. */
 enum { DS4MOE_STATE_F32 = 0, DS4MOE_STATE_FP8 = 1 };
 
 /* One tensor.  Pointers are device pointers aligned as their type; 16 bytes (8
